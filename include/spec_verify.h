@@ -379,6 +379,149 @@ SPEC_API spec_status_t spec_kv_rollback(const int32_t* kv_in, int32_t* kv_out, c
                                         spec_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The paged key-value cache of a verify round: the new tokens' keys and values
+ * are written (spec_kv_append), the new tokens attend over the cache
+ * (spec_kv_attend), the logits made from that go to a verify call, and the
+ * rejected entries are dropped: by a length truncate for a chain
+ * (kv_lens_out, spec_kv_rollback), by moving the accepted path to the front
+ * for a tree (spec_kv_compact). spec_kv_gather reads a cache back.
+ * ("Speculative decoding" (mhtirogla.ai), Implementation notes: paged KV,
+ * tree attention mask.) The pages give no layout; this library's is below.
+ * ------------------------------------------------------------------------- */
+
+/* Cache element type beside SPEC_BF16: 8-bit floats (4 exponent, 3 mantissa
+ * bits, largest value 448, no infinity) with one float32 scale for each
+ * token, head and layer; an element's value is code * scale. */
+#define SPEC_E4M3 2
+/* Most new tokens of one sequence in spec_kv_attend. */
+#define SPEC_KV_MAX_QUERIES 128
+
+/* A paged cache. Entry (layer l, page g, slot i, head h) is head_dim values
+ * at k + l*layer_stride + g*block_stride + i*token_stride + h*head_stride
+ * (elements; v alike, same strides), so pages of [slots, heads, dim] and of
+ * [heads, slots, dim] are both a choice of strides. Position j of sequence b
+ * lies in page block_table[b*max_blocks + j / block_size], slot
+ * j % block_size. Scales (SPEC_E4M3 only) are packed
+ * [layers, num_blocks, kv_heads, block_size].
+ * k, v and every stride must be multiples of 16 bytes, head_dim * element
+ * size too (SPEC_ERR_ALIGNMENT). head_dim up to 256, block_size up to 65536,
+ * max_blocks * block_size up to 2^30 (larger: SPEC_ERR_UNSUPPORTED). */
+typedef struct {
+    uint32_t struct_size; /* sizeof(spec_kv_cache_t), for ABI checks */
+    int32_t batch;        /* 1 <= B <= 65536 */
+    int32_t kv_heads;     /* 1 .. 65535 */
+    int32_t head_dim;
+    int32_t block_size;   /* positions of a page */
+    int32_t num_blocks;   /* pages in the pool */
+    int32_t max_blocks;   /* entries of a block_table row */
+    int32_t layers;       /* >= 1 */
+    int32_t dtype;        /* SPEC_BF16 or SPEC_E4M3 */
+    void* k;              /* device */
+    void* v;              /* device */
+    int64_t layer_stride, block_stride, token_stride, head_stride; /* elements */
+    float* k_scale;       /* device or NULL (SPEC_BF16) */
+    float* v_scale;       /* device or NULL (SPEC_BF16) */
+    const int32_t* block_table; /* device [batch, max_blocks]; a sequence's entries
+                                   past its last page are not read */
+} spec_kv_cache_t;
+
+/* Write new tokens into one layer of the cache. Sequence b's new tokens are
+ * rows row_off[b] .. row_off[b+1) of k_new / v_new (T_b of them; row_off NULL:
+ * t_max each, rows = batch * t_max), entry (r, h) at new + r*new_token_stride
+ * + h*head_dim elements; they become positions kv_lens[b] - T_b .. kv_lens[b])
+ * of the cache: kv_lens is the length with them, as the verify calls'
+ * kv_lens_in is. With row_off = a verify call's target_row_off these are the
+ * gamma_b + 1 tokens of its pass.
+ * SPEC_BF16 caches take the values (float32 rounded to nearest even).
+ * SPEC_E4M3: with a the largest finite |x_d| of the entry, scale = the
+ * smallest power of two, not below 2^-126, with a / scale <= 448 (1 if
+ * a = 0); code_d = x_d / scale (an exact division) rounded to nearest even; a
+ * NaN or an infinity becomes NaN.
+ * new_dtype: SPEC_BF16 or SPEC_F32; k_new, v_new and their row stride
+ * multiples of 16 bytes. seq_status (may be NULL): LAYOUT (offsets outside
+ * [0, rows] or falling, or a page of the new positions outside the pool: its
+ * entries are not written), KV (kv_lens[b] < T_b or past the table).
+ * A sequence with another error has nothing written. Two sequences that share
+ * the page of a new position race on it. */
+SPEC_API spec_status_t spec_kv_append(const spec_kv_cache_t* cache, int32_t layer, const void* k_new,
+                                      const void* v_new, int32_t new_dtype, int64_t new_token_stride, int64_t rows,
+                                      const int64_t* row_off, int32_t t_max, const int32_t* kv_lens,
+                                      int32_t* seq_status, spec_stream_t stream);
+
+/* Read one layer back: k_out / v_out [rows, kv_heads, head_dim] (packed,
+ * SPEC_BF16 or SPEC_F32, 16-byte aligned), row out_off[b] + j = position j of
+ * sequence b, 0 <= j < kv_lens[b], as its value (code * scale in float32,
+ * rounded to nearest even). seq_status (may be NULL): LAYOUT (offsets outside
+ * [0, rows], out_off[b+1] - out_off[b] != kv_lens[b], or a page outside the
+ * pool: its rows are zeros), KV (kv_lens[b] < 0 or past the table). Rows of a
+ * sequence with another error are not written, nor are rows no sequence owns.
+ * out_off must not fall. */
+SPEC_API spec_status_t spec_kv_gather(const spec_kv_cache_t* cache, int32_t layer, const int32_t* kv_lens,
+                                      const int64_t* out_off, int64_t rows, void* k_out, void* v_out,
+                                      int32_t out_dtype, int32_t* seq_status, spec_stream_t stream);
+
+/* After spec_tree_verify: keep the accepted path's entries, in every layer.
+ * The tree of sequence b (N_b = node_off[b+1] - node_off[b] nodes, node 0 the
+ * root) holds the last N_b positions of kv_lens_in[b]; for i < accepted[b] the
+ * entry of node path[node_off[b] + i] moves to the position of node 1 + i
+ * (codes and scales as they are), and kv_lens_out[b] = kv_lens_in[b] -
+ * (N_b - 1 - accepted[b]); out_num_blocks (may be NULL) = the pages that
+ * covers. accepted and path are spec_tree_verify's out_accepted and out_path.
+ * seq_status (may be NULL): LAYOUT (offsets, N_b < 1, accepted outside
+ * [0, N_b), a path that does not rise or leaves the tree, a page outside the
+ * pool), KV (kv_lens_in[b] < N_b or past the table); such a sequence moves
+ * nothing and keeps its length. kv_lens_out may alias kv_lens_in. */
+SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64_t* node_off, int64_t nodes,
+                                       const int32_t* path, const int32_t* accepted, const int32_t* kv_lens_in,
+                                       int32_t* kv_lens_out, int32_t* out_num_blocks, int32_t* seq_status,
+                                       spec_stream_t stream);
+
+/* Attention of each sequence's new tokens over one layer of the cache. The
+ * T_b new tokens (rows row_off[b] .. row_off[b+1) of q; 0 <= T_b <= t_max) are
+ * the last T_b of the kv_lens[b] positions and are in the cache already. With
+ * s_j = scale * <q, k_j>, query head h reading key-value head
+ * h / (q_heads / kv_heads):
+ *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  lse = m + ln(sum),
+ * m = max s_j, over the positions the token sees: chain (parent == NULL), its
+ * own and every earlier one; tree, every position before the new tokens, and
+ * the new tokens that are itself or an ancestor by parent (local node
+ * indices, -1 for node 0, as spec_tree_verify's). What a token does not see
+ * has no effect on it, a NaN or an infinity there included. A token whose
+ * every s_j is -inf gets zeros and lse -inf. Statistics and sums are float32;
+ * products run on the tensor cores with a query and a weight each rounded to
+ * 16 bits or held as a sum of parts no less exact.
+ * seq_status (may be NULL): LAYOUT (offsets outside [0, rows] or falling,
+ * T_b > t_max, a bad parent, or a page outside the pool, whose positions are
+ * then left out), KV (kv_lens[b] < T_b or past the table), TIMEOUT (a bounded
+ * wait gave up; outputs unspecified). Rows of a sequence with bad offsets are
+ * not written; with another LAYOUT or KV error than a bad page, they are
+ * zeros with lse -inf. */
+typedef struct {
+    uint32_t struct_size; /* sizeof(spec_kv_attend_args_t), for ABI checks */
+    int32_t layer;
+    int32_t q_heads;      /* a multiple of kv_heads */
+    int32_t t_max;        /* 1 .. SPEC_KV_MAX_QUERIES (larger: SPEC_ERR_UNSUPPORTED) */
+    int64_t rows;         /* rows of q; <= batch * t_max */
+    const int64_t* row_off; /* device [B+1], or NULL: T_b = t_max, rows = batch * t_max */
+    const int32_t* kv_lens; /* device [B], the new tokens included */
+    const int32_t* parent;  /* device [rows] or NULL: chain */
+    const void* q;          /* device bf16, row r head h at q + r*q_token_stride + h*head_dim */
+    int64_t q_token_stride; /* elements, a multiple of 16 bytes */
+    float scale;            /* > 0 and finite */
+    void* out;              /* device bf16 [rows, q_heads, head_dim], packed, 16-byte aligned */
+    float* lse;             /* device [rows, q_heads] or NULL */
+    int32_t* seq_status;    /* device [B] or NULL */
+    void* workspace;        /* as the verify calls': 256-byte aligned, spec_workspace_init once */
+    size_t workspace_bytes; /* >= spec_kv_attend_workspace_size */
+} spec_kv_attend_args_t;
+
+/* Workspace bytes of a call (host arithmetic on the host fields; 0 if they
+ * are out of range). It does not grow with the cache's length. */
+SPEC_API size_t spec_kv_attend_workspace_size(const spec_kv_cache_t* cache, const spec_kv_attend_args_t* args);
+SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* cache, const spec_kv_attend_args_t* args,
+                                      spec_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Test hooks. Same conventions; they expose intermediate values of the last
  * spec_verify_sample / spec_verify_greedy call made with the same arguments
  * and workspace (stream-ordered after it).

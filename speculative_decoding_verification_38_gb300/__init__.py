@@ -9,7 +9,10 @@ Low-level entry points (same names as the C ABI):
     spec_verify_workspace_size, spec_workspace_init, spec_verify_sample,
     spec_verify_greedy, spec_kv_rollback, spec_status_string, spec_abi_version,
     spec_debug_philox, spec_debug_row_stats, spec_debug_probs
-Convenience: VerifyArgs (builds the argument struct from tensors), Workspace.
+    spec_kv_append, spec_kv_gather, spec_kv_compact, spec_kv_attend,
+    spec_kv_attend_workspace_size (the paged key-value cache)
+Convenience: VerifyArgs, AttendArgs, KVCache (build the argument structs from
+tensors), Workspace.
 """
 from __future__ import annotations
 
@@ -26,12 +29,13 @@ SPEC_ERR_ALIGNMENT = 2
 SPEC_ERR_WORKSPACE = 3
 SPEC_ERR_CUDA = 4
 SPEC_ERR_UNSUPPORTED = 5
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_E4M3 = 0, 1, 2
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20  # scratch of spec_verify_sample_static, per device
 SPEC_ABI_VERSION = 5
 SEQ_OK, SEQ_BAD_TOKEN, SEQ_BAD_KV, SEQ_BAD_ROW, SEQ_BAD_LAYOUT, SEQ_BAD_TEMP = 0, 1, 2, 3, 4, 5
 SEQ_TIMEOUT, SEQ_UNSUPPORTED = 6, 7
 SPEC_TREE_MAX_CANDIDATES = 64
+SPEC_KV_MAX_QUERIES = 128
 
 
 class SpecError(RuntimeError):
@@ -110,6 +114,54 @@ class SpecTreeArgs(ctypes.Structure):
     ]
 
 
+class SpecKvCache(ctypes.Structure):
+    """Mirror of spec_kv_cache_t (include/spec_verify.h)."""
+
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("batch", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("layers", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("layer_stride", ctypes.c_int64),
+        ("block_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+    ]
+
+
+class SpecKvAttendArgs(ctypes.Structure):
+    """Mirror of spec_kv_attend_args_t (include/spec_verify.h)."""
+
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("layer", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("t_max", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("row_off", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("parent", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("seq_status", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -168,6 +220,18 @@ def lib():
             L.spec_debug_set_path.argtypes = [ctypes.c_int32]
             L.spec_debug_wait_probe.restype = ctypes.c_int
             L.spec_debug_wait_probe.argtypes = [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]
+            C = ctypes.POINTER(SpecKvCache)
+            T = ctypes.POINTER(SpecKvAttendArgs)
+            L.spec_kv_append.restype = ctypes.c_int
+            L.spec_kv_append.argtypes = [C, i32, vp, vp, i32, i64, i64, vp, i32, vp, vp, vp]
+            L.spec_kv_gather.restype = ctypes.c_int
+            L.spec_kv_gather.argtypes = [C, i32, vp, vp, i64, vp, vp, i32, vp, vp]
+            L.spec_kv_compact.restype = ctypes.c_int
+            L.spec_kv_compact.argtypes = [C, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+            L.spec_kv_attend_workspace_size.restype = sz
+            L.spec_kv_attend_workspace_size.argtypes = [C, T]
+            L.spec_kv_attend.restype = ctypes.c_int
+            L.spec_kv_attend.argtypes = [C, T, vp]
             if L.spec_abi_version() != SPEC_ABI_VERSION:
                 raise ImportError("libspecverify.so ABI version mismatch")
             _lib = L
@@ -317,6 +381,126 @@ class Workspace:
         return cls(int(n * slack), device=device, stream=stream)
 
 
+    @classmethod
+    def for_attend(cls, args: "AttendArgs", device=None, stream=None):
+        n = spec_kv_attend_workspace_size(args)
+        if n == 0:
+            raise SpecError(SPEC_ERR_INVALID_ARG, "spec_kv_attend_workspace_size")
+        return cls(n, device=device or args.tensors["q"].device, stream=stream)
+
+
+def _check_typed(t, name, dtype, numel=None, optional=True):
+    """A contiguous CUDA tensor of that type (and size), or None."""
+    if t is None:
+        if not optional:
+            raise ValueError(f"{name} is required")
+        return
+    _check_dev(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+
+
+class KVCache:
+    """spec_kv_cache_t over CUDA tensors, which it keeps alive.
+
+    k and v: [layers, num_blocks, block_size, kv_heads, head_dim] (or without
+    the first axis: one layer), bfloat16 or float8_e4m3fn, equal strides, the
+    last axis packed; pages held as [heads, slots, dim] are passed transposed.
+    block_table: int32 [batch, max_blocks]. k_scale, v_scale (float8 only):
+    float32 [layers, num_blocks, kv_heads, block_size], packed.
+    """
+
+    def __init__(self, k, v, block_table, k_scale=None, v_scale=None):
+        import torch
+
+        if k.dim() == 4:
+            k, v = k.unsqueeze(0), v.unsqueeze(0)
+        if k.dim() != 5 or v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must be [layers, num_blocks, block_size, kv_heads, head_dim], of equal strides")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise TypeError(f"cache must be bfloat16 or float8_e4m3fn, got {k.dtype}, {v.dtype}")
+        if not (k.is_cuda and v.is_cuda):
+            raise ValueError("the cache must be in CUDA tensors")
+        if k.stride(4) != 1:
+            raise ValueError("the cache's last axis must be packed")
+        layers, blocks, bs, heads, dim = k.shape
+        quantised = k.dtype != torch.bfloat16
+        if (k_scale is not None) != quantised or (v_scale is not None) != quantised:
+            raise ValueError("a float8 cache needs k_scale and v_scale, a bfloat16 one has none")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _check_typed(t, name, torch.float32, layers * blocks * heads * bs)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [batch, max_blocks]")
+        _check_typed(block_table, "block_table", torch.int32)
+        self.tensors = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
+        c = SpecKvCache()
+        c.struct_size = ctypes.sizeof(SpecKvCache)
+        c.batch, c.max_blocks = block_table.shape
+        c.layers, c.num_blocks, c.block_size, c.kv_heads, c.head_dim = layers, blocks, bs, heads, dim
+        c.dtype = SPEC_E4M3 if quantised else SPEC_BF16
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        # an axis of one element is never stepped along: its stride says nothing
+        c.layer_stride, c.block_stride, c.token_stride, c.head_stride = (
+            k.stride(i) if k.shape[i] > 1 else 0 for i in range(4))
+        c.k_scale, c.v_scale = _ptr(k_scale), _ptr(v_scale)
+        c.block_table = block_table.data_ptr()
+        self.struct = c
+
+
+class AttendArgs:
+    """spec_kv_attend_args_t over CUDA tensors, which it keeps alive.
+
+    q: bfloat16 [rows, q_heads, head_dim], a row's heads packed (rows may lie
+    apart, as a slice of a fused projection); out: bfloat16, packed; row_off
+    int64 [B+1], or None for t_max rows each; kv_lens int32 [B], the new
+    tokens included; parent int32 [rows] for token trees, or None for chains;
+    lse float32 [rows, q_heads] or None.
+    """
+
+    def __init__(self, *, cache, q, out, kv_lens, row_off=None, t_max, scale, parent=None, lse=None, layer=0,
+                 seq_status=None, workspace=None):
+        import torch
+
+        c = cache.struct
+        if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_cuda:
+            raise ValueError("q must be a bfloat16 CUDA tensor [rows, q_heads, head_dim]")
+        rows, heads, dim = q.shape
+        if dim != c.head_dim or q.stride(2) != 1 or (heads > 1 and q.stride(1) != dim):
+            raise ValueError("q must have the cache's head_dim and packed heads")
+        _check_typed(out, "out", torch.bfloat16, rows * heads * dim, optional=False)
+        _check_typed(kv_lens, "kv_lens", torch.int32, c.batch, optional=False)
+        _check_typed(row_off, "row_off", torch.int64, c.batch + 1)
+        _check_typed(parent, "parent", torch.int32, rows)
+        _check_typed(lse, "lse", torch.float32, rows * heads)
+        _check_typed(seq_status, "seq_status", torch.int32, c.batch)
+        self.cache = cache
+        self.tensors = dict(q=q, out=out, kv_lens=kv_lens, row_off=row_off, parent=parent, lse=lse,
+                            seq_status=seq_status)
+        a = SpecKvAttendArgs()
+        a.struct_size = ctypes.sizeof(SpecKvAttendArgs)
+        a.layer, a.q_heads, a.t_max, a.rows = int(layer), heads, int(t_max), rows
+        a.row_off, a.kv_lens, a.parent = _ptr(row_off), kv_lens.data_ptr(), _ptr(parent)
+        a.q = q.data_ptr()
+        a.q_token_stride = q.stride(0) if rows > 1 else 0
+        a.scale = float(scale)
+        a.out, a.lse, a.seq_status = out.data_ptr(), _ptr(lse), _ptr(seq_status)
+        self.struct = a
+        self.workspace = None
+        if workspace is not None:
+            self.set_workspace(workspace)
+
+    def set_workspace(self, ws):
+        buf = ws.buffer if isinstance(ws, Workspace) else ws
+        self.workspace = ws
+        self.struct.workspace = buf.data_ptr()
+        self.struct.workspace_bytes = buf.numel() * buf.element_size()
+
+    def set_layer(self, layer: int):
+        self.struct.layer = int(layer)
+
+
 def check(status: int, what: str = "spec call"):
     if status != SPEC_OK:
         raise SpecError(status, what)
@@ -418,6 +602,74 @@ def spec_kv_rollback(kv_in, kv_out, accepted, gammas, gamma_max, block_size=0, o
     return lib().spec_kv_rollback(_ptr(kv_in), _ptr(kv_out), _ptr(accepted), _ptr(gammas), int(gamma_max),
                                   int(kv_in.shape[0]), int(block_size), _ptr(out_num_blocks), _ptr(seq_status),
                                   _stream(stream))
+
+
+def spec_kv_append(cache: KVCache, k_new, v_new, kv_lens, row_off=None, t_max=None, layer=0, seq_status=None,
+                   stream=None) -> int:
+    """New tokens' keys and values [rows, kv_heads, head_dim] (bfloat16 or
+    float32, a row's heads packed, equal row strides) into one layer: the last
+    positions of each sequence's kv_lens. row_off int64 [B+1], or None for
+    t_max rows each (then t_max is required)."""
+    import torch
+
+    c = cache.struct
+    rows = k_new.shape[0]
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if not t.is_cuda or tuple(t.shape) != (rows, c.kv_heads, c.head_dim):
+            raise ValueError(f"{name} must be a CUDA tensor [rows, {c.kv_heads}, {c.head_dim}]")
+        if t.stride(2) != 1 or (c.kv_heads > 1 and t.stride(1) != c.head_dim):
+            raise ValueError(f"{name} must have packed heads")
+    if v_new.dtype != k_new.dtype or (rows > 1 and v_new.stride(0) != k_new.stride(0)):
+        raise ValueError("k_new and v_new must have one type and row stride")
+    _check_typed(kv_lens, "kv_lens", torch.int32, c.batch, optional=False)
+    _check_typed(row_off, "row_off", torch.int64, c.batch + 1)
+    _check_typed(seq_status, "seq_status", torch.int32, c.batch)
+    return lib().spec_kv_append(ctypes.byref(c), int(layer), k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new),
+                                k_new.stride(0) if rows > 1 else 0, rows, _ptr(row_off), int(t_max or 0),
+                                kv_lens.data_ptr(), _ptr(seq_status), _stream(stream))
+
+
+def spec_kv_gather(cache: KVCache, kv_lens, out_off, k_out, v_out, layer=0, seq_status=None, stream=None) -> int:
+    """One layer of every sequence's cache as rows [rows, kv_heads, head_dim]
+    (bfloat16 or float32): row out_off[b] + j is position j of sequence b."""
+    import torch
+
+    c = cache.struct
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _check_typed(t, name, k_out.dtype, k_out.shape[0] * c.kv_heads * c.head_dim, optional=False)
+    _check_typed(kv_lens, "kv_lens", torch.int32, c.batch, optional=False)
+    _check_typed(out_off, "out_off", torch.int64, c.batch + 1, optional=False)
+    _check_typed(seq_status, "seq_status", torch.int32, c.batch)
+    return lib().spec_kv_gather(ctypes.byref(c), int(layer), kv_lens.data_ptr(), out_off.data_ptr(), k_out.shape[0],
+                                k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), _ptr(seq_status),
+                                _stream(stream))
+
+
+def spec_kv_compact(cache: KVCache, node_off, path, accepted, kv_lens_in, kv_lens_out, out_num_blocks=None,
+                    seq_status=None, stream=None) -> int:
+    """Keep the accepted path's entries of each sequence's tree, in every
+    layer (path and accepted: spec_tree_verify's out_path and out_accepted)."""
+    import torch
+
+    c = cache.struct
+    _check_typed(node_off, "node_off", torch.int64, c.batch + 1, optional=False)
+    _check_typed(path, "path", torch.int32, optional=False)
+    for name, t in (("accepted", accepted), ("kv_lens_in", kv_lens_in), ("kv_lens_out", kv_lens_out)):
+        _check_typed(t, name, torch.int32, c.batch, optional=False)
+    for name, t in (("out_num_blocks", out_num_blocks), ("seq_status", seq_status)):
+        _check_typed(t, name, torch.int32, c.batch)
+    return lib().spec_kv_compact(ctypes.byref(c), node_off.data_ptr(), path.numel(), path.data_ptr(),
+                                 accepted.data_ptr(), kv_lens_in.data_ptr(), kv_lens_out.data_ptr(),
+                                 _ptr(out_num_blocks), _ptr(seq_status), _stream(stream))
+
+
+def spec_kv_attend_workspace_size(args: AttendArgs) -> int:
+    return int(lib().spec_kv_attend_workspace_size(ctypes.byref(args.cache.struct), ctypes.byref(args.struct)))
+
+
+def spec_kv_attend(args: AttendArgs, stream=None) -> int:
+    """Attention of every sequence's new tokens over its cache (see AttendArgs)."""
+    return lib().spec_kv_attend(ctypes.byref(args.cache.struct), ctypes.byref(args.struct), _stream(stream))
 
 
 def spec_debug_philox(seed, rnd, seq_offset, batch, npos, out, stream=None) -> int:

@@ -1,0 +1,487 @@
+// kv.cu -- the paged key-value cache: writing new tokens (with quantisation),
+// reading back, keeping a tree's accepted path, and the plain attention that
+// takes the shapes attend.cu does not.
+#include "kv.cuh"
+
+namespace specv {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Status of each sequence, one warp each: the offsets and length by `st`,
+// then every page of positions [p0, L).
+__device__ __forceinline__ int32_t check_pages(const KvView& c, int32_t b, int64_t p0, int64_t L) {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    if (L > p0)
+        for (int64_t j = p0 / c.bs + lane; j <= (L - 1) / c.bs; j += 32) {
+            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+            bad |= pg < 0 || pg >= c.num_blocks;
+        }
+    return __any_sync(0xFFFFFFFFu, bad) ? kKvBadLayout : kKvOk;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// The smallest power of two s >= 2^-126 with a / s <= 448 = 1.75 * 2^8, as
+// exponents: s = 2^e (a finite and >= 0; a = 0 gives 2^0).
+__device__ __forceinline__ int32_t scale_exponent(float a) {
+    const uint32_t w = __float_as_uint(a);
+    if (w == 0) return 0;
+    const int32_t e = (int32_t)(w >> 23) - 127 - 8 + ((w & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return max(e, -126);
+}
+__device__ __forceinline__ float pow2(int32_t e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
+
+// The eight values of lane `i` of an entry, as floats.
+template <int DT>
+__device__ __forceinline__ void load8(const unsigned char* row, int i, float (&x)[8]) {
+    if (DT == kKvBf16) {
+        const uint4 w = *(const uint4*)(row + 16 * i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16_lo(u[j]);
+            x[2 * j + 1] = bf16_hi(u[j]);
+        }
+    } else {
+        const float4 a = *(const float4*)(row + 32 * i), b = *(const float4*)(row + 32 * i + 16);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+
+// One entry (token, head) of K or V, `lanes` (a power of two, 8 values each)
+// threads together: scale from the largest finite value, codes, stores.
+template <int DT, bool Q8>
+__device__ __forceinline__ void write_entry(const float (&x)[8], bool live, unsigned char* dst, float* scale, int i,
+                                            int lanes) {
+    if (!Q8) {
+        if (live) {
+            uint4 w;
+            w.x = pack_bf16(x[0], x[1]);
+            w.y = pack_bf16(x[2], x[3]);
+            w.z = pack_bf16(x[4], x[5]);
+            w.w = pack_bf16(x[6], x[7]);
+            *(uint4*)(dst + 16 * i) = w;
+        }
+        return;
+    }
+    float a = 0.f;
+    if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float m = fabsf(x[j]);
+            a = m < __uint_as_float(0x7F800000u) ? fmaxf(a, m) : a;  // a NaN or an infinity is left out
+        }
+    }
+    for (int o = lanes >> 1; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    if (!live) return;
+    const int32_t e = scale_exponent(a);
+    const float f = pow2(-e);  // e lies in [-126, 120]: x * 2^-e is exact down to what e4m3 rounds to zero
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const bool fin = fabsf(x[j]) < __uint_as_float(0x7F800000u);
+        y[j] = fin ? x[j] * f : __uint_as_float(0x7FC00000u);
+    }
+    uint2 w;
+    w.x = pack_e4m3(y[0], y[1]) | (pack_e4m3(y[2], y[3]) << 16);
+    w.y = pack_e4m3(y[4], y[5]) | (pack_e4m3(y[6], y[7]) << 16);
+    *(uint2*)(dst + 8 * i) = w;
+    if (i == 0) *scale = pow2(e);
+}
+
+// New tokens into the cache. A flat range of entries (row, head), `lanes`
+// threads each; a CTA finds its first row's sequence by a warp search over
+// the offsets and steps on from there. The grid's last CTAs write the
+// statuses, one warp for each sequence.
+template <int DT, bool Q8>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const KvNew n, int lanes, int64_t ctas) {
+    __shared__ int32_t b_first;
+    const int warp = threadIdx.x >> 5;
+    if ((int64_t)blockIdx.x >= ctas) {
+        const int64_t b = ((int64_t)blockIdx.x - ctas) * (kThreads / 32) + warp;
+        if (b >= c.B) return;
+        const KvSeq s = kv_seq((int32_t)b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
+        int32_t st = s.st;
+        if (st == kKvOk) st = check_pages(c, (int32_t)b, s.L - s.T, s.L);
+        if ((threadIdx.x & 31) == 0) n.seq_status[b] = st;
+        return;
+    }
+    const int per = kThreads / lanes;  // entries of a CTA
+    const int64_t first = (int64_t)blockIdx.x * per;
+    if (n.row_off) {
+        if (warp == 0) {
+            const int32_t b = kv_find(n.row_off, c.B, first / c.H);
+            if (threadIdx.x == 0) b_first = b;
+        }
+        __syncthreads();
+    }
+    const int64_t e = first + threadIdx.x / lanes;
+    const int i = threadIdx.x % lanes;
+    const int64_t r = e / c.H;
+    const int32_t h = (int32_t)(e - r * c.H);
+    bool live = r < n.rows && i * 8 < c.D;
+    int64_t at = 0, sc = 0;
+    if (r < n.rows) {
+        int32_t b;
+        if (n.row_off) {
+            b = b_first;
+            while (b < c.B && n.row_off[b + 1] <= r) ++b;
+        } else {
+            b = (int32_t)(r / n.t_max);
+        }
+        bool ok = false;
+        if (b < c.B) {
+            const KvSeq s = kv_seq(b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
+            if (s.st == kKvOk && r >= s.lo) {
+                const int32_t pos = s.L - s.T + (int32_t)(r - s.lo);
+                const int32_t pg = c.table[(int64_t)b * c.max_blocks + pos / c.bs];
+                const int32_t sl = pos % c.bs;
+                ok = pg >= 0 && pg < c.num_blocks;
+                at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
+                sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+            }
+        }
+        live = live && ok;
+    }
+    float xk[8], xv[8];
+    if (live) {
+        const int64_t src = r * n.row_bytes + (int64_t)h * c.D * (DT == kKvBf16 ? 2 : 4);
+        load8<DT>(n.k + src, i, xk);
+        load8<DT>(n.v + src, i, xv);
+    }
+    write_entry<DT, Q8>(xk, live, c.k + at, Q8 ? c.ks + sc : nullptr, i, lanes);
+    write_entry<DT, Q8>(xv, live, c.v + at, Q8 ? c.vs + sc : nullptr, i, lanes);
+}
+
+// The cache back as rows: value = code * scale.
+template <bool Q8, int ODT>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, const KvRead g, int lanes, int64_t ctas) {
+    __shared__ int32_t b_first;
+    const int warp = threadIdx.x >> 5;
+    if ((int64_t)blockIdx.x >= ctas) {
+        const int64_t b = ((int64_t)blockIdx.x - ctas) * (kThreads / 32) + warp;
+        if (b >= c.B) return;
+        const int64_t lo = g.out_off[b], hi = g.out_off[b + 1];
+        const int32_t L = g.kv_lens[b];
+        int32_t st = kKvOk;
+        if (lo < 0 || hi > g.rows || hi - lo != L)
+            st = kKvBadLayout;
+        else if (L < 0 || L > (int64_t)c.bs * c.max_blocks)
+            st = kKvBadKv;
+        else
+            st = check_pages(c, (int32_t)b, 0, L);
+        if ((threadIdx.x & 31) == 0) g.seq_status[b] = st;
+        return;
+    }
+    const int per = kThreads / lanes;
+    const int64_t first = (int64_t)blockIdx.x * per;
+    if (warp == 0) {
+        const int32_t b = kv_find(g.out_off, c.B, first / c.H);
+        if (threadIdx.x == 0) b_first = b;
+    }
+    __syncthreads();
+    const int64_t e = first + threadIdx.x / lanes;
+    const int i = threadIdx.x % lanes;
+    const int64_t r = e / c.H;
+    const int32_t h = (int32_t)(e - r * c.H);
+    if (r >= g.rows || i * 8 >= c.D) return;
+    int32_t b = b_first;
+    while (b < c.B && g.out_off[b + 1] <= r) ++b;
+    if (b >= c.B) return;
+    const int64_t lo = g.out_off[b], hi = g.out_off[b + 1];
+    const int32_t L = g.kv_lens[b];
+    if (lo < 0 || hi > g.rows || hi - lo != L || r < lo || L > (int64_t)c.bs * c.max_blocks) return;
+    const int32_t pos = (int32_t)(r - lo);
+    const int32_t pg = c.table[(int64_t)b * c.max_blocks + pos / c.bs];
+    const int32_t sl = pos % c.bs;
+    const bool ok = pg >= 0 && pg < c.num_blocks;
+    const int64_t at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
+    const int64_t sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        const unsigned char* src = (kv ? c.v : c.k) + at;
+        unsigned char* dst = (kv ? g.v : g.k) + (r * c.H + h) * (int64_t)c.D * (ODT == kKvBf16 ? 2 : 4);
+        float x[8];
+        if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        } else if (Q8) {
+            const uint2 w = *(const uint2*)(src + 8 * i);
+            const float s = (kv ? c.vs : c.ks)[sc];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = kv_e4m3((uint8_t)(w.x >> (8 * j))) * s;
+                x[4 + j] = kv_e4m3((uint8_t)(w.y >> (8 * j))) * s;
+            }
+        } else {
+            load8<kKvBf16>(src, i, x);
+        }
+        if (ODT == kKvBf16) {
+            uint4 w;
+            w.x = pack_bf16(x[0], x[1]);
+            w.y = pack_bf16(x[2], x[3]);
+            w.z = pack_bf16(x[4], x[5]);
+            w.w = pack_bf16(x[6], x[7]);
+            *(uint4*)(dst + 16 * i) = w;
+        } else {
+            *(float4*)(dst + 32 * i) = make_float4(x[0], x[1], x[2], x[3]);
+            *(float4*)(dst + 32 * i + 16) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+// The accepted path's entries to the front of the tree's slots. Path nodes
+// rise (path[i] >= i + 1), so entry i's target, slot 1 + i, is read by no
+// later entry: taken in order, each thread's column moves in place. A thread
+// owns one 16-byte column (or one scale) of one layer and head, and takes the
+// path kMove entries at a time: loads together, then stores.
+constexpr int kMove = 8;
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, const KvMove m) {
+    __shared__ int64_t from[kMove], to[kMove];    // page * block + slot * token, bytes
+    __shared__ int64_t sfrom[kMove], sto[kMove];  // scales: page * H * bs + slot
+    const int32_t b = blockIdx.x;
+    const int64_t lo = m.node_off[b], hi = m.node_off[b + 1];
+    const int32_t L = m.kv_in[b], a = m.accepted[b];
+    int32_t st = kKvOk;
+    if (lo < 0 || hi > m.nodes || hi <= lo || a < 0 || a >= hi - lo)
+        st = kKvBadLayout;
+    else if (L < hi - lo || L > (int64_t)c.bs * c.max_blocks)
+        st = kKvBadKv;
+    const int32_t N = (int32_t)(hi - lo);
+    const int32_t base = L - N;
+    const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+    if (st == kKvOk) {
+        bool bad = false;
+        for (int32_t i = threadIdx.x; i < a; i += kThreads) {
+            const int32_t v = m.path[lo + i], u = i ? m.path[lo + i - 1] : 0;
+            if (v <= u || v >= N) {
+                bad = true;
+            } else {
+                const int32_t ps = table[(base + v) / c.bs], pd = table[(base + 1 + i) / c.bs];
+                bad |= ps < 0 || ps >= c.num_blocks || pd < 0 || pd >= c.num_blocks;
+            }
+        }
+        if (__syncthreads_or(bad)) st = kKvBadLayout;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        const int32_t out = st == kKvOk ? L - (N - 1 - a) : L;
+        m.kv_out[b] = out;
+        if (m.out_blocks) m.out_blocks[b] = (int32_t)(((int64_t)out + c.bs - 1) / c.bs);
+        if (m.seq_status) m.seq_status[b] = st;
+    }
+    if (st != kKvOk) return;
+    const int32_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);  // 16-byte columns of an entry, and its scale
+    const int64_t all = (int64_t)c.layers * c.H * 2 * cols;
+    const int64_t t = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+    const bool live = t < all;
+    const int32_t col = (int32_t)(t % cols);
+    int64_t x = t / cols;
+    const int32_t kv = (int32_t)(x & 1);
+    x >>= 1;
+    const int32_t h = (int32_t)(x % c.H);
+    const int64_t layer = x / c.H;
+    unsigned char* p = (kv ? c.v : c.k) + layer * c.layer_bytes + h * c.head_bytes + 16 * col;
+    const bool scale = c.ks && col == cols - 1;
+    float* sp = scale && live ? (kv ? c.vs : c.ks) + layer * c.scale_layer + (int64_t)h * c.bs : nullptr;
+    for (int32_t i0 = 0; i0 < a; i0 += kMove) {
+        const int32_t k = min(kMove, a - i0);
+        __syncthreads();
+        if (threadIdx.x < k) {
+            const int32_t i = i0 + threadIdx.x;
+            const int32_t s = base + m.path[lo + i], d = base + 1 + i;
+            const int64_t ps = table[s / c.bs], pd = table[d / c.bs];
+            from[threadIdx.x] = ps * c.block_bytes + (s % c.bs) * c.token_bytes;
+            to[threadIdx.x] = pd * c.block_bytes + (d % c.bs) * c.token_bytes;
+            sfrom[threadIdx.x] = ps * c.H * c.bs + s % c.bs;
+            sto[threadIdx.x] = pd * c.H * c.bs + d % c.bs;
+        }
+        __syncthreads();
+        if (!live) continue;
+        if (scale) {
+            float y[kMove];
+#pragma unroll
+            for (int j = 0; j < kMove; ++j)
+                if (j < k) y[j] = sp[sfrom[j]];
+#pragma unroll
+            for (int j = 0; j < kMove; ++j)
+                if (j < k && sfrom[j] != sto[j]) sp[sto[j]] = y[j];
+        } else {
+            uint4 y[kMove];
+#pragma unroll
+            for (int j = 0; j < kMove; ++j)
+                if (j < k && from[j] != to[j]) y[j] = *(const uint4*)(p + from[j]);
+#pragma unroll
+            for (int j = 0; j < kMove; ++j)
+                if (j < k && from[j] != to[j]) *(uint4*)(p + to[j]) = y[j];
+        }
+    }
+}
+
+// ------------------------------------------------------------ plain attention
+// One warp for each query row (token, query head), float32 throughout: 32
+// positions at a time, a lane's position's product with the query in shared
+// memory, the running maximum and sum over the warp, then the weighted values
+// with the head's columns spread over the lanes.
+constexpr int kPlainWarps = 4;
+
+__device__ __forceinline__ float entry_at(const KvView& c, const unsigned char* row, int d) {
+    return c.esz == 2 ? bf16_lo(*(const uint16_t*)(row + 2 * d)) : kv_e4m3(row[d]);
+}
+
+__global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const KvAttend p) {
+    __shared__ float q_sh[kPlainWarps][kKvMaxDim];
+    __shared__ uint32_t anc[kPlainWarps][kKvMaxQueries / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KvView& c = p.c;
+    const int32_t b = blockIdx.x;
+    const KvSeq s = kv_seq(b, p.row_off, p.t_max, p.rows, p.kv_lens, c.bs, c.max_blocks, true);
+    int32_t st = s.st;
+    if (st == kKvOk && p.parent) {
+        bool bad = false;
+        for (int32_t v = lane; v < s.T; v += 32) {
+            const int32_t u = p.parent[s.lo + v];
+            bad |= v == 0 ? u != -1 : (u < 0 || u >= v);
+        }
+        if (__any_sync(0xFFFFFFFFu, bad)) st = kKvBadLayout;
+    }
+    if (blockIdx.y == 0 && warp == 0 && p.seq_status) {
+        const int32_t st2 = st == kKvOk ? check_pages(c, b, 0, s.T ? s.L : 0) : st;
+        if (lane == 0) p.seq_status[b] = st2;
+    }
+    const int64_t w = (int64_t)blockIdx.y * kPlainWarps + warp;
+    if (s.lo < 0 || w >= (int64_t)s.T * p.Hq) return;
+    const int32_t t = (int32_t)(w / p.Hq), hq = (int32_t)(w % p.Hq), h = hq / p.G;
+    const int64_t row = s.lo + t;
+    unsigned char* out = p.out + (row * p.Hq + hq) * (int64_t)c.D * 2;
+    const float none = __uint_as_float(0xFF800000u);
+    if (st != kKvOk) {
+        for (int d = lane; d < c.D; d += 32) *(uint16_t*)(out + 2 * d) = 0;
+        if (p.lse && lane == 0) p.lse[row * p.Hq + hq] = none;
+        return;
+    }
+    const unsigned char* q = p.q + row * p.q_row_bytes + (int64_t)hq * c.D * 2;
+    for (int d = lane; d < c.D; d += 32) q_sh[warp][d] = bf16_lo(*(const uint16_t*)(q + 2 * d));
+    if (lane < kKvMaxQueries / 32) anc[warp][lane] = 0;
+    __syncwarp();
+    const int32_t ctx = s.L - s.T;
+    if (p.parent && lane == 0)
+        for (int32_t v = t; v >= 0; v = p.parent[s.lo + v]) anc[warp][v >> 5] |= 1u << (v & 31);
+    __syncwarp();
+    float m = none, l = 0.f, o[kKvMaxDim / 32];
+#pragma unroll
+    for (int j = 0; j < kKvMaxDim / 32; ++j) o[j] = 0.f;
+    const float k2 = p.scale * kLog2e;
+    const int32_t last = p.parent ? s.L : ctx + t + 1;  // positions past it are not seen
+    for (int32_t j0 = 0; j0 < last; j0 += 32) {
+        const int32_t j = j0 + lane;
+        float x = none, vscale = 1.f;
+        int64_t at = -1;
+        if (j < last && (!p.parent || j < ctx || (anc[warp][(j - ctx) >> 5] >> ((j - ctx) & 31) & 1))) {
+            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j / c.bs];
+            const int32_t sl = j % c.bs;
+            if (pg >= 0 && pg < c.num_blocks) {
+                at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
+                float acc = 0.f;
+                for (int d = 0; d < c.D; ++d) acc = fmaf(q_sh[warp][d], entry_at(c, c.k + at, d), acc);
+                if (c.ks) {
+                    const int64_t sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+                    acc *= c.ks[sc];
+                    vscale = c.vs[sc];
+                }
+                x = acc * k2;
+            }
+        }
+        float mt = x;
+        for (int sh = 16; sh; sh >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, sh));
+        const float mn = fmaxf(m, mt);
+        const float mr = mn == none ? 0.f : mn;
+        const float f = exp2f(m - mr);
+        const float w2 = at >= 0 ? exp2f(x - mr) : 0.f;
+        float lt = w2;
+        for (int sh = 16; sh; sh >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, sh);
+        l = l * f + lt;
+        m = mn;
+#pragma unroll
+        for (int k = 0; k < kKvMaxDim / 32; ++k) o[k] *= f;
+        const float wv = w2 * vscale;
+        for (int src = 0; src < 32; ++src) {
+            const int64_t a = __shfl_sync(0xFFFFFFFFu, at, src);
+            const float wt = __shfl_sync(0xFFFFFFFFu, wv, src);
+            if (a < 0) continue;
+#pragma unroll
+            for (int k = 0; k < kKvMaxDim / 32; ++k)
+                if (k * 32 + lane < c.D) o[k] = fmaf(wt, entry_at(c, c.v + a, k * 32 + lane), o[k]);
+        }
+    }
+    const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < kKvMaxDim / 32; ++k)
+        if (k * 32 + lane < c.D) *(uint16_t*)(out + 2 * (k * 32 + lane)) = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[k] * r, 0.f);
+    if (p.lse && lane == 0) p.lse[row * p.Hq + hq] = l == 0.f ? none : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+int lanes_of(int32_t D) {
+    int n = 1;
+    while (n * 8 < D) n <<= 1;
+    return n;  // D <= 256: at most a warp
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s) {
+    const int lanes = lanes_of(c.D);
+    const int per = kThreads / lanes;
+    const int64_t ctas = (n.rows * c.H + per - 1) / per;
+    const int64_t grid = ctas + (n.seq_status ? (c.B + kThreads / 32 - 1) / (kThreads / 32) : 0);
+    if (grid == 0) return cudaSuccess;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const bool q8 = c.esz == 1;
+    auto* f = n.dtype == kKvBf16 ? (q8 ? kv_append_kernel<kKvBf16, true> : kv_append_kernel<kKvBf16, false>)
+                                 : (q8 ? kv_append_kernel<kKvF32, true> : kv_append_kernel<kKvF32, false>);
+    f<<<(unsigned)grid, kThreads, 0, s>>>(c, n, lanes, ctas);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_gather(const KvView& c, const KvRead& g, cudaStream_t s) {
+    const int lanes = lanes_of(c.D);
+    const int per = kThreads / lanes;
+    const int64_t ctas = (g.rows * c.H + per - 1) / per;
+    const int64_t grid = ctas + (g.seq_status ? (c.B + kThreads / 32 - 1) / (kThreads / 32) : 0);
+    if (grid == 0) return cudaSuccess;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const bool q8 = c.esz == 1;
+    auto* f = g.dtype == kKvBf16 ? (q8 ? kv_gather_kernel<true, kKvBf16> : kv_gather_kernel<false, kKvBf16>)
+                                 : (q8 ? kv_gather_kernel<true, kKvF32> : kv_gather_kernel<false, kKvF32>);
+    f<<<(unsigned)grid, kThreads, 0, s>>>(c, g, lanes, ctas);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s) {
+    const int64_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);
+    const int64_t y = ((int64_t)c.layers * c.H * 2 * cols + kThreads - 1) / kThreads;
+    if (y > 65535) return cudaErrorInvalidValue;
+    kv_compact_kernel<<<dim3((unsigned)c.B, (unsigned)y), kThreads, 0, s>>>(c, m);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s) {
+    const int64_t y = ((int64_t)p.t_max * p.Hq + kPlainWarps - 1) / kPlainWarps;
+    if (y > 65535) return cudaErrorInvalidValue;
+    kv_attend_plain_kernel<<<dim3((unsigned)p.c.B, (unsigned)y), kPlainWarps * 32, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace specv

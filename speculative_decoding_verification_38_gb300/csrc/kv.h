@@ -1,0 +1,84 @@
+// kv.h -- parameter blocks and launch entry points of the paged key-value
+// cache's kernels (kv.cu, attend.cu). Not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace specv {
+
+constexpr int kKvMaxQueries = 128;  // new tokens of one sequence in the attention
+constexpr int kKvMaxDim = 256;
+
+enum KvType : int32_t { kKvF32 = 0, kKvBf16 = 1, kKvE4m3 = 2 };  // the API's dtype codes
+enum KvSeqStatus : int32_t { kKvOk = 0, kKvBadKv = 2, kKvBadLayout = 4, kKvTimeout = 6 };
+
+// One layer of a cache (k, v and the scales already point at the layer), or
+// the whole of it for the compaction.
+struct KvView {
+    unsigned char* k;
+    unsigned char* v;
+    float* ks;  // [num_blocks, kv_heads, block_size], or null
+    float* vs;
+    const int32_t* table;  // [B, max_blocks]
+    int64_t block_bytes, token_bytes, head_bytes, layer_bytes;
+    int64_t scale_layer;  // scales of a layer
+    int32_t B, H, D, bs, num_blocks, max_blocks, layers;
+    int32_t esz;  // bytes of an element: 2 or 1
+};
+
+struct KvNew {
+    const unsigned char* k;
+    const unsigned char* v;
+    int32_t dtype;
+    int64_t row_bytes;
+    int64_t rows;
+    const int64_t* row_off;  // [B+1] or null: t_max rows each
+    int32_t t_max;
+    const int32_t* kv_lens;
+    int32_t* seq_status;
+};
+
+struct KvRead {
+    unsigned char* k;
+    unsigned char* v;
+    int32_t dtype;
+    int64_t rows;
+    const int64_t* out_off;
+    const int32_t* kv_lens;
+    int32_t* seq_status;
+};
+
+struct KvMove {
+    const int64_t* node_off;
+    int64_t nodes;
+    const int32_t* path;
+    const int32_t* accepted;
+    const int32_t* kv_in;
+    int32_t* kv_out;
+    int32_t* out_blocks;
+    int32_t* seq_status;
+};
+
+struct KvAttend {
+    KvView c;
+    int32_t Hq, G, t_max;  // G = Hq / H
+    int64_t rows;
+    const int64_t* row_off;
+    const int32_t* kv_lens;
+    const int32_t* parent;
+    const unsigned char* q;
+    int64_t q_row_bytes;
+    float scale;
+    unsigned char* out;
+    float* lse;
+    int32_t* seq_status;
+};
+
+cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s);
+cudaError_t launch_kv_gather(const KvView& c, const KvRead& r, cudaStream_t s);
+cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s);
+cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s);
+
+}  // namespace specv
