@@ -1,0 +1,14 @@
+// attend_bf16.cu -- the attention kernel for bf16 caches, 16 and 32 query rows to a tile.
+#include "attend.cuh"
+
+namespace specv {
+
+cudaError_t attend_bf16(int nc, const AttParams& p, cudaStream_t s) {
+    switch (nc) {
+        case 8: return launch_dim<8, false>(p, s);
+        case 16: return launch_dim<16, false>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace specv

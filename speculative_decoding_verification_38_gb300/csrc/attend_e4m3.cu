@@ -1,0 +1,14 @@
+// attend_e4m3.cu -- the attention kernel for e4m3 caches, 16 and 32 query rows to a tile.
+#include "attend.cuh"
+
+namespace specv {
+
+cudaError_t attend_e4m3(int nc, const AttParams& p, cudaStream_t s) {
+    switch (nc) {
+        case 8: return launch_dim<8, true>(p, s);
+        case 16: return launch_dim<16, true>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace specv

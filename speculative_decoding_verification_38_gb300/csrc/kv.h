@@ -79,6 +79,12 @@ struct KvAttend {
 cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvView& c, const KvRead& r, cudaStream_t s);
 cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s);
+// The attention on the tensor cores (attend.cu), for head_dim up to 128;
+// rows = t_max * query heads of a key-value head sets the workspace.
+bool attend_takes(int32_t head_dim);
+size_t attend_workspace(int64_t rows);
+cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s);
+// One warp for each query row, for the rest.
 cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s);
 
 }  // namespace specv

@@ -168,7 +168,7 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* c, const int64_t* 
 
 SPEC_API size_t spec_kv_attend_workspace_size(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a) {
     if (check_attend_shape(c, a) != SPEC_OK) return 0;
-    return kHeaderBytes;
+    return attend_takes(c->head_dim) ? attend_workspace((int64_t)a->t_max * (a->q_heads / c->kv_heads)) : kHeaderBytes;
 }
 
 SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, spec_stream_t stream) {
@@ -202,7 +202,8 @@ SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* c, const spec_kv_at
     p.out = (unsigned char*)a->out;
     p.lse = a->lse;
     p.seq_status = a->seq_status;
-    return launched(launch_kv_attend_plain(p, (cudaStream_t)stream));
+    return launched(attend_takes(c->head_dim) ? launch_attend(p, a->workspace, (cudaStream_t)stream)
+                                              : launch_kv_attend_plain(p, (cudaStream_t)stream));
 }
 
 }  // extern "C"
