@@ -3,10 +3,10 @@
 
 namespace specv {
 
-cudaError_t attend_bf16(int nc, const AttParams& p, cudaStream_t s) {
-    switch (nc) {
-        case 8: return launch_dim<8, false>(p, s);
+cudaError_t attend_bf16(int n, const AttParams& p, cudaStream_t s) {
+    switch (n) {
         case 16: return launch_dim<16, false>(p, s);
+        case 32: return launch_dim<32, false>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }

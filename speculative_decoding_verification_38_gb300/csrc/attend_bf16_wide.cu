@@ -3,11 +3,11 @@
 
 namespace specv {
 
-cudaError_t attend_bf16_wide(int nc, const AttParams& p, cudaStream_t s) {
-    switch (nc) {
-        case 24: return launch_dim<24, false>(p, s);
-        case 40: return launch_dim<40, false>(p, s);
-        case 64: return launch_dim<64, false>(p, s);
+cudaError_t attend_bf16_wide(int n, const AttParams& p, cudaStream_t s) {
+    switch (n) {
+        case 48: return launch_dim<48, false>(p, s);
+        case 80: return launch_dim<80, false>(p, s);
+        case 128: return launch_dim<128, false>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,10 +3,10 @@
 
 namespace specv {
 
-cudaError_t attend_e4m3(int nc, const AttParams& p, cudaStream_t s) {
-    switch (nc) {
-        case 8: return launch_dim<8, true>(p, s);
+cudaError_t attend_e4m3(int n, const AttParams& p, cudaStream_t s) {
+    switch (n) {
         case 16: return launch_dim<16, true>(p, s);
+        case 32: return launch_dim<32, true>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }

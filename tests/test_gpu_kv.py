@@ -258,6 +258,17 @@ def test_attend_long(sv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,D,t", [(1, 64, 1), (4, 128, 1), (4, 128, 5), (4, 64, 9), (8, 128, 9), (4, 128, 29), (8, 128, 17)])
+def test_attend_many_tiles_to_a_processor(sv, dtype, G, D, t):
+    """More tiles than 152 processors take at once: runs of several tiles over several sequences and heads, every
+    size of row tile, groups of rows with nothing to do."""
+    lens = [int(x) for x in np.random.default_rng(3).integers(t, 1500, 24)]
+    c = Case(lens=lens, tokens=[max(1, t - b % 3) for b in range(24)], H=8, G=G, D=D, dtype=dtype, q_scale=2.0)
+    c.attend(sv)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attend_growing_scores(sv, dtype):
     """Scores that rise along the cache (every tile a new maximum), then fall."""
     for sign in (1, -1):
