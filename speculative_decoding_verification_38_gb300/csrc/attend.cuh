@@ -45,7 +45,7 @@ constexpr int kFeedWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
 constexpr int kSegWarp = kMmaWarp + 1;
 constexpr int kStatusWarp = kSegWarp + 1;
-constexpr int kAttThreads = (kStatusWarp + 1) * 32;
+constexpr int kAttThreads = (kStatusWarp + 2) * 32;  // whole groups of four warps
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 3;                  // tiles of the K ring, and of the V ring
 constexpr int kAuxRing = 8;                   // tiles of masks and scales kept: more than the ring and S can hold
@@ -86,6 +86,15 @@ __device__ __forceinline__ void tc_st8(uint32_t at, const float (&x)[8]) {
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// This group of four warps goes on with R registers a thread.
+template <int R>
+__device__ __forceinline__ void more_regs() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_regs() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 __device__ __forceinline__ uint64_t nanoseconds() {
     uint64_t t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -342,7 +351,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     const uint32_t tmem = *tmem_at;
     __syncthreads();  // P's memory is P's from here on
 
+    // The block starts with 72 registers a thread, 7 groups of four warps. bf16: softmax 88 (4 groups), feed 48 (2),
+    // the rest 56 (1); e4m3: 72, 80 and 56. Either adds up to 7 x 72.
     if (warp >= kSoftWarps && warp < kMmaWarp) {
+        if constexpr (Q8)
+            more_regs<80>();
+        else
+            fewer_regs<48>();
         // ============================================================ feed
         // Four warps bring the K tiles, four the V tiles, 32 rows each (lane =
         // row where an address is made). A bf16 tile goes straight to shared
@@ -359,10 +374,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         const int my_chunk = lane % chunks, my_row = lane / chunks;
         const bool chunk_in = my_chunk * (Q8 ? 16 : 8) < c.D;
         uint32_t kt = 0;
-        // where this warp writes chunk `ch` (eight 16-bit elements) of its row
-        auto swizzled = [&](uint32_t slot, int row, int ch) {
-            return ring + slot * X::slot_bytes + (ch >> 3) * (kTileTok * 128) + row * 128 + ((ch ^ row) & 7) * 16;
-        };
+        constexpr int rpr = 32 / chunks;  // rows of one load of the warp
+        // Where this lane writes its piece of row `my_row + r * rpr` (r constant): the swizzle exchanges 16-byte
+        // units within a row by its row's number, so the address is an exclusive or and an offset away from row my_row's.
+        const int unit = my_chunk * (Q8 ? 2 : 1);  // of eight 16-bit elements
+        const uint32_t at0 = ring + (unit >> 3) * (kTileTok * 128) + my_row * 128 + ((unit ^ my_row) & 7) * 16;
+        auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
         for (uint32_t si = 0;; ++si) {
             const Seg* const g = get_seg(si);
             const int n = g->n;
@@ -410,10 +427,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int r = 0; r < chunks; ++r) {
-                        const int row = r * (32 / chunks) + my_row;
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r * rpr + my_row);
                         const bool live = o >= 0 && chunk_in;
-                        cp16(swizzled(slot, row, my_chunk), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
+                        cp16(swizzled(at0 + slot * X::slot_bytes, r, 0), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     if (kt >= kLag) {
@@ -430,19 +446,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 auto issue = [&](uint4 (&w)[rounds], int64_t off, int half) {
 #pragma unroll
                     for (int r = 0; r < rounds; ++r) {
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, half * 16 + r * (32 / chunks) + my_row);
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, half * 16 + r * rpr + my_row);
                         w[r] = make_uint4(0, 0, 0, 0);
                         if (o >= 0 && chunk_in) w[r] = ld_stream_v4(src + o + my_chunk * 16);
                     }
                 };
-                auto hand = [&](const uint4 (&w)[rounds], uint32_t slot, int half) {
+                auto hand = [&](const uint4 (&w)[rounds], uint32_t base) {
 #pragma unroll
                     for (int r = 0; r < rounds; ++r) {
-                        const int row = half * 16 + r * (32 / chunks) + my_row;
-                        sts16(swizzled(slot, row, 2 * my_chunk),
+                        sts16(swizzled(base, r, 0),
                               make_uint4(e4m3_f16x2(w[r].x & 0xFFFF), e4m3_f16x2(w[r].x >> 16), e4m3_f16x2(w[r].y & 0xFFFF),
                                          e4m3_f16x2(w[r].y >> 16)));
-                        sts16(swizzled(slot, row, 2 * my_chunk + 1),
+                        sts16(swizzled(base, r, 1),
                               make_uint4(e4m3_f16x2(w[r].z & 0xFFFF), e4m3_f16x2(w[r].z >> 16), e4m3_f16x2(w[r].w & 0xFFFF),
                                          e4m3_f16x2(w[r].w >> 16)));
                     }
@@ -471,12 +486,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         if (lane == 0) mbar_arrive(aux_full + kt % kAuxRing);
                     }
                     off = next;
-                    hand(d[0], slot, 0);
+                    hand(d[0], at0 + slot * X::slot_bytes);
                     if (t + 1 < n) {
                         scales();
                         issue(d[0], off, 0);
                     }
-                    hand(d[1], slot, 1);
+                    hand(d[1], at0 + slot * X::slot_bytes + 16 * 128);
                     if (t + 1 < n) issue(d[1], off, 1);
                     fence_async();
                     __syncwarp();
@@ -491,7 +506,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             if (lane == 0)
                 for (uint32_t t = kt > kLag ? kt - kLag : 0; t < kt; ++t) mbar_arrive(my_full + t % S);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
+        fewer_regs<56>();
+        if (warp == kMmaWarp) {
         // ============================================================ products
         constexpr uint32_t id_qk = instr_desc(!Q8, false, false, N);
         constexpr uint32_t id_pv = instr_desc(!Q8, true, true, X::NP);
@@ -590,7 +607,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 if (lane == 0) a.seq_status[b] = st;
             }
         }
+        }
     } else {
+        if constexpr (!Q8) more_regs<88>();
         // ============================================================ softmax
         // Thread = one position of the tile; group gr has the 8-row pieces gr,
         // gr + 4, ... of the query rows. A weight is 2^(score - m) with m the
