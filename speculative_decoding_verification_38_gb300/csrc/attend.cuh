@@ -45,13 +45,14 @@ constexpr int kFeedWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
 constexpr int kSegWarp = kMmaWarp + 1;
 constexpr int kStatusWarp = kSegWarp + 1;
-constexpr int kAttThreads = (kStatusWarp + 2) * 32;  // whole groups of four warps
+constexpr int kQueryWarp = kStatusWarp + 1;
+constexpr int kAttThreads = (kQueryWarp + 1) * 32;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 3;                  // tiles of the K ring, and of the V ring
+constexpr int kRawTiles = 3;                  // e4m3 tiles under way as they are
 constexpr int kAuxRing = 8;                   // tiles of masks and scales kept: more than the ring and S can hold
 constexpr uint64_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
 constexpr float kNoMax = -1.0e30f;            // running maximum before any score
-constexpr float kGrow = 8.f;                  // a maximum may rise by 2^8 before the sums are rescaled
 constexpr size_t kSmemMax = 232448;
 
 // ------------------------------------------------------------ instructions
@@ -69,6 +70,13 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
 __device__ __forceinline__ void tc_ld8(uint32_t at, float (&x)[8]) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -76,6 +84,12 @@ __device__ __forceinline__ void tc_ld8(uint32_t at, float (&x)[8]) {
                  : "r"(at));
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld8(uint32_t at, float2 (&x)[4]) {
+    float y[8];
+    tc_ld8(at, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
 }
 __device__ __forceinline__ void tc_st8(uint32_t at, const float (&x)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
@@ -113,8 +127,26 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int K>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(K) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
+}
 __device__ __forceinline__ void sts16(uint32_t dst, uint4 w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+__device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // a in the low half
     uint32_t r;
@@ -160,23 +192,32 @@ struct Shape {
     static constexpr int N = NN;                           // query rows of a row tile
     static constexpr int MC = (N / 8 + kGroups - 1) / kGroups;  // 8-row pieces of a softmax group
     static constexpr int NP = Q8 ? N : 2 * N;              // P's columns: one f16, or two bf16 parts
+    static constexpr int QB = N == 128 || (Q8 && N == 80) ? 1 : 2;  // row tiles of queries held
+    static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory is full: rings of two
+    static constexpr int segs = tight ? 2 : 4;             // segments known ahead
+    static constexpr int ring_bars = tight ? 8 : 4 * kMaxSlots;  // full and empty, K and V
     static constexpr uint32_t slot_bytes = kTileTok * DP * 2;
+    static constexpr uint32_t raw_bytes = Q8 ? 2 * (N == 128 ? 2 : kRawTiles) * kTileTok * DP : 0;
+    static constexpr int raw_tiles = N == 128 ? 2 : kRawTiles;
     static constexpr uint32_t q_bytes = N * DP * 2;
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
-    static constexpr int segs = !Q8 && N == 128 && DP == 128 ? 2 : 4;  // segments known ahead
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
-    // after the slots, Q and P: aux ring, running maxima, row factors, ancestors, segments, poison, barriers
-    static constexpr uint32_t misc = kAuxRing * aux_bytes + N * 4 + (Q8 ? N * 4 + kGroups * red_bytes : 0) +
+    // after the tiles, Q and P: aux ring, running maxima, row factors, scratch, ancestors, segments, poison, barriers
+    static constexpr uint32_t misc = kAuxRing * aux_bytes + N * 4 + (Q8 ? segs * N * 4 : 0) + (tight ? 0 : kGroups * red_bytes) +
                                      kKvMaxQueries * 16 + segs * sizeof(Seg) + 32 +
-                                     (4 * kMaxSlots + 8 + kAuxRing + 2 * segs) * 8;
-    static constexpr int fit = (int)((kSmemMax - q_bytes - p_bytes - misc) / (2 * slot_bytes));
-    static constexpr int slots = fit > kMaxSlots ? kMaxSlots : fit;
-    static constexpr uint32_t total = 2 * slots * slot_bytes + q_bytes + p_bytes + misc;
-    static constexpr int lag = slots - 1;  // tiles whose copies are in flight when one is handed over
-    static_assert(slots >= 2, "a ring needs two tiles");
-    // the feed may wait for a new segment with `lag` tiles, each a segment, not handed over
-    static_assert(segs > lag, "the oldest known segment must be whole in the ring");
+                                     (ring_bars + 11 + kAuxRing + 2 * segs) * 8;
+    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - p_bytes - misc) / slot_bytes);
+    // tiles of the K ring (e4m3: in TMEM) and of the V ring; a V tile is held longer
+    static constexpr int SK = Q8 ? 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
+    static constexpr int rest = Q8 ? fit : fit - SK;
+    static constexpr int SV = rest > kMaxSlots ? kMaxSlots : rest;
+    static constexpr uint32_t ring_bytes = (Q8 ? SV : SK + SV) * slot_bytes;
+    static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + p_bytes + misc;
+    static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
+    static_assert(2 * (SK + SV) <= ring_bars && total <= kSmemMax, "shared memory");
+    // the feed may wait for a new segment with this many tiles, each a segment, not handed over
+    static_assert(segs > (Q8 ? raw_tiles - 1 : SV - 1), "the oldest known segment must be whole in the ring");
 };
 
 template <int N>
@@ -226,31 +267,36 @@ struct Walk {
 template <int NN, int DP, bool Q8>
 __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using X = Shape<NN, DP, Q8>;
-    constexpr int N = X::N, S = X::slots, MC = X::MC, R = X::segs;
-    constexpr uint32_t kLag = X::lag;
+    constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB;
+    constexpr uint32_t SK = X::SK, SV = X::SV;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char* const q_sm = smem + 2 * S * X::slot_bytes;
-    unsigned char* const p_sm = q_sm + X::q_bytes;
+    unsigned char* const v_sm = smem + (Q8 ? 0 : SK * X::slot_bytes);  // the V ring; the K ring, if any, is before it
+    unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [2][raw_tiles] K and V tiles as they are
+    unsigned char* const q_sm = raw_sm + X::raw_bytes;
+    unsigned char* const p_sm = q_sm + QB * X::q_bytes;
     unsigned char* const aux_sm = p_sm + X::p_bytes;
     float* const mref = (float*)(aux_sm + kAuxRing * X::aux_bytes);
-    float* const arow = mref + N;  // Q8: a query row's power of two times scale * log2(e)
-    unsigned char* const red_sm = (unsigned char*)(mref + (Q8 ? 2 * N : N));
-    uint32_t* const anc = (uint32_t*)(red_sm + (Q8 ? kGroups * X::red_bytes : 0));  // [T][4] ancestors of a tree's tokens
+    float* const arow_all = mref + N;  // Q8: [R][N] a query row's power of two times scale * log2(e)
+    unsigned char* const red_sm = (unsigned char*)(mref + (Q8 ? (1 + R) * N : N));
+    uint32_t* const anc = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] ancestors of a tree's tokens
     Seg* const segs = (Seg*)(anc + kKvMaxQueries * 4);
     uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then 4 words:
     volatile uint32_t* const aborted = poison + 4;   // a wait gave up
     uint32_t* const tmem_at = poison + 5;
     uint32_t* const last_in = poison + 6;
     uint32_t* const tree_bad = poison + 7;
-    uint64_t* const full = (uint64_t*)(poison + 8);  // [2][S]: the K ring, the V ring
-    uint64_t* const empty = full + 2 * S;
-    uint64_t* const s_full = empty + 2 * S;
+    uint64_t* const k_full = (uint64_t*)(poison + 8);
+    uint64_t* const v_full = k_full + SK;
+    uint64_t* const k_empty = v_full + SV;
+    uint64_t* const v_empty = k_empty + SK;
+    uint64_t* const s_full = v_empty + SV;
     uint64_t* const s_empty = s_full + 2;
     uint64_t* const p_full = s_empty + 2;
     uint64_t* const pv_done = p_full + 1;
-    uint64_t* const q_full = pv_done + 1;
-    uint64_t* const drain = q_full + 1;
-    uint64_t* const aux_full = drain + 1;
+    uint64_t* const drain = pv_done + 1;
+    uint64_t* const q_full = drain + 1;
+    uint64_t* const q_empty = q_full + 2;
+    uint64_t* const aux_full = q_empty + 2;
     uint64_t* const seg_full = aux_full + kAuxRing;
     uint64_t* const seg_empty = seg_full + R;
 
@@ -280,22 +326,27 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 
     // ------------------------------------------------- this CTA's run of tiles
     if (tid == 0) {
-        for (int i = 0; i < 2 * S; ++i) {
-            mbar_init(full + i, kFeedWarps / 2);
-            mbar_init(empty + i, 1);
+        for (uint32_t i = 0; i < SK; ++i) {
+            mbar_init(k_full + i, kFeedWarps / 2);
+            mbar_init(k_empty + i, 1);
+        }
+        for (uint32_t i = 0; i < SV; ++i) {
+            mbar_init(v_full + i, kFeedWarps / 2);
+            mbar_init(v_empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, kSoftWarps);
+            mbar_init(q_full + i, 1);
+            mbar_init(q_empty + i, 1);
         }
         mbar_init(p_full, kSoftWarps);
         mbar_init(pv_done, 1);
-        mbar_init(q_full, kSoftWarps);
         mbar_init(drain, 1);
         for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, kFeedWarps / 2);
         for (int i = 0; i < R; ++i) {
             mbar_init(seg_full + i, 1);
-            mbar_init(seg_empty + i, kSoftWarps + kFeedWarps + 1);
+            mbar_init(seg_empty + i, kSoftWarps + kFeedWarps + 2);
         }
         *aborted = 0;
         fence_barrier_init();
@@ -352,159 +403,195 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     __syncthreads();  // P's memory is P's from here on
 
     // The block starts with 72 registers a thread, 7 groups of four warps. bf16: softmax 88 (4 groups), feed 48 (2),
-    // the rest 56 (1); e4m3: 72, 80 and 56. Either adds up to 7 x 72.
+    // the rest 56 (1); e4m3: 80, 64 and 56. Either adds up to 7 x 72.
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         if constexpr (Q8)
-            more_regs<80>();
+            fewer_regs<64>();
         else
             fewer_regs<48>();
         // ============================================================ feed
         // Four warps bring the K tiles, four the V tiles, 32 rows each (lane =
-        // row where an address is made). A bf16 tile goes straight to shared
-        // memory (cp.async); an e4m3 tile passes the registers, where it becomes
-        // f16 (exactly), its lines asked into L2 a tile ahead. Rows past the
-        // length, on a page outside the pool or past head_dim are zeros.
+        // row where an address is made), by cp.async. bf16: straight to the
+        // rings. e4m3: as they are to a warp's own place; from there, two tiles
+        // later, as f16 (exactly) to the V ring, or to TMEM as the product's
+        // first operand. Rows past the length, on a page outside the pool or
+        // past head_dim are zeros.
         const bool is_k = warp < kSoftWarps + 4;
         const int fw = warp & 3;
         const unsigned char* const src = is_k ? c.k : c.v;
-        const uint32_t ring = smem_addr(smem) + (is_k ? 0 : S * X::slot_bytes) + fw * 32 * 128;
-        uint64_t* const my_full = full + (is_k ? 0 : S);
-        uint64_t* const my_empty = empty + (is_k ? 0 : S);
+        uint64_t* const my_full = is_k ? k_full : v_full;
+        uint64_t* const my_empty = is_k ? k_empty : v_empty;
         constexpr int chunks = DP * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a padded row
+        constexpr int rpr = 32 / chunks;                // rows of one load of the warp
         const int my_chunk = lane % chunks, my_row = lane / chunks;
         const bool chunk_in = my_chunk * (Q8 ? 16 : 8) < c.D;
-        uint32_t kt = 0;
-        constexpr int rpr = 32 / chunks;  // rows of one load of the warp
-        // Where this lane writes its piece of row `my_row + r * rpr` (r constant): the swizzle exchanges 16-byte
-        // units within a row by its row's number, so the address is an exclusive or and an offset away from row my_row's.
-        const int unit = my_chunk * (Q8 ? 2 : 1);  // of eight 16-bit elements
-        const uint32_t at0 = ring + (unit >> 3) * (kTileTok * 128) + my_row * 128 + ((unit ^ my_row) & 7) * 16;
+        // Where this lane writes eight 16-bit elements of row `my_row + r * rpr` (r constant) in a ring tile: the
+        // swizzle exchanges 16-byte units within a row by its row's number, so the address is an exclusive or and an
+        // offset away from row my_row's.
+        const int unit = my_chunk * (Q8 ? 2 : 1);
+        const uint32_t at0 = smem_addr(is_k && !Q8 ? smem : v_sm) + fw * 32 * 128 + (unit >> 3) * (kTileTok * 128) +
+                             my_row * 128 + ((unit ^ my_row) & 7) * 16;
         auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
-        for (uint32_t si = 0;; ++si) {
+
+        // the walk over this CTA's tiles: page of the row at `pos` one tile ahead
+        uint32_t si = 0, kt = 0;  // segment, tiles loaded
+        int n = 0, t = 0;
+        int32_t L = 0, pos = 0, pg = -1;
+        const int32_t* table = nullptr;
+        int64_t head = 0, sc_head = 0;
+        auto page_at = [&](int32_t at) { return at < L ? table[at / c.bs] : -1; };
+        // opens the next segment when this one is through; false: no more
+        auto more = [&]() {
+            if (t < n) return true;
             const Seg* const g = get_seg(si);
-            const int n = g->n;
-            if (!n) break;
-            const int32_t L = g->L;
-            int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
-            const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
-            const int64_t head = g->h * c.head_bytes, sc_head = (int64_t)g->h * c.bs;
-            done_seg(si);
-            // byte offset of the row at position pos (-1: no row), and its scales'
-            int64_t sc_next = 0;
-            auto row_at = [&]() {
-                int64_t o = -1;
-                if (pos < L) {
-                    const int32_t pg = table[pos / c.bs];
-                    const int32_t sl = pos % c.bs;
-                    if (pg >= 0 && pg < c.num_blocks) {
-                        o = pg * c.block_bytes + sl * c.token_bytes + head;
-                        if (Q8) {
-                            sc_next = (int64_t)pg * c.H * c.bs + sl + sc_head;
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + o));
-                            if (is_k) {
-                                asm volatile("prefetch.global.L2 [%0];" ::"l"(c.ks + sc_next));
-                                asm volatile("prefetch.global.L2 [%0];" ::"l"(c.vs + sc_next));
-                            }
-                        }
+            n = g->n;
+            t = 0;
+            if (!n) return false;
+            L = g->L;
+            pos = g->tile0 * kTileTok + fw * 32 + lane;
+            table = c.table + (int64_t)g->b * c.max_blocks;
+            head = g->h * c.head_bytes;
+            sc_head = (int64_t)g->h * c.bs;
+            done_seg(si++);
+            pg = page_at(pos);
+            return true;
+        };
+        // this lane's row of the tile: its byte offset (-1: no row) and its scales'; on to the next tile
+        int64_t sc_at = 0;
+        auto row = [&]() {
+            int64_t o = -1;
+            if (pg >= 0 && pg < c.num_blocks) {
+                const int32_t sl = pos % c.bs;
+                o = pg * c.block_bytes + sl * c.token_bytes + head;
+                if (Q8) sc_at = (int64_t)pg * c.H * c.bs + sl + sc_head;
+            }
+            pos += kTileTok;
+            ++t;
+            pg = t < n ? page_at(pos) : -1;
+            return o;
+        };
+        auto aux_of = [&](uint32_t tile) { return aux_sm + (tile % kAuxRing) * X::aux_bytes; };
+
+        if constexpr (!Q8) {
+            auto publish = [&](uint32_t slot) {
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(my_full + slot);
+            };
+            const uint32_t S = is_k ? SK : SV, lag = S - 1;  // copies of `lag` tiles are under way when one is handed over
+            uint32_t slot = 0, round = 0, out = 0;           // out: slot of the next tile to hand over
+            while (more()) {
+                const int64_t off = row();
+                if (round) wait(my_empty + slot, (round - 1) & 1);
+                if (is_k) {
+                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
+                    if (lane == 0) {
+                        ((uint32_t*)aux_of(kt))[fw] = bits;
+                        mbar_arrive(aux_full + kt % kAuxRing);
                     }
                 }
-                return o;
+                const uint32_t base = at0 + slot * X::slot_bytes;
+#pragma unroll
+                for (int r = 0; r < chunks; ++r) {
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r * rpr + my_row);
+                    const bool live = o >= 0 && chunk_in;
+                    cp16(swizzled(base, r, 0), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
+                }
+                cp_commit();
+                if (kt >= lag) {
+                    if (lag == 1)
+                        cp_wait<1>();
+                    else
+                        cp_wait<2>();
+                    publish(out);
+                    if (++out == S) out = 0;
+                }
+                ++kt;
+                if (++slot == S) slot = 0, ++round;
+            }
+            cp_wait<0>();
+            for (uint32_t i = kt > lag ? lag : kt; i; --i) {
+                publish(out);
+                if (++out == S) out = 0;
+            }
+        } else {
+            constexpr int RT = X::raw_tiles, ahead = RT - 1;
+            // a warp's own rows, 16-byte units exchanged so that a column of them lies in different banks
+            const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : RT * kTileTok * DP) + fw * 32 * DP;
+            auto raw_at = [&](int tile, int r, int u) {
+                return raw + tile * (kTileTok * DP) + r * DP + ((u ^ (DP == 128 ? r & 7 : (r >> 1) & 3)) * 16);
             };
-            int64_t next = row_at();
-            if constexpr (!Q8) {
-                for (int t = 0; t < n; ++t, ++kt) {
-                    const int64_t off = next;
-                    pos += kTileTok;
-                    next = t + 1 < n ? row_at() : -1;
-                    const uint32_t slot = kt % S, use = kt / S;
-                    if (use) wait(my_empty + slot, (use - 1) & 1);
-                    if (is_k) {
-                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
-                        if (lane == 0) {
-                            ((uint32_t*)(aux_sm + (kt % kAuxRing) * X::aux_bytes))[fw] = bits;
-                            mbar_arrive(aux_full + kt % kAuxRing);
-                        }
-                    }
+            bool open = true;
+            int in = 0;  // raw place of the next tile loaded
+            auto load = [&]() {
+                open = open && more();
+                if (open) {
+                    const int64_t off = row();
 #pragma unroll
                     for (int r = 0; r < chunks; ++r) {
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r * rpr + my_row);
+                        const int rr = r * rpr + my_row;
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
                         const bool live = o >= 0 && chunk_in;
-                        cp16(swizzled(at0 + slot * X::slot_bytes, r, 0), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
+                        cp16(raw_at(in, rr, my_chunk), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (kt >= kLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(my_full + (kt - kLag) % S);
-                    }
-                }
-            } else {
-                // a tile in pieces of 16 rows, two of them on their way in registers
-                constexpr int rounds = chunks / 2;
-                uint4 d[2][rounds];
-                auto issue = [&](uint4 (&w)[rounds], int64_t off, int half) {
-#pragma unroll
-                    for (int r = 0; r < rounds; ++r) {
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, half * 16 + r * rpr + my_row);
-                        w[r] = make_uint4(0, 0, 0, 0);
-                        if (o >= 0 && chunk_in) w[r] = ld_stream_v4(src + o + my_chunk * 16);
-                    }
-                };
-                auto hand = [&](const uint4 (&w)[rounds], uint32_t base) {
-#pragma unroll
-                    for (int r = 0; r < rounds; ++r) {
-                        sts16(swizzled(base, r, 0),
-                              make_uint4(e4m3_f16x2(w[r].x & 0xFFFF), e4m3_f16x2(w[r].x >> 16), e4m3_f16x2(w[r].y & 0xFFFF),
-                                         e4m3_f16x2(w[r].y >> 16)));
-                        sts16(swizzled(base, r, 1),
-                              make_uint4(e4m3_f16x2(w[r].z & 0xFFFF), e4m3_f16x2(w[r].z >> 16), e4m3_f16x2(w[r].w & 0xFFFF),
-                                         e4m3_f16x2(w[r].w >> 16)));
-                    }
-                };
-                int64_t off = next;
-                float sk = 0.f, sv = 0.f;
-                auto scales = [&]() {
-                    sk = sv = 0.f;
-                    if (is_k && off >= 0) sk = c.ks[sc_next], sv = c.vs[sc_next];
-                };
-                scales();
-                issue(d[0], off, 0);
-                issue(d[1], off, 1);
-                for (int t = 0; t < n; ++t, ++kt) {
-                    pos += kTileTok;
-                    next = t + 1 < n ? row_at() : -1;
-                    const uint32_t slot = kt % S, use = kt / S;
-                    if (use) wait(my_empty + slot, (use - 1) & 1);
                     if (is_k) {
-                        unsigned char* const at = aux_sm + (kt % kAuxRing) * X::aux_bytes;
+                        unsigned char* const at = aux_of(kt);
                         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
                         if (lane == 0) ((uint32_t*)at)[fw] = bits;
-                        ((float*)(at + 16))[fw * 32 + lane] = sk;
-                        ((float*)(at + 16))[kTileTok + fw * 32 + lane] = sv;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(aux_full + kt % kAuxRing);
+                        const uint32_t sc = smem_addr(at + 16) + (fw * 32 + lane) * 4;
+                        cp4(sc, off >= 0 ? c.ks + sc_at : c.ks, off >= 0 ? 4u : 0u);
+                        cp4(sc + kTileTok * 4, off >= 0 ? c.vs + sc_at : c.vs, off >= 0 ? 4u : 0u);
                     }
-                    off = next;
-                    hand(d[0], at0 + slot * X::slot_bytes);
-                    if (t + 1 < n) {
-                        scales();
-                        issue(d[0], off, 0);
-                    }
-                    hand(d[1], at0 + slot * X::slot_bytes + 16 * 128);
-                    if (t + 1 < n) issue(d[1], off, 1);
-                    fence_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(my_full + slot);
+                    ++kt;
+                    if (++in == RT) in = 0;
                 }
+                cp_commit();
+            };
+#pragma unroll
+            for (int i = 0; i < ahead; ++i) load();
+            const uint32_t S = is_k ? SK : SV;
+            uint32_t slot = 0, round = 0;
+            int from = 0;  // raw place of the next tile turned
+            for (uint32_t done = 0;; ++done) {
+                load();
+                if (done == kt) break;
+                cp_wait<ahead>();
+                __syncwarp();
+                if (round) wait(my_empty + slot, (round - 1) & 1);
+                if (is_k) {
+                    // lane = row = TMEM lane: two elements to a column
+                    tc_after();
+                    const uint32_t at = tmem + 2 * N + X::NP + slot * (DP / 2) + ((uint32_t)fw << 21);
+#pragma unroll
+                    for (int u = 0; u < DP / 16; ++u) {
+                        const uint4 w = lds16(raw_at(from, lane, u));
+                        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at + u * 8),
+                                     "r"(e4m3_f16x2(w.x & 0xFFFF)), "r"(e4m3_f16x2(w.x >> 16)),
+                                     "r"(e4m3_f16x2(w.y & 0xFFFF)), "r"(e4m3_f16x2(w.y >> 16)),
+                                     "r"(e4m3_f16x2(w.z & 0xFFFF)), "r"(e4m3_f16x2(w.z >> 16)),
+                                     "r"(e4m3_f16x2(w.w & 0xFFFF)), "r"(e4m3_f16x2(w.w >> 16))
+                                     : "memory");
+                    }
+                    tc_wait_st();
+                    tc_before();
+                    if (lane == 0) mbar_arrive(aux_full + done % kAuxRing);
+                } else {
+                    const uint32_t base = at0 + slot * X::slot_bytes;
+#pragma unroll
+                    for (int r = 0; r < chunks; ++r) {
+                        const uint4 w = lds16(raw_at(from, r * rpr + my_row, my_chunk));
+                        sts16(swizzled(base, r, 0), make_uint4(e4m3_f16x2(w.x & 0xFFFF), e4m3_f16x2(w.x >> 16),
+                                                               e4m3_f16x2(w.y & 0xFFFF), e4m3_f16x2(w.y >> 16)));
+                        sts16(swizzled(base, r, 1), make_uint4(e4m3_f16x2(w.z & 0xFFFF), e4m3_f16x2(w.z >> 16),
+                                                               e4m3_f16x2(w.w & 0xFFFF), e4m3_f16x2(w.w >> 16)));
+                    }
+                    fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(my_full + slot);
+                if (++slot == S) slot = 0, ++round;
+                if (++from == RT) from = 0;
             }
-        }
-        if constexpr (!Q8) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            fence_async();
-            __syncwarp();
-            if (lane == 0)
-                for (uint32_t t = kt > kLag ? kt - kLag : 0; t < kt; ++t) mbar_arrive(my_full + t % S);
         }
     } else if (warp >= kMmaWarp) {
         fewer_regs<56>();
@@ -512,41 +599,50 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         // ============================================================ products
         constexpr uint32_t id_qk = instr_desc(!Q8, false, false, N);
         constexpr uint32_t id_pv = instr_desc(!Q8, true, true, X::NP);
-        const uint64_t k_desc = operand(smem_addr(smem), 16, 1024, 2), q_desc = operand(smem_addr(q_sm), 16, 1024, 2);
-        const uint64_t v_desc = operand(smem_addr(smem) + S * X::slot_bytes, DP == 128 ? kTileTok * 128 : 0, 1024, 2);
+        const uint64_t k_desc = operand(smem_addr(smem), 16, 1024, 2);
+        const uint64_t v_desc = operand(smem_addr(v_sm), DP == 128 ? kTileTok * 128 : 0, 1024, 2);
         const uint64_t p_desc = operand(smem_addr(p_sm), 128, 2048, 0);
-        uint32_t gt = 0;
+        uint32_t gt = 0, ks = 0, kr = 0, vs = 0, vr = 0;  // ring places and rounds
         for (uint32_t si = 0;; ++si) {
             const int n = get_seg(si)->n;
             if (!n) break;
             if (lane == 0) {
-                wait(q_full, si & 1);
+                const uint32_t qb = si % QB;
+                const uint64_t q_desc = operand(smem_addr(q_sm + qb * X::q_bytes), 16, 1024, 2);
+                wait(q_full + qb, (si / QB) & 1);
                 auto scores = [&](int i) {
-                    const uint32_t t = gt + i, buf = t & 1, slot = t % S;
-                    wait(full + slot, (t / S) & 1);
+                    const uint32_t t = gt + i, buf = t & 1;
+                    wait(k_full + ks, kr & 1);
                     if (t >= 2) wait(s_empty + buf, ((t >> 1) - 1) & 1);
                     tc_after();
-                    const uint64_t ka = k_desc + slot * (X::slot_bytes >> 4);
+                    const uint64_t ka = k_desc + ks * (X::slot_bytes >> 4);
+                    const uint32_t kt = tmem + 2 * N + X::NP + ks * (DP / 2);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        tc_mma(tmem + buf * N, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4),
-                               q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
-                    tc_commit(empty + slot);
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint64_t qd = q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4);
+                        if constexpr (Q8)
+                            tc_mma_ts(tmem + buf * N, kt + k * 8, qd, id_qk, k > 0);
+                        else
+                            tc_mma(tmem + buf * N, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4), qd, id_qk, k > 0);
+                    }
+                    tc_commit(k_empty + ks);
                     tc_commit(s_full + buf);
+                    if (i + 1 == n) tc_commit(q_empty + qb);
+                    if (++ks == SK) ks = 0, ++kr;
                 };
                 scores(0);
                 for (int i = 0; i < n; ++i) {
                     if (i + 1 < n) scores(i + 1);
-                    const uint32_t t = gt + i, slot = t % S;
-                    wait(full + S + slot, (t / S) & 1);
-                    wait(p_full, t & 1);
+                    wait(v_full + vs, vr & 1);
+                    wait(p_full, (gt + i) & 1);
                     tc_after();
-                    const uint64_t va = v_desc + slot * (X::slot_bytes >> 4);
+                    const uint64_t va = v_desc + vs * (X::slot_bytes >> 4);
 #pragma unroll
                     for (int k = 0; k < kTileTok / 16; ++k)
                         tc_mma(tmem + 2 * N, va + ((k * 2048) >> 4), p_desc + ((k * 256) >> 4), id_pv, i > 0 || k > 0);
-                    tc_commit(empty + S + slot);
+                    tc_commit(v_empty + vs);
                     tc_commit(pv_done);
+                    if (++vs == SV) vs = 0, ++vr;
                 }
             }
             gt += n;
@@ -559,6 +655,79 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             }
         }
         __syncwarp();
+    } else if (warp == kQueryWarp) {
+        // ============================================================ queries
+        // Row tiles of queries, a segment ahead where there is room for two.
+        const float k2 = a.scale * kLog2e;
+        constexpr int qc = DP / 8, rpq = 32 / qc;  // 16-byte pieces of a row, rows of one load
+        constexpr int step = 4;
+        static_assert(N % (step * rpq) == 0, "rows of a round of loads");
+        const int piece = lane % qc, sub = lane / qc;
+        for (uint32_t si = 0;; ++si) {
+            const Seg* const g = get_seg(si);
+            if (!g->n) break;
+            const int32_t row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
+            const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)g->h * a.G * c.D * 2 + piece * 16;
+            auto row_of = [&](int r) {
+                const int32_t rr = row0 + r, t = rr / a.G;
+                return q0 + t * a.q_row_bytes + (int64_t)(rr - t * a.G) * c.D * 2;
+            };
+            if (QB == 1)  // into L2 while the last products still need the place
+                for (int r = sub; r < rows; r += rpq)
+                    if (piece * 8 < c.D && (piece & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(r)));
+            if (si >= QB) wait(q_empty + si % QB, (si / QB - 1) & 1);
+            const uint32_t q_at = smem_addr(q_sm) + (si % QB) * X::q_bytes + (piece >> 3) * (N * 128);
+            if constexpr (!Q8) {
+#pragma unroll 1
+                for (int r = sub; r < N; r += rpq) {
+                    const bool in = r < rows && piece * 8 < c.D;
+                    cp16(q_at + r * 128 + ((piece ^ r) & 7) * 16, in ? row_of(r) : a.q, in ? 16u : 0u);
+                }
+                cp_commit();
+                cp_wait<0>();
+            } else {
+            float* const arow = arow_all + (si % R) * N;
+#pragma unroll 1
+            for (int r0 = 0; r0 < N; r0 += step * rpq) {
+                uint4 w[step];
+#pragma unroll
+                for (int i = 0; i < step; ++i) {
+                    const int r = r0 + i * rpq + sub;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (r < rows && piece * 8 < c.D) w[i] = *(const uint4*)row_of(r);
+                }
+#pragma unroll
+                for (int i = 0; i < step; ++i) {
+                    const int r = r0 + i * rpq + sub;
+                    // bf16 to f16 under a power of two for the row: its largest element goes to [2^14, 2^15),
+                    // so that only what is 2^-28 of it or less loses bits
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    float x[8], top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[2 * j] = bf16_lo(u[j]);
+                        x[2 * j + 1] = bf16_hi(u[j]);
+                        const float m0 = fabsf(x[2 * j]), m1 = fabsf(x[2 * j + 1]);
+                        top = m0 < __uint_as_float(0x7F800000u) ? fmaxf(top, m0) : top;
+                        top = m1 < __uint_as_float(0x7F800000u) ? fmaxf(top, m1) : top;
+                    }
+#pragma unroll
+                    for (int o = qc / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;  // x / 2^e
+                    e = max(-126, min(113, top == 0.f ? 0 : e));
+                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+                    w[i] = make_uint4(f16x2(x[0] * f, x[1] * f), f16x2(x[2] * f, x[3] * f), f16x2(x[4] * f, x[5] * f),
+                                      f16x2(x[6] * f, x[7] * f));
+                    if (piece == 0) arow[r] = k2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                    sts16(q_at + r * 128 + ((piece ^ r) & 7) * 16, w[i]);
+                }
+            }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + si % QB);
+            done_seg(si);
+        }
     } else if (warp == kSegWarp) {
         // ============================================================ segments
         Walk<N> walk(a, u0, u1, b0, base0);
@@ -609,23 +778,39 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         }
         }
     } else {
-        if constexpr (!Q8) more_regs<88>();
+        more_regs<Q8 ? 80 : 88>();
         // ============================================================ softmax
         // Thread = one position of the tile; group gr has the 8-row pieces gr,
-        // gr + 4, ... of the query rows. A weight is 2^(score - m) with m the
-        // row's running maximum, which may lag by kGrow: rescaling is rare.
+        // gr + 4, ... of the query rows. A weight is 2^(score - m) with m a
+        // reference that starts as the row's maximum in its first tile and moves
+        // only when a later score passes it by 2^grow: a weight in bf16 parts or
+        // float32 sums may be that large (2^60), one in f16 less (2^8).
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
-        constexpr bool kKeep = MC <= 2;  // few pieces: the scores stay in registers between the two looks at them
+        constexpr float grow = Q8 ? 8.f : 60.f;
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t o_at = tmem + 2 * N + lanes;
         unsigned char* const pw = p_sm + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
-        // the group's scratch [5][MC * 8]: its own, or its second part of P while P is free
-        float* const red = (float*)(Q8 ? red_sm + gr * X::red_bytes : p_sm + (N / 8 + (gr < N / 8 ? gr : 0)) * 2048);
+        // the group's scratch [5][MC * 8]: its own, or in its second part of P while P is free
+        float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
         const float k2 = a.scale * kLog2e;
         const float none = __uint_as_float(0xFF800000u);
-        uint32_t gt = 0;
+        auto larger = [](float x, float y) { return x > y || x != x ? x : y; };  // a NaN wins
+        // eight values of each lane to one: lane's value (lane >> 2) over the warp, by halving what a lane holds
+        auto over_warp = [&](float (&x)[8], auto op) {
+#pragma unroll
+            for (int h = 4; h; h >>= 1) {
+                const bool hi = lane & (4 * h);
+#pragma unroll
+                for (int k = 0; k < h; ++k)
+                    x[k] = op(hi ? x[k + h] : x[k], __shfl_xor_sync(0xFFFFFFFFu, hi ? x[k] : x[k + h], 4 * h));
+            }
+            x[0] = op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 2));
+            return op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 1));
+        };
+        uint32_t gt = 0, vs_slot = 0, vs_round = 0;
+        int32_t anc_of = -1;  // the sequence whose ancestors are known
         for (uint32_t si = 0;; ++si) {
             const Seg* const g = get_seg(si);
             const int n = g->n;
@@ -634,97 +819,53 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             const int32_t rows = min(N, T * a.G - row0);
             const int pieces = (rows + 7) / 8;
             const int live = gr < pieces ? (pieces - gr + kGroups - 1) / kGroups : 0;  // this group's pieces
-            // ---- the queries, and per-row state. Q is free: every product
-            // with the last segment's queries has been waited for.
-            {
-                constexpr int qc = DP / 8;  // 16-byte pieces of a row
-                constexpr int loads = (N * qc + kSoftThreads - 1) / kSoftThreads;
-                uint4 w[loads];
-#pragma unroll
-                for (int i = 0; i < loads; ++i) {
-                    const int r = (tid + i * kSoftThreads) / qc, piece = tid % qc;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows && piece * 8 < c.D) {
-                        const int32_t rr = row0 + r, t = rr / a.G;
-                        w[i] = *(const uint4*)(a.q + (g->lo + t) * a.q_row_bytes +
-                                               ((int64_t)g->h * a.G + (rr - t * a.G)) * c.D * 2 + piece * 16);
+            const float* const arow = arow_all + (si % R) * N;
+            // ---- per-row state
+            if (tid < N) mref[tid] = kNoMax;
+            if (tid < 4) poison[tid] = 0;
+            if (a.parent && g->b != anc_of) {
+                anc_of = g->b;
+                // ancestors by doubling: after k rounds a token knows those up to 2^k - 1 above it
+                int32_t jump = -1;
+                bool bad = false;
+                uint32_t m[4] = {0, 0, 0, 0};
+                uint32_t* const jumps = (uint32_t*)p_sm;  // P is free between segments
+                if (tid < kKvMaxQueries) {
+                    if (tid < T) {
+                        jump = a.parent[g->lo + tid];
+                        bad = tid == 0 ? jump != -1 : (jump < 0 || jump >= tid);
+                        if (bad) jump = -1;
+                        m[tid >> 5] = 1u << (tid & 31);
                     }
+                    *(uint4*)(anc + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
+                    jumps[tid] = (uint32_t)jump;
                 }
-#pragma unroll
-                for (int i = 0; i < loads; ++i) {
-                    const int r = (tid + i * kSoftThreads) / qc, piece = tid % qc;
-                    if (Q8) {
-                        // bf16 to f16 under a power of two for the row: its largest element goes to [2^14, 2^15),
-                        // so that only what is 2^-28 of it or less loses bits
-                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                        float x[8], top = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[2 * j] = bf16_lo(u[j]);
-                            x[2 * j + 1] = bf16_hi(u[j]);
-                            const float m0 = fabsf(x[2 * j]), m1 = fabsf(x[2 * j + 1]);
-                            top = m0 < __uint_as_float(0x7F800000u) ? fmaxf(top, m0) : top;
-                            top = m1 < __uint_as_float(0x7F800000u) ? fmaxf(top, m1) : top;
-                        }
-#pragma unroll
-                        for (int o = qc / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                        int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;  // x / 2^e
-                        e = max(-126, min(113, top == 0.f ? 0 : e));
-                        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                        w[i] = make_uint4(f16x2(x[0] * f, x[1] * f), f16x2(x[2] * f, x[3] * f), f16x2(x[4] * f, x[5] * f),
-                                          f16x2(x[6] * f, x[7] * f));
-                        if (piece == 0 && r < N) arow[r] = k2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                const bool any = bar_or(bar_all, kSoftThreads, bad);
+                if (tid == 0) *tree_bad = any;
+                for (int reach = 1; reach < T; reach <<= 1) {
+                    uint4 up = make_uint4(0, 0, 0, 0);
+                    int32_t far = -1;
+                    if (jump >= 0) {
+                        up = *(const uint4*)(anc + jump * 4);
+                        far = (int32_t)jumps[jump];
                     }
-                    if (r < N) sts16(smem_addr(q_sm) + (piece >> 3) * (N * 128) + r * 128 + ((piece ^ r) & 7) * 16, w[i]);
-                }
-                if (tid < N) mref[tid] = kNoMax;
-                if (tid < 4) poison[tid] = 0;
-                if (a.parent) {
-                    // ancestors by doubling: after k rounds a token knows those up to 2^k - 1 above it
-                    int32_t jump = -1;
-                    bool bad = false;
-                    uint32_t m[4] = {0, 0, 0, 0};
-                    uint32_t* const jumps = (uint32_t*)p_sm;  // P is free between segments
-                    if (tid < kKvMaxQueries) {
-                        if (tid < T) {
-                            jump = a.parent[g->lo + tid];
-                            bad = tid == 0 ? jump != -1 : (jump < 0 || jump >= tid);
-                            if (bad) jump = -1;
-                            m[tid >> 5] = 1u << (tid & 31);
-                        }
+                    bar_sync(bar_all, kSoftThreads);
+                    if (jump >= 0) {
+                        m[0] |= up.x, m[1] |= up.y, m[2] |= up.z, m[3] |= up.w;
                         *(uint4*)(anc + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
-                        jumps[tid] = (uint32_t)jump;
+                        jumps[tid] = (uint32_t)far;
                     }
-                    const bool any = bar_or(bar_all, kSoftThreads, bad);
-                    if (tid == 0) *tree_bad = any;
-                    for (int reach = 1; reach < T; reach <<= 1) {
-                        uint4 up = make_uint4(0, 0, 0, 0);
-                        int32_t far = -1;
-                        if (jump >= 0) {
-                            up = *(const uint4*)(anc + jump * 4);
-                            far = (int32_t)jumps[jump];
-                        }
-                        bar_sync(bar_all, kSoftThreads);
-                        if (jump >= 0) {
-                            m[0] |= up.x, m[1] |= up.y, m[2] |= up.z, m[3] |= up.w;
-                            *(uint4*)(anc + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
-                            jumps[tid] = (uint32_t)far;
-                        }
-                        jump = far;
-                        bar_sync(bar_all, kSoftThreads);
-                    }
-                } else {
+                    jump = far;
                     bar_sync(bar_all, kSoftThreads);
                 }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+            } else {
+                bar_sync(bar_all, kSoftThreads);
             }
-            float l[MC][8];
+            float2 l[MC][4];
 #pragma unroll
             for (int m = 0; m < MC; ++m)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) l[m][k] = 0.f;
+                for (int k = 0; k < 4; ++k) l[m][k] = make_float2(0.f, 0.f);
             int32_t lv = -100;  // Q8: values count in units of 2^lv
 
             for (int i = 0; i < n; ++i) {
@@ -736,7 +877,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     const float ks = Q8 ? ((const float*)(aux + 16))[wt] : 1.f;
                     const float vs = Q8 ? ((const float*)(aux + 16))[kTileTok + wt] : 1.f;
                     const int32_t pos0 = (g->tile0 + i) * kTileTok, pos = pos0 + wt;
-                    const uint32_t s_at = tmem + buf * N + lanes;
+                    const uint32_t s_at = tmem + buf * N + lanes + gr * 8;
                     const bool tail = pos0 + kTileTok > ctx;
                     // rows that see this position (a bit for each of the group's rows), where not every row sees
                     // every one; a page outside the pool hides positions anywhere
@@ -745,67 +886,46 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         const int32_t u = pos - ctx;
                         vis = 0;
 #pragma unroll 1
-                        for (int m = 0; m < live; ++m)
+                        for (int m = 0; m < live; ++m) {
+                            int32_t tk = (row0 + (gr + kGroups * m) * 8) / a.G;
+                            int32_t left = (tk + 1) * a.G - (row0 + (gr + kGroups * m) * 8);  // rows of token tk from here
 #pragma unroll 1
                             for (int k = 0; k < 8; ++k) {
-                                const int32_t tk = (row0 + (gr + kGroups * m) * 8 + k) / a.G;
                                 const bool see = a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u;
                                 vis |= (uint32_t)see << (m * 8 + k);
+                                if (--left == 0) left = a.G, ++tk;
                             }
+                        }
                     }
                     const bool masked = tail || __any_sync(0xFFFFFFFFu, !in);
                     wait(s_full + buf, (t >> 1) & 1);
                     tc_after();
 
-                    // scores of piece m relative to the running maximum, in units of log2
-                    auto relative = [&](int m, float (&z)[8], bool from_zero) {
+                    // scores of piece m less the reference, in units of log2
+                    auto relative = [&](int m, float2 (&z)[4], bool from_zero) {
                         const int r = (gr + kGroups * m) * 8;
-                        float f[8], x[8];
-                        *(float4*)x = *(const float4*)(mref + r);
-                        *(float4*)(x + 4) = *(const float4*)(mref + r + 4);
+                        const float4 m0 = *(const float4*)(mref + r), m1 = *(const float4*)(mref + r + 4);
+                        float2 x[4] = {{-m0.x, -m0.y}, {-m0.z, -m0.w}, {-m1.x, -m1.y}, {-m1.z, -m1.w}};
+                        if (from_zero) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
                         if (Q8) {
-                            *(float4*)f = *(const float4*)(arow + r);
-                            *(float4*)(f + 4) = *(const float4*)(arow + r + 4);
-                        }
+                            const float4 a0 = *(const float4*)(arow + r), a1 = *(const float4*)(arow + r + 4);
+                            const float2 f[4] = {{a0.x, a0.y}, {a0.z, a0.w}, {a1.x, a1.y}, {a1.z, a1.w}};
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) z[k] = fmaf(z[k], Q8 ? f[k] * ks : k2, from_zero ? 0.f : -x[k]);
+                            for (int k = 0; k < 4; ++k) z[k] = fma2(z[k], mul2(f[k], make_float2(ks, ks)), x[k]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k] = fma2(z[k], make_float2(k2, k2), x[k]);
+                        }
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) z[k] = (vis >> (m * 8 + k) & 1) ? z[k] : none;
+                            for (int k = 0; k < 4; ++k) {
+                                z[k].x = (vis >> (m * 8 + 2 * k) & 1) ? z[k].x : none;
+                                z[k].y = (vis >> (m * 8 + 2 * k + 1) & 1) ? z[k].y : none;
+                            }
                         }
                     };
-                    float zk[kKeep ? MC : 1][8];
-                    float top = none;
-                    if constexpr (kKeep) {
-#pragma unroll
-                        for (int m = 0; m < MC; ++m)
-                            if (m < live) tc_ld8(s_at + (gr + kGroups * m) * 8, zk[m]);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int m = 0; m < MC; ++m)
-                            if (m < live) {
-                                relative(m, zk[m], false);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) top = fmaxf(top, zk[m][k]);
-                            }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < MC; ++m)
-                            if (m < live) {
-                                float z[8];
-                                tc_ld8(s_at + (gr + kGroups * m) * 8, z);
-                                tc_wait_ld();
-                                relative(m, z, false);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) top = fmaxf(top, z[k]);
-                            }
-                    }
-                    const float v_unit = Q8 ? __uint_as_float((uint32_t)(lv + 127) << 23) : 0.f;
-                    const bool rise = top > kGrow || i == 0 || (Q8 && fabsf(vs) > v_unit);
-                    const bool slow = bar_or(bar_gr, 128, rise);
-                    if (t) wait(pv_done, (t - 1) & 1);  // P and O are free
-                    tc_after();
-                    if (slow) {
+                    // the references to the maxima of this tile and before, the sums after them
+                    auto refer = [&]() {
                         int32_t up = 0;
                         if (Q8) {
                             // the smallest 2^lv that no scale passes
@@ -816,17 +936,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
-                            float z[8];
-                            tc_ld8(s_at + (gr + kGroups * m) * 8, z);
+                            float2 z[4];
+                            tc_ld8(s_at + kGroups * m * 8, z);
                             tc_wait_ld();
                             relative(m, z, true);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                int32_t x = __float_as_int(z[k]);
-                                x ^= (x >> 31) & 0x7FFFFFFF;  // the order of the floats as integers
-                                x = __reduce_max_sync(0xFFFFFFFFu, x);
-                                if (lane == 0) red[wq * MC * 8 + m * 8 + k] = __int_as_float(x ^ ((x >> 31) & 0x7FFFFFFF));
-                            }
+                            float y[8] = {z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y};
+                            const float x = over_warp(y, larger);
+                            if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = x;
                         }
                         bar_sync(bar_gr, 128);
                         if (Q8) {
@@ -838,25 +954,23 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                             const float old = mref[r];
                             float m = old;
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const float x = red[w * MC * 8 + wt];
-                                m = x > m || x != x ? x : m;
-                            }
+                            for (int w = 0; w < 4; ++w) m = larger(red[w * MC * 8 + wt], m);
                             red[4 * MC * 8 + wt] = ex2(old - m);
                             mref[r] = m;
                         }
                         bar_sync(bar_gr, 128);
                         lv += up;
-                        const float shrink = Q8 ? (up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23)) : 1.f;
-#pragma unroll
-                        for (int m = 0; m < MC; ++m)
-                            if (m < live)
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) l[m][k] *= red[4 * MC * 8 + m * 8 + k];
                         if (i > 0) {
+                            const float shrink = Q8 ? (up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23)) : 1.f;
+#pragma unroll
+                            for (int m = 0; m < MC; ++m)
+                                if (m < live)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        l[m][k] = mul2(l[m][k], *(const float2*)(red + 4 * MC * 8 + m * 8 + 2 * k));
 #pragma unroll 1
                             for (int m = 0; m < live; ++m)
-#pragma unroll
+#pragma unroll 1
                                 for (int part = 0; part < (Q8 ? 1 : 2); ++part) {
                                     float o[8];
                                     const uint32_t at = o_at + part * N + (gr + kGroups * m) * 8;
@@ -869,64 +983,83 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                             tc_wait_st();
                         }
                         bar_sync(bar_gr, 128);  // the scratch may be P again
-                        if constexpr (kKeep) {
+                    };
+                    if (t) wait(pv_done, (t - 1) & 1);  // P and O are free
+                    tc_after();
+                    if (i == 0) refer();
+                    // ---- weights. When a score passes the reference by too much, they leave the row sums again
+                    // (exactly enough: what rounding leaves behind is within an ulp of that score's weight), the
+                    // reference moves, and they are made anew.
+                    for (float sign = 1.f;;) {
+                        float top = none;
+                        // Q8: f16 in units that bring the largest possible one, 2^grow, to 2^14
+                        const float wv = Q8 ? vs * __uint_as_float((uint32_t)(127 + 6 - lv) << 23) : 1.f;
+                        float2 zb[2][4];
+                        tc_ld8(s_at, zb[0]);
 #pragma unroll
-                            for (int m = 0; m < MC; ++m)
-                                if (m < live) tc_ld8(s_at + (gr + kGroups * m) * 8, zk[m]);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int m = 0; m < MC; ++m)
-                                if (m < live) relative(m, zk[m], false);
-                        }
-                    }
-                    // ---- weights
-                    // Q8: f16 in units that bring the largest possible one, 2^kGrow, to 2^14
-                    const float wv = Q8 ? vs * __uint_as_float((uint32_t)(127 + 6 - lv) << 23) : 1.f;
-#pragma unroll
-                    for (int m = 0; m < MC; ++m) {
-                        if (m < live) {
-                            float z[8];
-                            if constexpr (kKeep) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) z[k] = zk[m][k];
-                            } else {
-                                tc_ld8(s_at + (gr + kGroups * m) * 8, z);
+                        for (int m = 0; m < MC; ++m) {
+                            if (m < live) {
+                                float2(&z)[4] = zb[m & 1];
                                 tc_wait_ld();
+                                if (m + 1 < MC && m + 1 < live) tc_ld8(s_at + kGroups * (m + 1) * 8, zb[(m + 1) & 1]);
                                 relative(m, z, false);
-                            }
+                                float high = max3(z[0].x, z[0].y, z[1].x);
+                                high = max3(high, z[1].y, z[2].x);
+                                high = max3(high, z[2].y, z[3].x);
+                                high = fmaxf(high, z[3].y);
+                                top = fmaxf(top, high);
+                                if (__any_sync(0xFFFFFFFFu, high > grow))  // sums stay finite until the reference moves
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                z[k] = ex2(z[k]);
-                                l[m][k] += z[k];
-                            }
-                            const int piece = gr + kGroups * m;
-                            uint4 w;
-                            if (Q8) {
+                                    for (int k = 0; k < 4; ++k)
+                                        z[k] = make_float2(min_nan(z[k].x, grow), min_nan(z[k].y, grow));
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) z[k] *= wv;
-                                if (masked) {
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) z[k] = (vis >> (m * 8 + k) & 1) ? z[k] : 0.f;
+                                for (int k = 0; k < 4; ++k) {
+                                    z[k] = make_float2(ex2(z[k].x), ex2(z[k].y));
+                                    l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
                                 }
-                                w = make_uint4(f16x2(z[0], z[1]), f16x2(z[2], z[3]), f16x2(z[4], z[5]), f16x2(z[6], z[7]));
-                                *(uint4*)(pw + piece * 2048) = w;
-                            } else {
-                                // two bf16 parts: 16 bits of the weight
-                                w = make_uint4(bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7]));
-                                *(uint4*)(pw + piece * 2048) = w;
-                                w = make_uint4(bf16x2(z[0] - bf16_lo(w.x), z[1] - bf16_hi(w.x)),
-                                               bf16x2(z[2] - bf16_lo(w.y), z[3] - bf16_hi(w.y)),
-                                               bf16x2(z[4] - bf16_lo(w.z), z[5] - bf16_hi(w.z)),
-                                               bf16x2(z[6] - bf16_lo(w.w), z[7] - bf16_hi(w.w)));
-                                *(uint4*)(pw + (N / 8 + piece) * 2048) = w;
+                                const int piece = gr + kGroups * m;
+                                if (Q8) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
+                                    if (masked) {
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k) {
+                                            z[k].x = (vis >> (m * 8 + 2 * k) & 1) ? z[k].x : 0.f;
+                                            z[k].y = (vis >> (m * 8 + 2 * k + 1) & 1) ? z[k].y : 0.f;
+                                        }
+                                    }
+                                    *(uint4*)(pw + piece * 2048) = make_uint4(f16x2(z[0].x, z[0].y), f16x2(z[1].x, z[1].y),
+                                                                              f16x2(z[2].x, z[2].y), f16x2(z[3].x, z[3].y));
+                                } else {
+                                    // two bf16 parts: 16 bits of the weight
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        w[k] = bf16x2(z[k].x, z[k].y);
+                                        z[k] = sub2(z[k], make_float2(bf16_lo(w[k]), bf16_hi(w[k])));
+                                    }
+                                    *(uint4*)(pw + piece * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+                                    *(uint4*)(pw + (N / 8 + piece) * 2048) =
+                                        make_uint4(bf16x2(z[0].x, z[0].y), bf16x2(z[1].x, z[1].y), bf16x2(z[2].x, z[2].y),
+                                                   bf16x2(z[3].x, z[3].y));
+                                }
                             }
                         }
+                        if (sign < 0.f) {
+                            bar_sync(bar_gr, 128);
+                            refer();
+                            sign = 1.f;
+                            continue;
+                        }
+                        const float v_unit = Q8 ? __uint_as_float((uint32_t)(lv + 127) << 23) : 0.f;
+                        if (i == 0 || !bar_or(bar_gr, 128, top > grow || (Q8 && fabsf(vs) > v_unit && lv < 126))) break;
+                        sign = -1.f;
                     }
                     if (tail && gr == 0 && in && pos >= ctx && T > 1) {
                         // A new token's values that are not finite would reach rows that do not see it (0 * inf):
                         // they leave the tile here and join the rows that do see it at the end.
-                        wait(full + S + t % S, (t / S) & 1);
-                        unsigned char* const v_row = smem + (S + t % S) * X::slot_bytes + wt * 128;
+                        wait(v_full + vs_slot, vs_round & 1);
+                        unsigned char* const v_row = v_sm + vs_slot * X::slot_bytes + wt * 128;
                         constexpr uint32_t ex = Q8 ? 0x7C00u : 0x7F80u;
                         bool found = false;
 #pragma unroll 1
@@ -957,6 +1090,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     mbar_arrive(s_empty + buf);
                     mbar_arrive(p_full);
                 }
+                if (++vs_slot == SV) vs_slot = 0, ++vs_round;
             }
             gt += n;
 
@@ -968,26 +1102,15 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 const int32_t rr = row0 + r, tk = rr / a.G;
                 return (g->lo + tk) * a.Hq + (int64_t)g->h * a.G + (rr - tk * a.G);
             };
-            wait(pv_done, (gt - 1) & 1);
-            tc_after();
+            if (X::tight) wait(pv_done, (gt - 1) & 1);
             if (live) {
                 // each row's weights over the 128 positions: a warp's 32 by halving the rows a lane holds
 #pragma unroll
                 for (int m = 0; m < MC; ++m)
                     if (m < live) {
-                        float x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = l[m][k];
-#pragma unroll
-                        for (int h = 4; h; h >>= 1) {
-                            const bool hi = lane & (4 * h);
-#pragma unroll
-                            for (int k = 0; k < h; ++k)
-                                x[k] = (hi ? x[k + h] : x[k]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? x[k] : x[k + h], 4 * h);
-                        }
-                        x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 2);
-                        x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
-                        if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = x[0];
+                        float x[8] = {l[m][0].x, l[m][0].y, l[m][1].x, l[m][1].y, l[m][2].x, l[m][2].y, l[m][3].x, l[m][3].y};
+                        const float sum = over_warp(x, [](float u, float v) { return u + v; });
+                        if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = sum;
                     }
                 bar_sync(bar_gr, 128);
                 if (wt < live * 8) {
@@ -1002,6 +1125,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     }
                 }
                 bar_sync(bar_gr, 128);
+                if (!X::tight) wait(pv_done, (gt - 1) & 1);
+                tc_after();
                 const float back = Q8 ? __uint_as_float((uint32_t)(127 + lv) << 23) * 0.015625f : 1.f;
                 const bool any_poison = poison[0] | poison[1] | poison[2] | poison[3];
 #pragma unroll 1
