@@ -14,6 +14,8 @@
 // their order.
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 #include "kv.cuh"
 
@@ -39,7 +41,7 @@ constexpr int kAttMaxGrid = 160;  // CTAs (the workspace holds two parts for eac
 namespace {
 
 constexpr int kTileTok = 128;   // positions of a tile
-constexpr int kGroups = 4;      // softmax groups of four warps; a group takes every fourth 8 query rows
+constexpr int kGroups = 4;      // softmax groups of four warps
 constexpr int kSoftWarps = 4 * kGroups;
 constexpr int kFeedWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
@@ -49,8 +51,6 @@ constexpr int kQueryWarp = kStatusWarp + 1;
 constexpr int kAttThreads = (kQueryWarp + 1) * 32;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 3;                  // tiles of the K ring, and of the V ring
-constexpr int kRawTiles = 3;                  // e4m3 tiles under way as they are
-constexpr int kAuxRing = 8;                   // tiles of masks and scales kept: more than the ring and S can hold
 constexpr uint64_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
 constexpr float kNoMax = -1.0e30f;            // running maximum before any score
 constexpr size_t kSmemMax = 232448;
@@ -59,6 +59,13 @@ constexpr size_t kSmemMax = 232448;
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// One lane of the warp, the same each time. The warps that issue products run whole, so that descriptors and addresses
+// stay in uniform registers: with one lane's own registers an issue took about 160 cycles.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
@@ -98,7 +105,16 @@ __device__ __forceinline__ void tc_st8(uint32_t at, const float (&x)[8]) {
                  "r"(__float_as_uint(x[6])), "r"(__float_as_uint(x[7]))
                  : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads before it are done; their registers pass through it, so that no use of them moves ahead.
+__device__ __forceinline__ void tc_wait_ld(float (&x)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7])::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld(float2 (&x)[4]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0].x), "+f"(x[0].y), "+f"(x[1].x), "+f"(x[1].y), "+f"(x[2].x), "+f"(x[2].y), "+f"(x[3].x),
+                   "+f"(x[3].y)::"memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // This group of four warps goes on with R registers a thread.
 template <int R>
@@ -142,6 +158,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint4 w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
     float r;
@@ -190,34 +215,46 @@ struct __align__(16) Seg {
 template <int NN, int DP, bool Q8>
 struct Shape {
     static constexpr int N = NN;                           // query rows of a row tile
-    static constexpr int MC = (N / 8 + kGroups - 1) / kGroups;  // 8-row pieces of a softmax group
+    static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory and TMEM are full
+    // Teams of softmax groups take the tiles in turn, each with sums of its own, so that a tile may take a team as
+    // long as `TM` tiles take the loads; the groups of a team share the rows.
+    static constexpr int TM = N <= 32 ? 4 : N == 48 || (Q8 && N == 80) ? 2 : 1;
+    static constexpr int GT = kGroups / TM;                // groups of a team
+    static constexpr int SB = TM == 1 ? 2 : TM;            // score tiles in TMEM
+    static constexpr int MC = (N / 8 + GT - 1) / GT;       // 8-row pieces of a group
     static constexpr int NP = Q8 ? N : 2 * N;              // P's columns: one f16, or two bf16 parts
+    static constexpr int O_at = SB * N, K_at = O_at + TM * NP, columns = K_at + (Q8 ? DP : 0);  // TMEM
     static constexpr int QB = N == 128 || (Q8 && N == 80) ? 1 : 2;  // row tiles of queries held
-    static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory is full: rings of two
     static constexpr int segs = tight ? 2 : 4;             // segments known ahead
     static constexpr int ring_bars = tight ? 8 : 4 * kMaxSlots;  // full and empty, K and V
     static constexpr uint32_t slot_bytes = kTileTok * DP * 2;
-    static constexpr uint32_t raw_bytes = Q8 ? 2 * (N == 128 ? 2 : kRawTiles) * kTileTok * DP : 0;
-    static constexpr int raw_tiles = N == 128 ? 2 : kRawTiles;
+    static constexpr int RK = N == 32 || N >= 80 ? 2 : 3, RV = N == 128 ? 2 : 3;  // e4m3 tiles as they are
+    static constexpr uint32_t raw_bytes = Q8 ? (RK + RV) * kTileTok * DP : 0;
     static constexpr uint32_t q_bytes = N * DP * 2;
-    static constexpr uint32_t p_bytes = NP * kTileTok * 2;
+    static constexpr uint32_t p_bytes = NP * kTileTok * 2;      // of a team
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
+    static constexpr int aux_ring = Q8 && TM == 4 ? 16 : 8;     // tiles of them: more than rings and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
-    // after the tiles, Q and P: aux ring, running maxima, row factors, scratch, ancestors, segments, poison, barriers
-    static constexpr uint32_t misc = kAuxRing * aux_bytes + N * 4 + (Q8 ? segs * N * 4 : 0) + (tight ? 0 : kGroups * red_bytes) +
-                                     kKvMaxQueries * 16 + segs * sizeof(Seg) + 32 +
-                                     (ring_bars + 11 + kAuxRing + 2 * segs) * 8;
-    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - p_bytes - misc) / slot_bytes);
+    // after the tiles, Q and P: aux ring, per team and row the reference, weight sum and factor, row factors of Q,
+    // scratch, ancestors, segments, poison, barriers
+    static constexpr uint32_t state = tight ? N * 4 : 3 * TM * N * 4;
+    static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
+                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 32 : 48) +
+                                     (ring_bars + 2 * SB + 2 * TM + 5 + aux_ring + 2 * segs) * 8;
+    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - TM * p_bytes - misc) / slot_bytes);
     // tiles of the K ring (e4m3: in TMEM) and of the V ring; a V tile is held longer
     static constexpr int SK = Q8 ? 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
     static constexpr int rest = Q8 ? fit : fit - SK;
     static constexpr int SV = rest > kMaxSlots ? kMaxSlots : rest;
     static constexpr uint32_t ring_bytes = (Q8 ? SV : SK + SV) * slot_bytes;
-    static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + p_bytes + misc;
+    static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + TM * p_bytes + misc;
     static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
-    static_assert(2 * (SK + SV) <= ring_bars && total <= kSmemMax, "shared memory");
+    static_assert(2 * (SK + SV) <= ring_bars && total <= kSmemMax && columns <= 512, "memory");
+    // a tile's masks and scales are written while those of the last SK + SB tiles (and, e4m3, those loaded ahead) may
+    // be in use
+    static_assert(aux_ring > SK + SB + (Q8 ? RK - 1 : 0), "aux ring");
     // the feed may wait for a new segment with this many tiles, each a segment, not handed over
-    static_assert(segs > (Q8 ? raw_tiles - 1 : SV - 1), "the oldest known segment must be whole in the ring");
+    static_assert(segs > (Q8 ? RV : SV) - 1 && segs > (Q8 ? RK : SK) - 1, "the oldest known segment must be whole in the ring");
 };
 
 template <int N>
@@ -267,33 +304,37 @@ struct Walk {
 template <int NN, int DP, bool Q8>
 __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using X = Shape<NN, DP, Q8>;
-    constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB;
+    constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, kAuxRing = X::aux_ring;
     constexpr uint32_t SK = X::SK, SV = X::SV;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const v_sm = smem + (Q8 ? 0 : SK * X::slot_bytes);  // the V ring; the K ring, if any, is before it
-    unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [2][raw_tiles] K and V tiles as they are
+    unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [RK] K and [RV] V tiles as they are
     unsigned char* const q_sm = raw_sm + X::raw_bytes;
-    unsigned char* const p_sm = q_sm + QB * X::q_bytes;
-    unsigned char* const aux_sm = p_sm + X::p_bytes;
-    float* const mref = (float*)(aux_sm + kAuxRing * X::aux_bytes);
-    float* const arow_all = mref + N;  // Q8: [R][N] a query row's power of two times scale * log2(e)
-    unsigned char* const red_sm = (unsigned char*)(mref + (Q8 ? (1 + R) * N : N));
+    unsigned char* const p_sm = q_sm + QB * X::q_bytes;                // [TM]
+    unsigned char* const aux_sm = p_sm + TM * X::p_bytes;
+    float* const mref_all = (float*)(aux_sm + kAuxRing * X::aux_bytes);  // [TM][N] references
+    // [TM][N] each: weight sums and factors of the teams, used between segments (tight: in P, free then)
+    float* const lsum = X::tight ? (float*)(p_sm + (N / 8 + 4) * 2048) : mref_all + TM * N;
+    float* const fac = lsum + TM * N;
+    float* const arow_all = mref_all + X::state / 4;  // Q8: [R][N] a query row's power of two times scale * log2(e)
+    unsigned char* const red_sm = (unsigned char*)(arow_all + (Q8 ? R * N : 0));
     uint32_t* const anc = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] ancestors of a tree's tokens
     Seg* const segs = (Seg*)(anc + kKvMaxQueries * 4);
-    uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then 4 words:
+    uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then 8 words:
     volatile uint32_t* const aborted = poison + 4;   // a wait gave up
     uint32_t* const tmem_at = poison + 5;
     uint32_t* const last_in = poison + 6;
     uint32_t* const tree_bad = poison + 7;
-    uint64_t* const k_full = (uint64_t*)(poison + 8);
+    float* const unit_of = (float*)(poison + 8);     // [kGroups] Q8: what a group's sums count in
+    uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 8 : 12));
     uint64_t* const v_full = k_full + SK;
     uint64_t* const k_empty = v_full + SV;
     uint64_t* const v_empty = k_empty + SK;
     uint64_t* const s_full = v_empty + SV;
-    uint64_t* const s_empty = s_full + 2;
-    uint64_t* const p_full = s_empty + 2;
-    uint64_t* const pv_done = p_full + 1;
-    uint64_t* const drain = pv_done + 1;
+    uint64_t* const s_empty = s_full + SB;
+    uint64_t* const p_full = s_empty + SB;
+    uint64_t* const pv_done = p_full + TM;
+    uint64_t* const drain = pv_done + TM;
     uint64_t* const q_full = drain + 1;
     uint64_t* const q_empty = q_full + 2;
     uint64_t* const aux_full = q_empty + 2;
@@ -302,7 +343,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 
     const KvAttend& a = p.a;
     const KvView& c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return;
@@ -314,9 +355,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         } while (nanoseconds() - t0 < kAttWaitNs);
         *aborted = 1;
     };
-    // Segment s of this CTA, by every warp that works on it; next_seg gives its place back.
+    // Once a wait has given up, every wait but those for segments returns at once, so that all roles run out in
+    // step: the same segments, the same named barriers, whatever the data.
+    auto wait_seg = [&](uint64_t* bar, uint32_t parity) {
+        const uint64_t t0 = nanoseconds();
+        while (!mbar_try_wait(bar, parity) && nanoseconds() - t0 < 8 * kAttWaitNs) {
+        }
+    };
+    // Segment s of this CTA, by every warp that works on it; done_seg gives its place back.
     auto get_seg = [&](uint32_t s) {
-        wait(seg_full + s % R, (s / R) & 1);
+        wait_seg(seg_full + s % R, (s / R) & 1);
         return segs + s % R;
     };
     auto done_seg = [&](uint32_t s) {
@@ -334,14 +382,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             mbar_init(v_full + i, kFeedWarps / 2);
             mbar_init(v_empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SB; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(s_empty + i, kSoftWarps);
+            mbar_init(s_empty + i, 4 * X::GT);
+        }
+        for (int i = 0; i < TM; ++i) {
+            mbar_init(p_full + i, 4 * X::GT);
+            mbar_init(pv_done + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
         }
-        mbar_init(p_full, kSoftWarps);
-        mbar_init(pv_done, 1);
         mbar_init(drain, 1);
         for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, kFeedWarps / 2);
         for (int i = 0; i < R; ++i) {
@@ -399,7 +451,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     tc_after();
     const int32_t b0 = u0 < u1 ? (int32_t)scan[32] : 0;
     const int64_t base0 = u0 < u1 ? scan[33] : 0;
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);
     __syncthreads();  // P's memory is P's from here on
 
     // The block starts with 72 registers a thread, 7 groups of four warps. bf16: softmax 88 (4 groups), feed 48 (2),
@@ -440,6 +492,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         const int32_t* table = nullptr;
         int64_t head = 0, sc_head = 0;
         auto page_at = [&](int32_t at) { return at < L ? table[at / c.bs] : -1; };
+        // Whether the next tile is known without a wait. Before a wait for a segment, every tile loaded so far is
+        // handed over: the segment may not come before they have been used.
+        auto known = [&]() { return t < n || mbar_test(seg_full + si % R, (si / R) & 1); };
         // opens the next segment when this one is through; false: no more
         auto more = [&]() {
             if (t < n) return true;
@@ -479,8 +534,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(my_full + slot);
             };
             const uint32_t S = is_k ? SK : SV, lag = S - 1;  // copies of `lag` tiles are under way when one is handed over
-            uint32_t slot = 0, round = 0, out = 0;           // out: slot of the next tile to hand over
-            while (more()) {
+            uint32_t slot = 0, round = 0;
+            uint32_t out = 0, held = 0;  // slot of the next tile to hand over, tiles not handed over
+            auto flush = [&]() {
+                cp_wait<0>();
+                for (; held; --held) {
+                    publish(out);
+                    if (++out == S) out = 0;
+                }
+            };
+            for (;;) {
+                if (held && __any_sync(0xFFFFFFFFu, !known())) flush();
+                if (!more()) break;
                 const int64_t off = row();
                 if (round) wait(my_empty + slot, (round - 1) & 1);
                 if (is_k) {
@@ -498,70 +563,72 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     cp16(swizzled(base, r, 0), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
                 }
                 cp_commit();
-                if (kt >= lag) {
+                if (++held > lag) {
                     if (lag == 1)
                         cp_wait<1>();
                     else
                         cp_wait<2>();
                     publish(out);
                     if (++out == S) out = 0;
+                    --held;
                 }
                 ++kt;
                 if (++slot == S) slot = 0, ++round;
             }
-            cp_wait<0>();
-            for (uint32_t i = kt > lag ? lag : kt; i; --i) {
-                publish(out);
-                if (++out == S) out = 0;
-            }
+            flush();
         } else {
-            constexpr int RT = X::raw_tiles, ahead = RT - 1;
+            const int RT = is_k ? X::RK : X::RV;
             // a warp's own rows, 16-byte units exchanged so that a column of them lies in different banks
-            const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : RT * kTileTok * DP) + fw * 32 * DP;
+            const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : X::RK * kTileTok * DP) + fw * 32 * DP;
             auto raw_at = [&](int tile, int r, int u) {
                 return raw + tile * (kTileTok * DP) + r * DP + ((u ^ (DP == 128 ? r & 7 : (r >> 1) & 3)) * 16);
             };
-            bool open = true;
             int in = 0;  // raw place of the next tile loaded
             auto load = [&]() {
-                open = open && more();
-                if (open) {
-                    const int64_t off = row();
+                const int64_t off = row();
 #pragma unroll
-                    for (int r = 0; r < chunks; ++r) {
-                        const int rr = r * rpr + my_row;
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
-                        const bool live = o >= 0 && chunk_in;
-                        cp16(raw_at(in, rr, my_chunk), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
-                    }
-                    if (is_k) {
-                        unsigned char* const at = aux_of(kt);
-                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
-                        if (lane == 0) ((uint32_t*)at)[fw] = bits;
-                        const uint32_t sc = smem_addr(at + 16) + (fw * 32 + lane) * 4;
-                        cp4(sc, off >= 0 ? c.ks + sc_at : c.ks, off >= 0 ? 4u : 0u);
-                        cp4(sc + kTileTok * 4, off >= 0 ? c.vs + sc_at : c.vs, off >= 0 ? 4u : 0u);
-                    }
-                    ++kt;
-                    if (++in == RT) in = 0;
+                for (int r = 0; r < chunks; ++r) {
+                    const int rr = r * rpr + my_row;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
+                    const bool live = o >= 0 && chunk_in;
+                    cp16(raw_at(in, rr, my_chunk), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
+                }
+                if (is_k) {
+                    unsigned char* const at = aux_of(kt);
+                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
+                    if (lane == 0) ((uint32_t*)at)[fw] = bits;
+                    const uint32_t sc = smem_addr(at + 16) + (fw * 32 + lane) * 4;
+                    cp4(sc, off >= 0 ? c.ks + sc_at : c.ks, off >= 0 ? 4u : 0u);
+                    cp4(sc + kTileTok * 4, off >= 0 ? c.vs + sc_at : c.vs, off >= 0 ? 4u : 0u);
                 }
                 cp_commit();
+                ++kt;
+                if (++in == RT) in = 0;
             };
-#pragma unroll
-            for (int i = 0; i < ahead; ++i) load();
             const uint32_t S = is_k ? SK : SV;
             uint32_t slot = 0, round = 0;
             int from = 0;  // raw place of the next tile turned
             for (uint32_t done = 0;; ++done) {
-                load();
-                if (done == kt) break;
-                cp_wait<ahead>();
+                // load as far ahead as there is room; wait for a segment only with nothing left to turn
+#pragma unroll 1
+                while (kt - done < (uint32_t)RT) {
+                    if (kt != done && __any_sync(0xFFFFFFFFu, !known())) break;
+                    if (!more()) break;
+                    load();
+                }
+                if (kt == done) break;
+                if (kt - done == 1)
+                    cp_wait<0>();
+                else if (kt - done == 2)
+                    cp_wait<1>();
+                else
+                    cp_wait<2>();
                 __syncwarp();
                 if (round) wait(my_empty + slot, (round - 1) & 1);
                 if (is_k) {
                     // lane = row = TMEM lane: two elements to a column
                     tc_after();
-                    const uint32_t at = tmem + 2 * N + X::NP + slot * (DP / 2) + ((uint32_t)fw << 21);
+                    const uint32_t at = tmem + X::K_at + slot * (DP / 2) + ((uint32_t)fw << 21);
 #pragma unroll
                     for (int u = 0; u < DP / 16; ++u) {
                         const uint4 w = lds16(raw_at(from, lane, u));
@@ -602,53 +669,73 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         const uint64_t k_desc = operand(smem_addr(smem), 16, 1024, 2);
         const uint64_t v_desc = operand(smem_addr(v_sm), DP == 128 ? kTileTok * 128 : 0, 1024, 2);
         const uint64_t p_desc = operand(smem_addr(p_sm), 128, 2048, 0);
-        uint32_t gt = 0, ks = 0, kr = 0, vs = 0, vr = 0;  // ring places and rounds
-        for (uint32_t si = 0;; ++si) {
-            const int n = get_seg(si)->n;
-            if (!n) break;
-            if (lane == 0) {
-                const uint32_t qb = si % QB;
-                const uint64_t q_desc = operand(smem_addr(q_sm + qb * X::q_bytes), 16, 1024, 2);
-                wait(q_full + qb, (si / QB) & 1);
-                auto scores = [&](int i) {
-                    const uint32_t t = gt + i, buf = t & 1;
-                    wait(k_full + ks, kr & 1);
-                    if (t >= 2) wait(s_empty + buf, ((t >> 1) - 1) & 1);
-                    tc_after();
-                    const uint64_t ka = k_desc + ks * (X::slot_bytes >> 4);
-                    const uint32_t kt = tmem + 2 * N + X::NP + ks * (DP / 2);
+        const uint64_t q_desc = operand(smem_addr(q_sm), 16, 1024, 2);
+        // Scores run ahead of the weights' products, over segments' ends too, as far as there is room in TMEM: two
+        // cursors over the segments.
+        uint32_t qs = 0, qt = 0, ks = 0, kr = 0, vs = 0, vr = 0;  // segment, tile, ring places and rounds
+        int qi = 0, qn = -1;
+        auto count_of = [&](uint32_t seg) { return __shfl_sync(0xFFFFFFFFu, get_seg(seg)->n, 0); };
+        auto scores = [&]() {  // of the next tile, if there is one
+            if (qn == 0) return;
+            if (qi >= qn) {
+                qn = count_of(qs);
+                if (!qn) return;
+                qi = 0;
+                wait(q_full + qs % QB, (qs / QB) & 1);
+            }
+            const uint32_t buf = qt % SB;
+            wait(k_full + ks, kr & 1);
+            if (qt >= SB) wait(s_empty + buf, (qt / SB - 1) & 1);
+            tc_after();
+            ++qi;
+            if (elect()) {
+                const uint64_t ka = k_desc + ks * (X::slot_bytes >> 4);
+                const uint64_t qd = q_desc + (qs % QB) * (X::q_bytes >> 4);
+                const uint32_t kt = tmem + X::K_at + ks * (DP / 2), d = tmem + buf * N;
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint64_t qd = q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4);
-                        if constexpr (Q8)
-                            tc_mma_ts(tmem + buf * N, kt + k * 8, qd, id_qk, k > 0);
-                        else
-                            tc_mma(tmem + buf * N, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4), qd, id_qk, k > 0);
-                    }
-                    tc_commit(k_empty + ks);
-                    tc_commit(s_full + buf);
-                    if (i + 1 == n) tc_commit(q_empty + qb);
-                    if (++ks == SK) ks = 0, ++kr;
-                };
-                scores(0);
-                for (int i = 0; i < n; ++i) {
-                    if (i + 1 < n) scores(i + 1);
-                    wait(v_full + vs, vr & 1);
-                    wait(p_full, (gt + i) & 1);
-                    tc_after();
-                    const uint64_t va = v_desc + vs * (X::slot_bytes >> 4);
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint64_t qk = qd + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4);
+                    if constexpr (Q8)
+                        tc_mma_ts(d, kt + k * 8, qk, id_qk, k > 0);
+                    else
+                        tc_mma(d, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4), qk, id_qk, k > 0);
+                }
+                tc_commit(k_empty + ks);
+                tc_commit(s_full + buf);
+                if (qi == qn) tc_commit(q_empty + qs % QB);
+            }
+            __syncwarp();
+            if (qi == qn) ++qs;
+            ++qt;
+            if (++ks == SK) ks = 0, ++kr;
+        };
+        uint32_t t = 0;
+        for (int i = 0; i < TM; ++i) scores();
+        for (uint32_t si = 0;; ++si) {
+            const int n = count_of(si);
+            if (!n) break;
+            done_seg(si);  // at once: the cursor ahead, which has read it, may have to wait for its place
+            for (int i = 0; i < n; ++i, ++t) {
+                if (TM == 1) scores();
+                const uint32_t team = t % TM;
+                wait(v_full + vs, vr & 1);
+                wait(p_full + team, (t / TM) & 1);
+                tc_after();
+                if (elect()) {
+                    const uint64_t va = v_desc + vs * (X::slot_bytes >> 4), pd = p_desc + team * (X::p_bytes >> 4);
+                    const uint32_t d = tmem + X::O_at + team * X::NP;
 #pragma unroll
                     for (int k = 0; k < kTileTok / 16; ++k)
-                        tc_mma(tmem + 2 * N, va + ((k * 2048) >> 4), p_desc + ((k * 256) >> 4), id_pv, i > 0 || k > 0);
+                        tc_mma(d, va + ((k * 2048) >> 4), pd + ((k * 256) >> 4), id_pv, k > 0 || i >= TM);
                     tc_commit(v_empty + vs);
-                    tc_commit(pv_done);
-                    if (++vs == SV) vs = 0, ++vr;
+                    tc_commit(pv_done + team);
                 }
+                __syncwarp();
+                if (++vs == SV) vs = 0, ++vr;
+                if (TM > 1) scores();
             }
-            gt += n;
-            done_seg(si);
         }
-        if (lane == 0) {
+        if (elect()) {
             tc_commit(drain);  // everything issued here is done before TMEM is freed
             const uint64_t t0 = nanoseconds();
             while (!mbar_try_wait(drain, 0) && nanoseconds() - t0 < kAttWaitNs) {
@@ -734,7 +821,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         for (uint32_t s = 0;; ++s) {
             Seg g;
             walk.next(g);
-            if (s >= R) wait(seg_empty + s % R, (s / R - 1) & 1);
+            if (s >= R) wait_seg(seg_empty + s % R, (s / R - 1) & 1);
             if (lane == 0) {
                 segs[s % R] = g;
                 mbar_arrive(seg_full + s % R);
@@ -780,8 +867,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     } else {
         more_regs<Q8 ? 80 : 88>();
         // ============================================================ softmax
-        // Thread = one position of the tile; group gr has the 8-row pieces gr,
-        // gr + 4, ... of the query rows. A weight is 2^(score - m) with m a
+        // Thread = one position of the tile; group gr is of team gr % TM and has
+        // every GT-th 8-row piece of the query rows. A weight is 2^(score - m) with m a
         // reference that starts as the row's maximum in its first tile and moves
         // only when a later score passes it by 2^grow: a weight in bf16 parts or
         // float32 sums may be that large (2^60), one in f16 less (2^8).
@@ -790,8 +877,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         constexpr int bar_all = 1 + kGroups;
         constexpr float grow = Q8 ? 8.f : 60.f;
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
-        const uint32_t o_at = tmem + 2 * N + lanes;
-        unsigned char* const pw = p_sm + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
+        const uint32_t team = gr % TM, sub = gr / TM;
+        const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;
+        unsigned char* const pw = p_sm + team * X::p_bytes + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
+        float* const mref = mref_all + team * N;
         // the group's scratch [5][MC * 8]: its own, or in its second part of P while P is free
         float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
         const float k2 = a.scale * kLog2e;
@@ -809,7 +898,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             x[0] = op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 2));
             return op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 1));
         };
-        uint32_t gt = 0, vs_slot = 0, vs_round = 0;
+        uint32_t gt = 0;
         int32_t anc_of = -1;  // the sequence whose ancestors are known
         for (uint32_t si = 0;; ++si) {
             const Seg* const g = get_seg(si);
@@ -818,10 +907,11 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             const int32_t T = g->T, L = g->L, row0 = g->rt * N, ctx = L - T;
             const int32_t rows = min(N, T * a.G - row0);
             const int pieces = (rows + 7) / 8;
-            const int live = gr < pieces ? (pieces - gr + kGroups - 1) / kGroups : 0;  // this group's pieces
+            const int live = (int)sub < pieces ? (pieces - (int)sub + X::GT - 1) / X::GT : 0;  // this group's pieces
             const float* const arow = arow_all + (si % R) * N;
             // ---- per-row state
-            if (tid < N) mref[tid] = kNoMax;
+            if (tid < TM * N) mref_all[tid] = kNoMax;
+            if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
             if (tid < 4) poison[tid] = 0;
             if (a.parent && g->b != anc_of) {
                 anc_of = g->b;
@@ -868,8 +958,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 for (int k = 0; k < 4; ++k) l[m][k] = make_float2(0.f, 0.f);
             int32_t lv = -100;  // Q8: values count in units of 2^lv
 
-            for (int i = 0; i < n; ++i) {
-                const uint32_t t = gt + i, buf = t & 1;
+            const int first = (int)((team - gt) & (TM - 1));  // this team's first tile of the segment
+            for (int i = first; i < n; i += TM) {
+                const uint32_t t = gt + i, buf = t % SB, turn = t / TM;
                 if (live) {
                     wait(aux_full + t % kAuxRing, (t / kAuxRing) & 1);
                     const unsigned char* aux = aux_sm + (t % kAuxRing) * X::aux_bytes;
@@ -877,33 +968,35 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     const float ks = Q8 ? ((const float*)(aux + 16))[wt] : 1.f;
                     const float vs = Q8 ? ((const float*)(aux + 16))[kTileTok + wt] : 1.f;
                     const int32_t pos0 = (g->tile0 + i) * kTileTok, pos = pos0 + wt;
-                    const uint32_t s_at = tmem + buf * N + lanes + gr * 8;
+                    const uint32_t s_at = tmem + buf * N + lanes + sub * 8;
                     const bool tail = pos0 + kTileTok > ctx;
                     // rows that see this position (a bit for each of the group's rows), where not every row sees
                     // every one; a page outside the pool hides positions anywhere
-                    uint32_t vis = in ? ~0u : 0u;
+                    using Rows = typename std::conditional<(MC > 4), uint64_t, uint32_t>::type;  // a bit for each
+                    static_assert(MC * 8 <= 8 * (int)sizeof(Rows), "a bit for each row of the group");
+                    Rows vis = in ? ~(Rows)0 : (Rows)0;
                     if (tail && in && pos >= ctx) {
                         const int32_t u = pos - ctx;
                         vis = 0;
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
-                            int32_t tk = (row0 + (gr + kGroups * m) * 8) / a.G;
-                            int32_t left = (tk + 1) * a.G - (row0 + (gr + kGroups * m) * 8);  // rows of token tk from here
+                            int32_t tk = (row0 + (sub + X::GT * m) * 8) / a.G;
+                            int32_t left = (tk + 1) * a.G - (row0 + (sub + X::GT * m) * 8);  // rows of token tk from here
 #pragma unroll 1
                             for (int k = 0; k < 8; ++k) {
                                 const bool see = a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u;
-                                vis |= (uint32_t)see << (m * 8 + k);
+                                vis |= (Rows)see << (m * 8 + k);
                                 if (--left == 0) left = a.G, ++tk;
                             }
                         }
                     }
                     const bool masked = tail || __any_sync(0xFFFFFFFFu, !in);
-                    wait(s_full + buf, (t >> 1) & 1);
+                    wait(s_full + buf, (t / SB) & 1);
                     tc_after();
 
                     // scores of piece m less the reference, in units of log2
                     auto relative = [&](int m, float2 (&z)[4], bool from_zero) {
-                        const int r = (gr + kGroups * m) * 8;
+                        const int r = (sub + X::GT * m) * 8;
                         const float4 m0 = *(const float4*)(mref + r), m1 = *(const float4*)(mref + r + 4);
                         float2 x[4] = {{-m0.x, -m0.y}, {-m0.z, -m0.w}, {-m1.x, -m1.y}, {-m1.z, -m1.w}};
                         if (from_zero) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
@@ -937,8 +1030,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
                             float2 z[4];
-                            tc_ld8(s_at + kGroups * m * 8, z);
-                            tc_wait_ld();
+                            tc_ld8(s_at + X::GT * m * 8, z);
+                            tc_wait_ld(z);
                             relative(m, z, true);
                             float y[8] = {z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y};
                             const float x = over_warp(y, larger);
@@ -950,7 +1043,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                             up = min(126, max(lv, max(max(e[0], e[1]), max(e[2], e[3])))) - lv;
                         }
                         if (wt < live * 8) {
-                            const int r = (gr + kGroups * (wt >> 3)) * 8 + (wt & 7);
+                            const int r = (sub + X::GT * (wt >> 3)) * 8 + (wt & 7);
                             const float old = mref[r];
                             float m = old;
 #pragma unroll
@@ -960,7 +1053,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
                         bar_sync(bar_gr, 128);
                         lv += up;
-                        if (i > 0) {
+                        if (i != first) {
                             const float shrink = Q8 ? (up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23)) : 1.f;
 #pragma unroll
                             for (int m = 0; m < MC; ++m)
@@ -973,9 +1066,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll 1
                                 for (int part = 0; part < (Q8 ? 1 : 2); ++part) {
                                     float o[8];
-                                    const uint32_t at = o_at + part * N + (gr + kGroups * m) * 8;
+                                    const uint32_t at = o_at + part * N + (sub + X::GT * m) * 8;
                                     tc_ld8(at, o);
-                                    tc_wait_ld();
+                                    tc_wait_ld(o);
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) o[k] *= red[4 * MC * 8 + m * 8 + k] * shrink;
                                     tc_st8(at, o);
@@ -984,12 +1077,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
                         bar_sync(bar_gr, 128);  // the scratch may be P again
                     };
-                    if (t) wait(pv_done, (t - 1) & 1);  // P and O are free
+                    if (turn) wait(pv_done + team, (turn - 1) & 1);  // the team's P and O are free
                     tc_after();
-                    if (i == 0) refer();
+                    if (i == first) refer();
                     // ---- weights. When a score passes the reference by too much, they leave the row sums again
                     // (exactly enough: what rounding leaves behind is within an ulp of that score's weight), the
                     // reference moves, and they are made anew.
+                    bool moved = false;
                     for (float sign = 1.f;;) {
                         float top = none;
                         // Q8: f16 in units that bring the largest possible one, 2^grow, to 2^14
@@ -1000,24 +1094,23 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         for (int m = 0; m < MC; ++m) {
                             if (m < live) {
                                 float2(&z)[4] = zb[m & 1];
-                                tc_wait_ld();
-                                if (m + 1 < MC && m + 1 < live) tc_ld8(s_at + kGroups * (m + 1) * 8, zb[(m + 1) & 1]);
+                                tc_wait_ld(z);
+                                if (m + 1 < MC && m + 1 < live) tc_ld8(s_at + X::GT * (m + 1) * 8, zb[(m + 1) & 1]);
                                 relative(m, z, false);
                                 float high = max3(z[0].x, z[0].y, z[1].x);
                                 high = max3(high, z[1].y, z[2].x);
                                 high = max3(high, z[2].y, z[3].x);
                                 high = fmaxf(high, z[3].y);
                                 top = fmaxf(top, high);
-                                if (__any_sync(0xFFFFFFFFu, high > grow))  // sums stay finite until the reference moves
+                                // sums stay finite until the reference moves
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        z[k] = make_float2(min_nan(z[k].x, grow), min_nan(z[k].y, grow));
+                                for (int k = 0; k < 4; ++k) z[k] = make_float2(min_nan(z[k].x, grow), min_nan(z[k].y, grow));
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     z[k] = make_float2(ex2(z[k].x), ex2(z[k].y));
                                     l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
                                 }
-                                const int piece = gr + kGroups * m;
+                                const int piece = sub + X::GT * m;
                                 if (Q8) {
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
@@ -1048,18 +1141,20 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         if (sign < 0.f) {
                             bar_sync(bar_gr, 128);
                             refer();
+                            moved = true;
                             sign = 1.f;
                             continue;
                         }
                         const float v_unit = Q8 ? __uint_as_float((uint32_t)(lv + 127) << 23) : 0.f;
-                        if (i == 0 || !bar_or(bar_gr, 128, top > grow || (Q8 && fabsf(vs) > v_unit && lv < 126))) break;
+                        // (after a move nothing passes the reference, so that a second one is never due)
+                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || (Q8 && fabsf(vs) > v_unit && lv < 126))) break;
                         sign = -1.f;
                     }
-                    if (tail && gr == 0 && in && pos >= ctx && T > 1) {
+                    if (tail && sub == 0 && in && pos >= ctx && T > 1) {
                         // A new token's values that are not finite would reach rows that do not see it (0 * inf):
                         // they leave the tile here and join the rows that do see it at the end.
-                        wait(v_full + vs_slot, vs_round & 1);
-                        unsigned char* const v_row = v_sm + vs_slot * X::slot_bytes + wt * 128;
+                        wait(v_full + t % SV, (t / SV) & 1);
+                        unsigned char* const v_row = v_sm + t % SV * X::slot_bytes + wt * 128;
                         constexpr uint32_t ex = Q8 ? 0x7C00u : 0x7F80u;
                         bool found = false;
 #pragma unroll 1
@@ -1084,13 +1179,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 __syncwarp();
                 if (lane == 0) {
                     if (!live) {  // in step with the tiles: one arrival in each phase
-                        wait(s_full + buf, (t >> 1) & 1);
-                        if (t) wait(pv_done, (t - 1) & 1);
+                        wait(s_full + buf, (t / SB) & 1);
+                        if (turn) wait(pv_done + team, (turn - 1) & 1);
                     }
                     mbar_arrive(s_empty + buf);
-                    mbar_arrive(p_full);
+                    mbar_arrive(p_full + team);
                 }
-                if (++vs_slot == SV) vs_slot = 0, ++vs_round;
             }
             gt += n;
 
@@ -1102,8 +1196,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 const int32_t rr = row0 + r, tk = rr / a.G;
                 return (g->lo + tk) * a.Hq + (int64_t)g->h * a.G + (rr - tk * a.G);
             };
-            if (X::tight) wait(pv_done, (gt - 1) & 1);
-            if (live) {
+            // the last product of a team with a tile here
+            auto finished = [&](uint32_t tm) {
+                const int f = (int)((tm - (gt - n)) & (TM - 1));
+                if (f < n) wait(pv_done + tm, ((gt - n + f + (n - 1 - f) / TM * TM) / TM) & 1);
+                return f < n;
+            };
+            if (X::tight) finished(0);  // the scratch is P's
+            if (live && first < n) {
                 // each row's weights over the 128 positions: a warp's 32 by halving the rows a lane holds
 #pragma unroll
                 for (int m = 0; m < MC; ++m)
@@ -1113,71 +1213,86 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = sum;
                     }
                 bar_sync(bar_gr, 128);
-                if (wt < live * 8) {
-                    const float sum = red[wt] + red[MC * 8 + wt] + red[2 * MC * 8 + wt] + red[3 * MC * 8 + wt];
-                    const int r = (gr + kGroups * (wt >> 3)) * 8 + (wt & 7);
-                    red[4 * MC * 8 + wt] = sum == 0.f ? 0.f : 1.f / sum;
-                    if (r < rows) {
-                        if (!whole)
-                            p.part_ml[part * N + r] = make_float2(mref[r], sum);
-                        else if (a.lse && !skip)
-                            a.lse[out_row(r)] = sum == 0.f ? none : (mref[r] + log2f(sum)) * 0.69314718055994531f;
-                    }
+                if (wt < live * 8)
+                    lsum[team * N + (sub + X::GT * (wt >> 3)) * 8 + (wt & 7)] =
+                        red[wt] + red[MC * 8 + wt] + red[2 * MC * 8 + wt] + red[3 * MC * 8 + wt];
+                if (Q8 && wt == 0) unit_of[gr] = __uint_as_float((uint32_t)(127 + lv) << 23) * 0.015625f;
+            }
+            bar_sync(bar_all, kSoftThreads);
+            if (tid < rows) {
+                float M = mref_all[tid];
+#pragma unroll
+                for (int tm = 1; tm < TM; ++tm) M = larger(mref_all[tm * N + tid], M);
+                float sum = 0.f, f[TM];
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm) {
+                    f[tm] = ex2(mref_all[tm * N + tid] - M);
+                    sum = fmaf(f[tm], lsum[tm * N + tid], sum);
                 }
-                bar_sync(bar_gr, 128);
-                if (!X::tight) wait(pv_done, (gt - 1) & 1);
-                tc_after();
-                const float back = Q8 ? __uint_as_float((uint32_t)(127 + lv) << 23) * 0.015625f : 1.f;
-                const bool any_poison = poison[0] | poison[1] | poison[2] | poison[3];
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm)
+                    fac[tm * N + tid] = f[tm] * (whole ? inv : 1.f) * (Q8 ? unit_of[tm + TM * ((tid >> 3) % X::GT)] : 1.f);
+                if (!whole)
+                    p.part_ml[part * N + tid] = make_float2(M, sum);
+                else if (a.lse && !skip)
+                    a.lse[out_row(tid)] = sum == 0.f ? none : (M + log2f(sum)) * 0.69314718055994531f;
+            }
+            bool has[TM];
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) has[tm] = finished(tm);
+            tc_after();
+            bar_sync(bar_all, kSoftThreads);
+            const bool any_poison = poison[0] | poison[1] | poison[2] | poison[3];
 #pragma unroll 1
-                for (int m = 0; m < live; ++m) {
-                    const int piece = gr + kGroups * m, r0 = piece * 8;
-                    float o[8];
-                    tc_ld8(o_at + r0, o);
-                    if constexpr (!Q8) {
-                        float lo[8];
-                        tc_ld8(o_at + N + r0, lo);
-                        tc_wait_ld();
+            for (int piece = gr; piece < pieces; piece += kGroups) {
+                const int r0 = piece * 8;
+                float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] += lo[k];
-                    } else {
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] *= back;
-                    }
-                    if (any_poison && wt < c.D) {
-#pragma unroll 1
-                        for (int32_t u = 0; u < T; ++u) {
-                            if (!(poison[u >> 5] >> (u & 31) & 1)) continue;
-                            const int32_t pos = ctx + u;
-                            const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + pos / c.bs], sl = pos % c.bs;
-                            const unsigned char* v = c.v + pg * c.block_bytes + sl * c.token_bytes + g->h * c.head_bytes;
-                            const float x = Q8 ? kv_e4m3(v[wt]) : bf16_lo(*(const uint16_t*)(v + 2 * wt));
-                            if (fabsf(x) < __uint_as_float(0x7F800000u)) continue;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int32_t tk = (row0 + r0 + k) / a.G;
-                                if (a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u) o[k] += x;
-                            }
-                        }
-                    }
-                    if (whole) {
-                        // through shared memory (this piece's own P) to 16-byte stores
-                        uint16_t* const st = (uint16_t*)(p_sm + piece * 2048);
+                for (int tm = 0; tm < TM; ++tm)
+                    if (has[tm]) {
+                        float x[8], y[8];
+                        const uint32_t at = tmem + X::O_at + lanes + tm * X::NP + r0;
+                        tc_ld8(at, x);
+                        if (!Q8) tc_ld8(at + N, y);
+                        tc_wait_ld(x);
+                        if (!Q8) tc_wait_ld(y);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float f = red[4 * MC * 8 + m * 8 + k];
-                            st[k * 128 + wt] = (uint16_t)bf16x2(f == 0.f ? 0.f : o[k] * f, 0.f);
+                            const float f = fac[tm * N + r0 + k];
+                            if (!Q8) x[k] += y[k];
+                            o[k] = f == 0.f ? o[k] : fmaf(f, x[k], o[k]);
                         }
-                        bar_sync(bar_gr, 128);
-                        const int k = wt >> 4, ch = wt & 15;
-                        if (r0 + k < rows && ch * 8 < c.D && !skip)
-                            *(uint4*)(a.out + (out_row(r0 + k) * c.D + ch * 8) * 2) = *(const uint4*)(st + k * 128 + ch * 8);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (r0 + k < rows) p.part_o[(part * N + r0 + k) * 128 + wt] = o[k];
                     }
+                if (any_poison && wt < c.D) {
+#pragma unroll 1
+                    for (int32_t u = 0; u < T; ++u) {
+                        if (!(poison[u >> 5] >> (u & 31) & 1)) continue;
+                        const int32_t pos = ctx + u;
+                        const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + pos / c.bs], sl = pos % c.bs;
+                        const unsigned char* v = c.v + pg * c.block_bytes + sl * c.token_bytes + g->h * c.head_bytes;
+                        const float x = Q8 ? kv_e4m3(v[wt]) : bf16_lo(*(const uint16_t*)(v + 2 * wt));
+                        if (fabsf(x) < __uint_as_float(0x7F800000u)) continue;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int32_t tk = (row0 + r0 + k) / a.G;
+                            if (a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u) o[k] += x;
+                        }
+                    }
+                }
+                if (whole) {
+                    // through shared memory (the piece's own P) to 16-byte stores
+                    uint16_t* const st = (uint16_t*)(p_sm + piece * 2048);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) st[k * 128 + wt] = (uint16_t)bf16x2(o[k], 0.f);
+                    bar_sync(bar_gr, 128);
+                    const int k = wt >> 4, ch = wt & 15;
+                    if (r0 + k < rows && ch * 8 < c.D && !skip)
+                        *(uint4*)(a.out + (out_row(r0 + k) * c.D + ch * 8) * 2) = *(const uint4*)(st + k * 128 + ch * 8);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (r0 + k < rows) p.part_o[(part * N + r0 + k) * 128 + wt] = o[k];
                 }
             }
             if (!whole) {

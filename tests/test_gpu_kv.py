@@ -265,6 +265,20 @@ def test_attend_many_tiles_to_a_processor(sv, dtype, G, D, t):
     lens = [int(x) for x in np.random.default_rng(3).integers(t, 1500, 24)]
     c = Case(lens=lens, tokens=[max(1, t - b % 3) for b in range(24)], H=8, G=G, D=D, dtype=dtype, q_scale=2.0)
     c.attend(sv)
+    assert c.status.tolist() == [0] * c.B
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,D,t", [(1, 128, 1), (2, 64, 9), (4, 128, 9), (8, 128, 9), (4, 128, 29)])
+def test_attend_many_short_sequences(sv, dtype, G, D, t):
+    """Many sequences of a tile or less, so that each processor has more entries than tiles in flight; some empty."""
+    B = 300
+    tokens = [0 if b % 7 == 3 else 1 + (b * 5) % t for b in range(B)]
+    lens = [max(tokens[b], (b * 37) % 150) for b in range(B)]
+    c = Case(lens=lens, tokens=tokens, H=4, G=G, D=D, dtype=dtype, q_scale=2.0)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * c.B
     c.check()
 
 
