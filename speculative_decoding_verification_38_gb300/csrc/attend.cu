@@ -20,6 +20,40 @@ int tile_rows(int64_t rows) {
 
 constexpr size_t kPartAlign = 256;
 
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder, looked up once (the library does not link the driver).
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void* at = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            at = nullptr;
+        return (EncodeTiled)at;
+    }();
+    return f;
+}
+
+// One layer of K or V as (elements, slots, heads, pages), read in boxes of 128
+// bytes of a row (past head_dim: zeros) by `box` slots.
+cudaError_t box_map(CUtensorMap& m, const KvView& c, void* base, int32_t box) {
+    const EncodeTiled f = encoder();
+    if (!f) return cudaErrorNotSupported;
+    const bool q8 = c.esz == 1;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.bs, (cuuint64_t)c.H, (cuuint64_t)c.num_blocks};
+    // an axis of one element is never stepped along, but its stride must pass the encoder
+    auto stride = [&](int64_t bytes, cuuint64_t n) { return (cuuint64_t)(n > 1 ? bytes : 16); };
+    const cuuint64_t strides[3] = {stride(c.token_bytes, dims[1]), stride(c.head_bytes, dims[2]),
+                                   stride(c.block_bytes, dims[3])};
+    const cuuint32_t boxes[4] = {q8 ? 128u : 64u, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r =
+        f(&m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes, steps,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 bool attend_takes(int32_t head_dim) { return head_dim <= 128; }
@@ -43,6 +77,11 @@ cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
     AttParams p;
     p.a = a;
     p.grid = grid;
+    p.box = 1;
+    p.box_log = 0;
+    while (p.box < kTileTok && a.c.bs % (2 * p.box) == 0) p.box *= 2, ++p.box_log;
+    if ((e = box_map(p.k_map, a.c, a.c.k, p.box)) != cudaSuccess) return e;
+    if ((e = box_map(p.v_map, a.c, a.c.v, p.box)) != cudaSuccess) return e;
     const int n = tile_rows((int64_t)a.t_max * a.G);
     char* ws = (char*)workspace;
     p.arrive = (uint32_t*)ws;

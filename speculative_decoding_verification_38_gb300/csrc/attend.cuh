@@ -14,6 +14,8 @@
 // their order.
 #pragma once
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "internal.h"
@@ -22,7 +24,9 @@
 namespace specv {
 
 struct AttParams {
+    CUtensorMap k_map, v_map;  // boxes of `box` slots of a page's head
     KvAttend a;
+    int32_t box, box_log;  // the largest power of two that divides a page and a tile
     float* part_o;     // [grid * 2][N][128] partial sums
     float2* part_ml;   // [grid * 2][N] their maxima (log2) and weights' sums
     uint32_t* arrive;  // [grid] parts arrived, zero between calls
@@ -43,15 +47,14 @@ namespace {
 constexpr int kTileTok = 128;   // positions of a tile
 constexpr int kGroups = 4;      // softmax groups of four warps
 constexpr int kSoftWarps = 4 * kGroups;
-constexpr int kFeedWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
-constexpr int kSegWarp = kMmaWarp + 1;
-constexpr int kStatusWarp = kSegWarp + 1;
-constexpr int kQueryWarp = kStatusWarp + 1;
-constexpr int kAttThreads = (kQueryWarp + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps;      // issues the products
+constexpr int kSegWarp = kMmaWarp + 1;    // makes the segments, loads K
+constexpr int kValueWarp = kSegWarp + 1;  // loads V, checks the sequences
+constexpr int kQueryWarp = kValueWarp + 1;
+constexpr int kTurnWarp = kQueryWarp + 1; // e4m3: four warps turn K tiles to f16, four V tiles
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kMaxSlots = 3;                  // tiles of the K ring, and of the V ring
-constexpr uint64_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
+constexpr int kMaxSlots = 4;                  // tiles of the K ring, and of the V ring
+constexpr uint32_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
 constexpr float kNoMax = -1.0e30f;            // running maximum before any score
 constexpr size_t kSmemMax = 232448;
 
@@ -125,9 +128,9 @@ template <int R>
 __device__ __forceinline__ void fewer_regs() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-__device__ __forceinline__ uint64_t nanoseconds() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+__device__ __forceinline__ uint32_t nanoseconds() {  // of a clock that comes round every 4.3 s
+    uint32_t t;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
     return t;
 }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -143,14 +146,16 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// A box of the cache (elements, slots, head, page) into shared memory; past the pool or head_dim: zeros.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t e, int32_t slot, int32_t head,
+                                        int32_t page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(e), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
 }
-template <int K>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(K) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 w;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
@@ -158,15 +163,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint4 w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
     float r;
@@ -226,21 +222,22 @@ struct Shape {
     static constexpr int O_at = SB * N, K_at = O_at + TM * NP, columns = K_at + (Q8 ? DP : 0);  // TMEM
     static constexpr int QB = N == 128 || (Q8 && N == 80) ? 1 : 2;  // row tiles of queries held
     static constexpr int segs = tight ? 2 : 4;             // segments known ahead
-    static constexpr int ring_bars = tight ? 8 : 4 * kMaxSlots;  // full and empty, K and V
+    static constexpr int threads = (kTurnWarp + (Q8 ? 8 : 0)) * 32;
     static constexpr uint32_t slot_bytes = kTileTok * DP * 2;
     static constexpr int RK = N == 32 || N >= 80 ? 2 : 3, RV = N == 128 ? 2 : 3;  // e4m3 tiles as they are
-    static constexpr uint32_t raw_bytes = Q8 ? (RK + RV) * kTileTok * DP : 0;
+    static constexpr uint32_t raw_bytes = Q8 ? (RK + RV) * kTileTok * 128 : 0;  // rows of 128 bytes, whatever DP
     static constexpr uint32_t q_bytes = N * DP * 2;
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;      // of a team
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
-    static constexpr int aux_ring = Q8 && TM == 4 ? 16 : 8;     // tiles of them: more than rings and scores can hold
+    static constexpr int aux_ring = TM == 4 ? 16 : 8;           // tiles of them: more than the K ring and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
     // after the tiles, Q and P: aux ring, per team and row the reference, weight sum and factor, row factors of Q,
     // scratch, ancestors, segments, poison, barriers
     static constexpr uint32_t state = tight ? N * 4 : 3 * TM * N * 4;
     static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
-                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 32 : 48) +
-                                     (ring_bars + 2 * SB + 2 * TM + 5 + aux_ring + 2 * segs) * 8;
+                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 64) +
+                                     (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * (RK + RV) : 0)) * 8 +
+                                     (2 * SB + 2 * TM + 5 + aux_ring + 2 * segs) * 8;
     static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - TM * p_bytes - misc) / slot_bytes);
     // tiles of the K ring (e4m3: in TMEM) and of the V ring; a V tile is held longer
     static constexpr int SK = Q8 ? 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
@@ -249,12 +246,9 @@ struct Shape {
     static constexpr uint32_t ring_bytes = (Q8 ? SV : SK + SV) * slot_bytes;
     static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + TM * p_bytes + misc;
     static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
-    static_assert(2 * (SK + SV) <= ring_bars && total <= kSmemMax && columns <= 512, "memory");
-    // a tile's masks and scales are written while those of the last SK + SB tiles (and, e4m3, those loaded ahead) may
-    // be in use
-    static_assert(aux_ring > SK + SB + (Q8 ? RK - 1 : 0), "aux ring");
-    // the feed may wait for a new segment with this many tiles, each a segment, not handed over
-    static_assert(segs > (Q8 ? RV : SV) - 1 && segs > (Q8 ? RK : SK) - 1, "the oldest known segment must be whole in the ring");
+    static_assert(2 * (SK + SV) <= (tight ? 8 : 4 * kMaxSlots) && total <= kSmemMax && columns <= 512, "memory");
+    // a tile's masks and scales are written while those of the last SK + SB tiles may be in use
+    static_assert(aux_ring > SK + SB, "aux ring");
 };
 
 template <int N>
@@ -302,10 +296,11 @@ struct Walk {
 };
 
 template <int NN, int DP, bool Q8>
-__global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
+__global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using X = Shape<NN, DP, Q8>;
     constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, kAuxRing = X::aux_ring;
-    constexpr uint32_t SK = X::SK, SV = X::SV;
+    constexpr uint32_t SK = X::SK, SV = X::SV, RK = X::RK, RV = X::RV;
+    constexpr int kAttThreads = X::threads;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const v_sm = smem + (Q8 ? 0 : SK * X::slot_bytes);  // the V ring; the K ring, if any, is before it
     unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [RK] K and [RV] V tiles as they are
@@ -320,13 +315,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     unsigned char* const red_sm = (unsigned char*)(arow_all + (Q8 ? R * N : 0));
     uint32_t* const anc = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] ancestors of a tree's tokens
     Seg* const segs = (Seg*)(anc + kKvMaxQueries * 4);
-    uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then 8 words:
+    uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then:
     volatile uint32_t* const aborted = poison + 4;   // a wait gave up
     uint32_t* const tmem_at = poison + 5;
     uint32_t* const last_in = poison + 6;
     uint32_t* const tree_bad = poison + 7;
-    float* const unit_of = (float*)(poison + 8);     // [kGroups] Q8: what a group's sums count in
-    uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 8 : 12));
+    uint32_t* const last_seq = poison + 8;           // the last sequence of the run
+    float* const unit_of = (float*)(poison + 12);    // [kGroups] Q8: what a group's sums count in
+    uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 10 : 16));
     uint64_t* const v_full = k_full + SK;
     uint64_t* const k_empty = v_full + SV;
     uint64_t* const v_empty = k_empty + SK;
@@ -340,6 +336,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     uint64_t* const aux_full = q_empty + 2;
     uint64_t* const seg_full = aux_full + kAuxRing;
     uint64_t* const seg_empty = seg_full + R;
+    uint64_t* const raw_full = seg_empty + R;       // Q8: [RK] of K, [RV] of V
+    uint64_t* const raw_empty = raw_full + RK + RV;
 
     const KvAttend& a = p.a;
     const KvView& c = a.c;
@@ -347,19 +345,19 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return;
-        const uint64_t t0 = nanoseconds();
-        do {
-            for (int i = 0; i < 16; ++i)
-                if (mbar_try_wait(bar, parity)) return;
+        const uint32_t t0 = nanoseconds();
+#pragma unroll 1
+        while (!mbar_try_wait(bar, parity)) {
             if (*aborted) return;
-        } while (nanoseconds() - t0 < kAttWaitNs);
-        *aborted = 1;
+            if (nanoseconds() - t0 > kAttWaitNs) *aborted = 1;
+        }
     };
     // Once a wait has given up, every wait but those for segments returns at once, so that all roles run out in
     // step: the same segments, the same named barriers, whatever the data.
     auto wait_seg = [&](uint64_t* bar, uint32_t parity) {
-        const uint64_t t0 = nanoseconds();
-        while (!mbar_try_wait(bar, parity) && nanoseconds() - t0 < 8 * kAttWaitNs) {
+        const uint32_t t0 = nanoseconds();
+#pragma unroll 1
+        while (!mbar_try_wait(bar, parity) && nanoseconds() - t0 < 2 * kAttWaitNs) {
         }
     };
     // Segment s of this CTA, by every warp that works on it; done_seg gives its place back.
@@ -375,13 +373,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     // ------------------------------------------------- this CTA's run of tiles
     if (tid == 0) {
         for (uint32_t i = 0; i < SK; ++i) {
-            mbar_init(k_full + i, kFeedWarps / 2);
+            mbar_init(k_full + i, Q8 ? 4 : 1);
             mbar_init(k_empty + i, 1);
         }
         for (uint32_t i = 0; i < SV; ++i) {
-            mbar_init(v_full + i, kFeedWarps / 2);
+            mbar_init(v_full + i, Q8 ? 4 : 1);
             mbar_init(v_empty + i, 1);
         }
+        if (Q8)
+            for (uint32_t i = 0; i < RK + RV; ++i) {
+                mbar_init(raw_full + i, 1);
+                mbar_init(raw_empty + i, 4);
+            }
         for (int i = 0; i < SB; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, 4 * X::GT);
@@ -395,10 +398,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             mbar_init(q_empty + i, 1);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, kFeedWarps / 2);
+        for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, Q8 ? 4 : 1);
         for (int i = 0; i < R; ++i) {
             mbar_init(seg_full + i, 1);
-            mbar_init(seg_empty + i, kSoftWarps + kFeedWarps + 2);
+            mbar_init(seg_empty + i, kSoftWarps + 3 + (Q8 ? 8 : 0));
         }
         *aborted = 0;
         fence_barrier_init();
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     const int32_t per_thr = (c.B + kAttThreads - 1) / kAttThreads;
     const int32_t bt0 = min(c.B, tid * per_thr), bt1 = min(c.B, bt0 + per_thr);
     int64_t mine = 0;
+#pragma unroll 1
     for (int32_t b = bt0; b < bt1; ++b) {
         KvSeq s;
         int32_t tiles, nrt;
@@ -424,6 +428,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int64_t before = 0, W = 0;
+#pragma unroll 1
     for (int w = 0; w < kAttThreads / 32; ++w) {
         const int64_t x = scan[w];
         before += w < warp ? x : 0;
@@ -434,6 +439,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(u0 + per, W);
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
         int64_t at = pre;
+#pragma unroll 1
         for (int32_t b = bt0; b < bt1; ++b) {
             KvSeq s;
             int32_t tiles, nrt;
@@ -454,184 +460,97 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);
     __syncthreads();  // P's memory is P's from here on
 
-    // The block starts with 72 registers a thread, 7 groups of four warps. bf16: softmax 88 (4 groups), feed 48 (2),
-    // the rest 56 (1); e4m3: 80, 64 and 56. Either adds up to 7 x 72.
-    if (warp >= kSoftWarps && warp < kMmaWarp) {
-        if constexpr (Q8)
-            fewer_regs<64>();
-        else
-            fewer_regs<48>();
-        // ============================================================ feed
-        // Four warps bring the K tiles, four the V tiles, 32 rows each (lane =
-        // row where an address is made), by cp.async. bf16: straight to the
-        // rings. e4m3: as they are to a warp's own place; from there, two tiles
-        // later, as f16 (exactly) to the V ring, or to TMEM as the product's
-        // first operand. Rows past the length, on a page outside the pool or
-        // past head_dim are zeros.
-        const bool is_k = warp < kSoftWarps + 4;
-        const int fw = warp & 3;
-        const unsigned char* const src = is_k ? c.k : c.v;
-        uint64_t* const my_full = is_k ? k_full : v_full;
-        uint64_t* const my_empty = is_k ? k_empty : v_empty;
-        constexpr int chunks = DP * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a padded row
-        constexpr int rpr = 32 / chunks;                // rows of one load of the warp
-        const int my_chunk = lane % chunks, my_row = lane / chunks;
-        const bool chunk_in = my_chunk * (Q8 ? 16 : 8) < c.D;
-        // Where this lane writes eight 16-bit elements of row `my_row + r * rpr` (r constant) in a ring tile: the
-        // swizzle exchanges 16-byte units within a row by its row's number, so the address is an exclusive or and an
-        // offset away from row my_row's.
-        const int unit = my_chunk * (Q8 ? 2 : 1);
-        const uint32_t at0 = smem_addr(is_k && !Q8 ? smem : v_sm) + fw * 32 * 128 + (unit >> 3) * (kTileTok * 128) +
-                             my_row * 128 + ((unit ^ my_row) & 7) * 16;
-        auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
-
-        // the walk over this CTA's tiles: page of the row at `pos` one tile ahead
-        uint32_t si = 0, kt = 0;  // segment, tiles loaded
-        int n = 0, t = 0;
-        int32_t L = 0, pos = 0, pg = -1;
-        const int32_t* table = nullptr;
-        int64_t head = 0, sc_head = 0;
-        auto page_at = [&](int32_t at) { return at < L ? table[at / c.bs] : -1; };
-        // Whether the next tile is known without a wait. Before a wait for a segment, every tile loaded so far is
-        // handed over: the segment may not come before they have been used.
-        auto known = [&]() { return t < n || mbar_test(seg_full + si % R, (si / R) & 1); };
-        // opens the next segment when this one is through; false: no more
-        auto more = [&]() {
-            if (t < n) return true;
-            const Seg* const g = get_seg(si);
-            n = g->n;
-            t = 0;
-            if (!n) return false;
-            L = g->L;
-            pos = g->tile0 * kTileTok + fw * 32 + lane;
-            table = c.table + (int64_t)g->b * c.max_blocks;
-            head = g->h * c.head_bytes;
-            sc_head = (int64_t)g->h * c.bs;
-            done_seg(si++);
-            pg = page_at(pos);
-            return true;
-        };
-        // this lane's row of the tile: its byte offset (-1: no row) and its scales'; on to the next tile
-        int64_t sc_at = 0;
-        auto row = [&]() {
-            int64_t o = -1;
-            if (pg >= 0 && pg < c.num_blocks) {
-                const int32_t sl = pos % c.bs;
-                o = pg * c.block_bytes + sl * c.token_bytes + head;
-                if (Q8) sc_at = (int64_t)pg * c.H * c.bs + sl + sc_head;
-            }
-            pos += kTileTok;
-            ++t;
-            pg = t < n ? page_at(pos) : -1;
-            return o;
-        };
-        auto aux_of = [&](uint32_t tile) { return aux_sm + (tile % kAuxRing) * X::aux_bytes; };
-
-        if constexpr (!Q8) {
-            auto publish = [&](uint32_t slot) {
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(my_full + slot);
-            };
-            const uint32_t S = is_k ? SK : SV, lag = S - 1;  // copies of `lag` tiles are under way when one is handed over
-            uint32_t slot = 0, round = 0;
-            uint32_t out = 0, held = 0;  // slot of the next tile to hand over, tiles not handed over
-            auto flush = [&]() {
-                cp_wait<0>();
-                for (; held; --held) {
-                    publish(out);
-                    if (++out == S) out = 0;
-                }
-            };
-            for (;;) {
-                if (held && __any_sync(0xFFFFFFFFu, !known())) flush();
-                if (!more()) break;
-                const int64_t off = row();
-                if (round) wait(my_empty + slot, (round - 1) & 1);
-                if (is_k) {
-                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
-                    if (lane == 0) {
-                        ((uint32_t*)aux_of(kt))[fw] = bits;
-                        mbar_arrive(aux_full + kt % kAuxRing);
-                    }
-                }
-                const uint32_t base = at0 + slot * X::slot_bytes;
-#pragma unroll
-                for (int r = 0; r < chunks; ++r) {
-                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r * rpr + my_row);
-                    const bool live = o >= 0 && chunk_in;
-                    cp16(swizzled(base, r, 0), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
-                }
-                cp_commit();
-                if (++held > lag) {
-                    if (lag == 1)
-                        cp_wait<1>();
-                    else
-                        cp_wait<2>();
-                    publish(out);
-                    if (++out == S) out = 0;
-                    --held;
-                }
-                ++kt;
-                if (++slot == S) slot = 0, ++round;
-            }
-            flush();
-        } else {
-            const int RT = is_k ? X::RK : X::RV;
-            // a warp's own rows, 16-byte units exchanged so that a column of them lies in different banks
-            const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : X::RK * kTileTok * DP) + fw * 32 * DP;
-            auto raw_at = [&](int tile, int r, int u) {
-                return raw + tile * (kTileTok * DP) + r * DP + ((u ^ (DP == 128 ? r & 7 : (r >> 1) & 3)) * 16);
-            };
-            int in = 0;  // raw place of the next tile loaded
-            auto load = [&]() {
-                const int64_t off = row();
-#pragma unroll
-                for (int r = 0; r < chunks; ++r) {
-                    const int rr = r * rpr + my_row;
-                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
-                    const bool live = o >= 0 && chunk_in;
-                    cp16(raw_at(in, rr, my_chunk), live ? src + o + my_chunk * 16 : src, live ? 16u : 0u);
-                }
-                if (is_k) {
-                    unsigned char* const at = aux_of(kt);
-                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, off >= 0);
-                    if (lane == 0) ((uint32_t*)at)[fw] = bits;
-                    const uint32_t sc = smem_addr(at + 16) + (fw * 32 + lane) * 4;
-                    cp4(sc, off >= 0 ? c.ks + sc_at : c.ks, off >= 0 ? 4u : 0u);
-                    cp4(sc + kTileTok * 4, off >= 0 ? c.vs + sc_at : c.vs, off >= 0 ? 4u : 0u);
-                }
-                cp_commit();
-                ++kt;
-                if (++in == RT) in = 0;
-            };
-            const uint32_t S = is_k ? SK : SV;
-            uint32_t slot = 0, round = 0;
-            int from = 0;  // raw place of the next tile turned
-            for (uint32_t done = 0;; ++done) {
-                // load as far ahead as there is room; wait for a segment only with nothing left to turn
+    // A tile's rows lie in boxes of p.box slots (a whole page's, for pages of 16 to 128). Lane j knows the page of box
+    // j; one lane issues the loads, in a loop of the whole warp. Past the length or on a page outside the pool the box
+    // is one past the pool: zeros. A page's slots past the length come as they are; softmax hides their scores and
+    // clears their values.
+    const int boxes = kTileTok >> p.box_log;
+    auto page_of = [&](const int32_t* table, int32_t pos, int32_t L) {
+        int32_t pg = -1;
+        if (pos < L) pg = table[c.by_bs.of(pos)];
+        return pg >= 0 && pg < c.num_blocks ? pg : c.num_blocks;
+    };
+    auto bring = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar, const int32_t* table, int32_t at, int32_t L,
+                     int32_t head, int32_t pages) {  // pages: of boxes 0 .. 31, a lane each
+        if (elect()) mbar_arrive_expect_tx(bar, kTileTok * (Q8 || DP == 64 ? 128 : 256));
+        __syncwarp();
+        int32_t sl = at - c.by_bs.of(at) * c.bs;
 #pragma unroll 1
-                while (kt - done < (uint32_t)RT) {
-                    if (kt != done && __any_sync(0xFFFFFFFFu, !known())) break;
-                    if (!more()) break;
-                    load();
+        for (int j = 0; j < boxes; ++j) {
+            if (j && (j & 31) == 0) pages = page_of(table, at + (j + lane) * p.box, L);
+            const int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, j & 31);
+            if (elect()) {
+                tma_box(dst, map, 0, sl, head, pg, bar);
+                if (!Q8 && DP == 128) tma_box(dst + kTileTok * 128, map, 64, sl, head, pg, bar);
+            }
+            dst += p.box * 128;
+            sl += p.box;
+            if (sl >= c.bs) sl = 0;
+        }
+        __syncwarp();
+    };
+    auto aux_of = [&](uint32_t tile) { return aux_sm + (tile % kAuxRing) * X::aux_bytes; };
+
+    // Registers by role. bf16: 5 groups of four warps start with 96 a thread; softmax (4 groups) goes on with 104, the
+    // rest with 64. e4m3: 7 groups with 72; softmax 80, the turning warps (2) 64, the rest 56.
+    if (Q8 && warp >= kTurnWarp) {
+        fewer_regs<64>();
+        // ============================================================ e4m3 to f16
+        // Exactly, 32 rows to a warp: V tiles from shared memory to the V ring, K tiles to TMEM as the scores' first
+        // operand (lane = row = TMEM lane, two elements to a column). The K warps also bring the tile's scales.
+        const bool is_k = warp < kTurnWarp + 4;
+        const int fw = warp & 3;
+        const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : RK * kTileTok * 128) + fw * 32 * 128;
+        // 16-byte unit u of row r, as the load exchanged them: a column of them lies in different banks
+        auto raw_at = [&](uint32_t tile, int r, int u) {
+            return raw + tile * (kTileTok * 128) + r * 128 + ((u ^ r) & 7) * 16;
+        };
+        constexpr int chunks = DP / 16, rpr = 32 / chunks;  // 16-byte units of a row, rows of a warp's access
+        const int my_chunk = lane % chunks, my_row = lane / chunks;
+        // where this lane's unit of row `my_row + r * rpr` goes in a V tile: an exclusive or and an offset away from
+        // row my_row's, as 16-byte units are exchanged within a row by its row's number
+        const uint32_t at0 = smem_addr(v_sm) + fw * 32 * 128 + (my_chunk >> 2) * (kTileTok * 128) + my_row * 128 +
+                             ((2 * my_chunk ^ my_row) & 7) * 16;
+        auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
+        uint32_t kt = 0;
+        for (uint32_t si = 0;; ++si) {
+            const Seg* const g = get_seg(si);
+            const int n = g->n;
+            if (!n) break;
+            const int32_t L = g->L, h = g->h;
+            int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
+            const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
+            done_seg(si);
+            int32_t pg = is_k && pos < L ? table[c.by_bs.of(pos)] : -1;
+            float sk = 0.f, sv = 0.f;
+            bool in = false;
+            // scales of the row at pos, its page known; on to the next tile's page
+            auto scales = [&]() {
+                in = pg >= 0 && pg < c.num_blocks;
+                sk = sv = 0.f;
+                if (in) {
+                    const int64_t i = ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs);
+                    sk = c.ks[i];
+                    sv = c.vs[i];
                 }
-                if (kt == done) break;
-                if (kt - done == 1)
-                    cp_wait<0>();
-                else if (kt - done == 2)
-                    cp_wait<1>();
-                else
-                    cp_wait<2>();
-                __syncwarp();
-                if (round) wait(my_empty + slot, (round - 1) & 1);
+                pos += kTileTok;
+                pg = pos < L ? table[c.by_bs.of(pos)] : -1;
+            };
+            if (is_k) scales();
+#pragma unroll 1
+            for (int t = 0; t < n; ++t, ++kt) {
                 if (is_k) {
-                    // lane = row = TMEM lane: two elements to a column
-                    tc_after();
+                    const uint32_t from = kt % RK, slot = kt % SK;
+                    wait(raw_full + from, (kt / RK) & 1);
                     const uint32_t at = tmem + X::K_at + slot * (DP / 2) + ((uint32_t)fw << 21);
+                    uint4 d[chunks];
 #pragma unroll
-                    for (int u = 0; u < DP / 16; ++u) {
-                        const uint4 w = lds16(raw_at(from, lane, u));
+                    for (int u = 0; u < chunks; ++u) d[u] = lds16(raw_at(from, lane, u));
+                    if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
+                    tc_after();
+#pragma unroll
+                    for (int u = 0; u < chunks; ++u) {
+                        const uint4 w = d[u];
                         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at + u * 8),
                                      "r"(e4m3_f16x2(w.x & 0xFFFF)), "r"(e4m3_f16x2(w.x >> 16)),
                                      "r"(e4m3_f16x2(w.y & 0xFFFF)), "r"(e4m3_f16x2(w.y >> 16)),
@@ -639,29 +558,48 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                                      "r"(e4m3_f16x2(w.w & 0xFFFF)), "r"(e4m3_f16x2(w.w >> 16))
                                      : "memory");
                     }
+                    unsigned char* const aux = aux_of(kt);
+                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
+                    if (lane == 0) ((uint32_t*)aux)[fw] = bits;
+                    ((float*)(aux + 16))[fw * 32 + lane] = sk;
+                    ((float*)(aux + 16))[kTileTok + fw * 32 + lane] = sv;
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(raw_empty + from);
+                        mbar_arrive(aux_full + kt % kAuxRing);
+                    }
+                    if (t + 1 < n) scales();
                     tc_wait_st();
                     tc_before();
-                    if (lane == 0) mbar_arrive(aux_full + done % kAuxRing);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(k_full + slot);
                 } else {
+                    const uint32_t from = kt % RV, slot = kt % SV;
+                    wait(raw_full + RK + from, (kt / RV) & 1);
                     const uint32_t base = at0 + slot * X::slot_bytes;
+                    uint4 d[chunks];
+#pragma unroll
+                    for (int r = 0; r < chunks; ++r) d[r] = lds16(raw_at(from, r * rpr + my_row, my_chunk));
+                    if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
 #pragma unroll
                     for (int r = 0; r < chunks; ++r) {
-                        const uint4 w = lds16(raw_at(from, r * rpr + my_row, my_chunk));
+                        const uint4 w = d[r];
                         sts16(swizzled(base, r, 0), make_uint4(e4m3_f16x2(w.x & 0xFFFF), e4m3_f16x2(w.x >> 16),
                                                                e4m3_f16x2(w.y & 0xFFFF), e4m3_f16x2(w.y >> 16)));
                         sts16(swizzled(base, r, 1), make_uint4(e4m3_f16x2(w.z & 0xFFFF), e4m3_f16x2(w.z >> 16),
                                                                e4m3_f16x2(w.w & 0xFFFF), e4m3_f16x2(w.w >> 16)));
                     }
                     fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(raw_empty + RK + from);
+                        mbar_arrive(v_full + slot);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(my_full + slot);
-                if (++slot == S) slot = 0, ++round;
-                if (++from == RT) from = 0;
             }
         }
     } else if (warp >= kMmaWarp) {
-        fewer_regs<56>();
+        fewer_regs<Q8 ? 56 : 64>();
         if (warp == kMmaWarp) {
         // ============================================================ products
         constexpr uint32_t id_qk = instr_desc(!Q8, false, false, N);
@@ -710,11 +648,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             if (++ks == SK) ks = 0, ++kr;
         };
         uint32_t t = 0;
+#pragma unroll 1
         for (int i = 0; i < TM; ++i) scores();
         for (uint32_t si = 0;; ++si) {
             const int n = count_of(si);
             if (!n) break;
             done_seg(si);  // at once: the cursor ahead, which has read it, may have to wait for its place
+#pragma unroll 1
             for (int i = 0; i < n; ++i, ++t) {
                 if (TM == 1) scores();
                 const uint32_t team = t % TM;
@@ -737,9 +677,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         }
         if (elect()) {
             tc_commit(drain);  // everything issued here is done before TMEM is freed
-            const uint64_t t0 = nanoseconds();
-            while (!mbar_try_wait(drain, 0) && nanoseconds() - t0 < kAttWaitNs) {
-            }
+            wait_seg(drain, 0);
         }
         __syncwarp();
     } else if (warp == kQueryWarp) {
@@ -756,7 +694,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             const int32_t row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
             const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)g->h * a.G * c.D * 2 + piece * 16;
             auto row_of = [&](int r) {
-                const int32_t rr = row0 + r, t = rr / a.G;
+                const int32_t rr = row0 + r, t = a.by_G.of(rr);
                 return q0 + t * a.q_row_bytes + (int64_t)(rr - t * a.G) * c.D * 2;
             };
             if (QB == 1)  // into L2 while the last products still need the place
@@ -770,8 +708,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     const bool in = r < rows && piece * 8 < c.D;
                     cp16(q_at + r * 128 + ((piece ^ r) & 7) * 16, in ? row_of(r) : a.q, in ? 16u : 0u);
                 }
-                cp_commit();
-                cp_wait<0>();
+                cp_wait_all();
             } else {
             float* const arow = arow_all + (si % R) * N;
 #pragma unroll 1
@@ -816,28 +753,65 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             done_seg(si);
         }
     } else if (warp == kSegWarp) {
-        // ============================================================ segments
+        // ============================================================ segments, K
         Walk<N> walk(a, u0, u1, b0, base0);
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.k_map) : "memory");
+        uint32_t kt = 0;
         for (uint32_t s = 0;; ++s) {
             Seg g;
             walk.next(g);
             if (s >= R) wait_seg(seg_empty + s % R, (s / R - 1) & 1);
             if (lane == 0) {
                 segs[s % R] = g;
+                *last_seq = (uint32_t)walk.b;
                 mbar_arrive(seg_full + s % R);
             }
             if (!g.n) break;
+            const int n = __shfl_sync(0xFFFFFFFFu, g.n, 0);
+            const int32_t* const table = c.table + (int64_t)g.b * c.max_blocks;
+            int32_t at = g.tile0 * kTileTok;
+            int32_t next = page_of(table, at + lane * p.box, g.L);
+#pragma unroll 1
+            for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
+                const int32_t pages = next;
+                if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, g.L);
+                if constexpr (Q8) {
+                    const uint32_t slot = kt % RK;
+                    if (kt >= RK) wait(raw_empty + slot, (kt / RK - 1) & 1);
+                    bring(&p.k_map, smem_addr(raw_sm) + slot * (kTileTok * 128), raw_full + slot, table, at, g.L, g.h, pages);
+                } else {
+                    const uint32_t slot = kt % SK;
+                    if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
+                    bring(&p.k_map, smem_addr(smem) + slot * X::slot_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                    // which positions are there
+                    uint32_t* const aux = (uint32_t*)aux_of(kt);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int32_t r = w * 32 + lane;
+                        int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, (r >> p.box_log) & 31);
+                        if (boxes > 32) pg = page_of(table, at + r, g.L);
+                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, pg < c.num_blocks && at + r < g.L);
+                        if (lane == 0) aux[w] = bits;
+                    }
+                    if (lane == 0) mbar_arrive(aux_full + kt % kAuxRing);
+                }
+            }
         }
         __syncwarp();
-    } else if (warp == kStatusWarp) {
-        // ============================================================ statuses
-        // One sequence at a time: its offsets, length, tree and pages; the
-        // rows of a sequence with an error become zeros.
-        for (int32_t b = blockIdx.x; b < c.B; b += p.grid) {
+    } else if (warp == kValueWarp) {
+        // ============================================================ V, statuses
+        // A sequence's status: its offsets, length, tree and pages; the rows of
+        // a sequence with an error become zeros. One after each segment.
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.v_map) : "memory");
+        int32_t next_b = blockIdx.x;
+        auto check_one = [&]() {
+            const int32_t b = next_b;
+            next_b += p.grid;
             const KvSeq s = kv_seq(b, a.row_off, a.t_max, a.rows, a.kv_lens, c.bs, c.max_blocks, true);
             int32_t st = s.st;
             bool bad = false;
             if (st == kKvOk && a.parent)
+#pragma unroll 1
                 for (int32_t v = lane; v < s.T; v += 32) {
                     const int32_t u = a.parent[s.lo + v];
                     bad |= v == 0 ? u != -1 : (u < 0 || u >= v);
@@ -845,8 +819,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             if (__any_sync(0xFFFFFFFFu, bad)) st = kKvBadLayout;
             if (st != kKvOk && s.lo >= 0) {
                 const int64_t m = (int64_t)s.T * a.Hq * c.D, o = s.lo * a.Hq * c.D;  // head_dim is a multiple of 8
+#pragma unroll 1
                 for (int64_t i = (int64_t)lane * 8; i < m; i += 256) *(uint4*)(a.out + (o + i) * 2) = make_uint4(0, 0, 0, 0);
                 if (a.lse)
+#pragma unroll 1
                     for (int64_t i = lane; i < (int64_t)s.T * a.Hq; i += 32)
                         a.lse[s.lo * a.Hq + i] = __uint_as_float(0xFF800000u);
             }
@@ -854,7 +830,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 if (st == kKvOk) {
                     bad = false;
                     if (s.T > 0)
-                        for (int64_t j = lane; j * c.bs < s.L; j += 32) {
+#pragma unroll 1
+                        for (int32_t j = lane; j <= c.by_bs.of(s.L - 1); j += 32) {
                             const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
                             bad |= pg < 0 || pg >= c.num_blocks;
                         }
@@ -862,10 +839,41 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 }
                 if (lane == 0) a.seq_status[b] = st;
             }
+        };
+        uint32_t kt = 0, si = 0;
+        for (bool open = true; open || next_b < c.B;) {
+            if (open) {
+                const Seg* const g = get_seg(si);
+                const int n = __shfl_sync(0xFFFFFFFFu, g->n, 0);
+                open = n != 0;
+                if (open) {
+                    const int32_t L = g->L, h = g->h;
+                    int32_t at = g->tile0 * kTileTok;
+                    const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
+                    done_seg(si++);
+                    int32_t next = page_of(table, at + lane * p.box, L);
+#pragma unroll 1
+                    for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
+                        const int32_t pages = next;
+                        if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, L);
+                        if constexpr (Q8) {
+                            const uint32_t slot = kt % RV;
+                            if (kt >= RV) wait(raw_empty + RK + slot, (kt / RV - 1) & 1);
+                            bring(&p.v_map, smem_addr(raw_sm) + (RK + slot) * (kTileTok * 128), raw_full + RK + slot, table, at, L, h,
+                                  pages);
+                        } else {
+                            const uint32_t slot = kt % SV;
+                            if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
+                            bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages);
+                        }
+                    }
+                }
+            }
+            if (next_b < c.B) check_one();
         }
         }
     } else {
-        more_regs<Q8 ? 80 : 88>();
+        more_regs<Q8 ? 80 : 104>();
         // ============================================================ softmax
         // Thread = one position of the tile; group gr is of team gr % TM and has
         // every GT-th 8-row piece of the query rows. A weight is 2^(score - m) with m a
@@ -932,6 +940,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 }
                 const bool any = bar_or(bar_all, kSoftThreads, bad);
                 if (tid == 0) *tree_bad = any;
+#pragma unroll 1
                 for (int reach = 1; reach < T; reach <<= 1) {
                     uint4 up = make_uint4(0, 0, 0, 0);
                     int32_t far = -1;
@@ -959,6 +968,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             int32_t lv = -100;  // Q8: values count in units of 2^lv
 
             const int first = (int)((team - gt) & (TM - 1));  // this team's first tile of the segment
+#pragma unroll 1
             for (int i = first; i < n; i += TM) {
                 const uint32_t t = gt + i, buf = t % SB, turn = t / TM;
                 if (live) {
@@ -980,7 +990,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         vis = 0;
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
-                            int32_t tk = (row0 + (sub + X::GT * m) * 8) / a.G;
+                            int32_t tk = a.by_G.of(row0 + (sub + X::GT * m) * 8);
                             int32_t left = (tk + 1) * a.G - (row0 + (sub + X::GT * m) * 8);  // rows of token tk from here
 #pragma unroll 1
                             for (int k = 0; k < 8; ++k) {
@@ -1079,29 +1089,39 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     };
                     if (turn) wait(pv_done + team, (turn - 1) & 1);  // the team's P and O are free
                     tc_after();
-                    if (i == first) refer();
                     // ---- weights. When a score passes the reference by too much, they leave the row sums again
                     // (exactly enough: what rounding leaves behind is within an ulp of that score's weight), the
                     // reference moves, and they are made anew.
-                    bool moved = false;
+                    bool moved = false, due = i == first;
+#pragma unroll 1
                     for (float sign = 1.f;;) {
+                        if (due) refer();
+                        due = false;
                         float top = none;
                         // Q8: f16 in units that bring the largest possible one, 2^grow, to 2^14
                         const float wv = Q8 ? vs * __uint_as_float((uint32_t)(127 + 6 - lv) << 23) : 1.f;
-                        float2 zb[2][4];
-                        tc_ld8(s_at, zb[0]);
+                        // two pieces at a time, so that one's latencies hide the other's
 #pragma unroll
-                        for (int m = 0; m < MC; ++m) {
-                            if (m < live) {
-                                float2(&z)[4] = zb[m & 1];
-                                tc_wait_ld(z);
-                                if (m + 1 < MC && m + 1 < live) tc_ld8(s_at + X::GT * (m + 1) * 8, zb[(m + 1) & 1]);
-                                relative(m, z, false);
+                        for (int m0 = 0; m0 < MC; m0 += 2) {
+                            if (m0 >= live) break;
+                            float2 zb[2][4];
+#pragma unroll
+                            for (int d = 0; d < 2; ++d)
+                                if (m0 + d < MC) tc_ld8(s_at + X::GT * (m0 + d < live ? m0 + d : m0) * 8, zb[d]);
+#pragma unroll
+                            for (int d = 0; d < 2; ++d)
+                                if (m0 + d < MC) tc_wait_ld(zb[d]);
+#pragma unroll
+                            for (int d = 0; d < 2; ++d) {
+                                const int m = m0 + d;
+                                if (m >= MC) continue;
+                                float2(&z)[4] = zb[d];
+                                const int piece = sub + X::GT * (m < live ? m : m0);  // (a piece that is not there: the other again)
+                                relative(m < live ? m : m0, z, false);
                                 float high = max3(z[0].x, z[0].y, z[1].x);
                                 high = max3(high, z[1].y, z[2].x);
                                 high = max3(high, z[2].y, z[3].x);
-                                high = fmaxf(high, z[3].y);
-                                top = fmaxf(top, high);
+                                top = max3(top, high, z[3].y);
                                 // sums stay finite until the reference moves
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) z[k] = make_float2(min_nan(z[k].x, grow), min_nan(z[k].y, grow));
@@ -1110,15 +1130,15 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                                     z[k] = make_float2(ex2(z[k].x), ex2(z[k].y));
                                     l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
                                 }
-                                const int piece = sub + X::GT * m;
                                 if (Q8) {
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
                                     if (masked) {
 #pragma unroll
                                         for (int k = 0; k < 4; ++k) {
-                                            z[k].x = (vis >> (m * 8 + 2 * k) & 1) ? z[k].x : 0.f;
-                                            z[k].y = (vis >> (m * 8 + 2 * k + 1) & 1) ? z[k].y : 0.f;
+                                            const int at = (m < live ? m : m0) * 8 + 2 * k;
+                                            z[k].x = (vis >> at & 1) ? z[k].x : 0.f;
+                                            z[k].y = (vis >> (at + 1) & 1) ? z[k].y : 0.f;
                                         }
                                     }
                                     *(uint4*)(pw + piece * 2048) = make_uint4(f16x2(z[0].x, z[0].y), f16x2(z[1].x, z[1].y),
@@ -1140,8 +1160,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
                         if (sign < 0.f) {
                             bar_sync(bar_gr, 128);
-                            refer();
-                            moved = true;
+                            due = moved = true;
                             sign = 1.f;
                             continue;
                         }
@@ -1150,9 +1169,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         if (i == first || moved || !bar_or(bar_gr, 128, top > grow || (Q8 && fabsf(vs) > v_unit && lv < 126))) break;
                         sign = -1.f;
                     }
-                    if (tail && sub == 0 && in && pos >= ctx && T > 1) {
-                        // A new token's values that are not finite would reach rows that do not see it (0 * inf):
-                        // they leave the tile here and join the rows that do see it at the end.
+                    if (tail && sub == 0 && (pos >= L || (in && pos >= ctx && T > 1))) {
+                        // The values of a page's slots past the length are cleared. A new token's values that are not
+                        // finite would reach rows that do not see it (0 * inf): they leave the tile here and join the
+                        // rows that do see it at the end.
+                        // (The last tile's product first: before it the ring may be two rounds behind, and a round two
+                        // behind looks done.)
+                        if (TM > 1 && t) wait(pv_done + (t - 1) % TM, ((t - 1) / TM) & 1);
                         wait(v_full + t % SV, (t / SV) & 1);
                         unsigned char* const v_row = v_sm + t % SV * X::slot_bytes + wt * 128;
                         constexpr uint32_t ex = Q8 ? 0x7C00u : 0x7F80u;
@@ -1160,6 +1183,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll 1
                         for (int k = 0; k < DP / 8; ++k) {
                             uint4* const at = (uint4*)(v_row + (k >> 3) * (kTileTok * 128) + (k & 7) * 16);
+                            if (pos >= L) {
+                                *at = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
                             uint4 v = *at;
                             uint32_t* const w = (uint32_t*)&v;
                             bool here = false;
@@ -1193,7 +1220,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             const bool skip = a.parent && *tree_bad;  // its rows are zeros, written with the statuses
             const int64_t part = (int64_t)blockIdx.x * 2 + (g->tile0 == 0 ? 1 : 0);
             auto out_row = [&](int r) {
-                const int32_t rr = row0 + r, tk = rr / a.G;
+                const int32_t rr = row0 + r, tk = a.by_G.of(rr);
                 return (g->lo + tk) * a.Hq + (int64_t)g->h * a.G + (rr - tk * a.G);
             };
             // the last product of a team with a tile here
@@ -1269,13 +1296,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                     for (int32_t u = 0; u < T; ++u) {
                         if (!(poison[u >> 5] >> (u & 31) & 1)) continue;
                         const int32_t pos = ctx + u;
-                        const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + pos / c.bs], sl = pos % c.bs;
+                        const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + c.by_bs.of(pos)], sl = (pos - c.by_bs.of(pos) * c.bs);
                         const unsigned char* v = c.v + pg * c.block_bytes + sl * c.token_bytes + g->h * c.head_bytes;
                         const float x = Q8 ? kv_e4m3(v[wt]) : bf16_lo(*(const uint16_t*)(v + 2 * wt));
                         if (fabsf(x) < __uint_as_float(0x7F800000u)) continue;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const int32_t tk = (row0 + r0 + k) / a.G;
+                            const int32_t tk = a.by_G.of(row0 + r0 + k);
                             if (a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u) o[k] += x;
                         }
                     }
@@ -1312,6 +1339,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll 1
                     for (int r = warp; r < rows; r += kSoftWarps) {
                         float M = kNoMax;
+#pragma unroll 1
                         for (int32_t j = c0 + lane; j <= c1; j += 32) {
                             const float x = __ldcg(&p.part_ml[((int64_t)j * 2 + (j == c0)) * N + r].x);
                             M = x > M || x != x ? x : M;
@@ -1323,7 +1351,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
                         float sum = 0.f;
                         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
                         for (int32_t j = c0; j <= c1; ++j) {
                             const int64_t at = ((int64_t)j * 2 + (j == c0)) * N + r;
                             const float2 ml = __ldcg(p.part_ml + at);
@@ -1359,11 +1387,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     }
     if (*aborted && tid == 0) {
         atomicOr(p.err, 1u);
-        if (a.seq_status) {
-            Walk<N> walk(a, u0, u1, b0, base0);
-            Seg g;
-            for (walk.next(g); g.n; walk.next(g)) a.seq_status[g.b] = kKvTimeout;
-        }
+        if (a.seq_status && u0 < u1)
+            for (int32_t b = b0; b <= (int32_t)*last_seq; ++b) a.seq_status[b] = kKvTimeout;
     }
 }
 
@@ -1375,7 +1400,7 @@ cudaError_t launch(const AttParams& p, cudaStream_t s) {
     constexpr int bytes = (int)(X::total > kSmemMax / 2 + 1024 ? X::total : kSmemMax / 2 + 1024);
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    f<<<p.grid, kAttThreads, bytes, s>>>(p);
+    f<<<p.grid, X::threads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 

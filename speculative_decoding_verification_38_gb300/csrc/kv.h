@@ -11,6 +11,24 @@ namespace specv {
 constexpr int kKvMaxQueries = 128;  // new tokens of one sequence in the attention
 constexpr int kKvMaxDim = 256;
 
+// Division of 0 <= n < 2^31 by a number the launch knows: with s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1 the
+// error n (m - 2^(31+s) / d) / 2^(31+s) stays below 1 / d, so n / d = n m >> (31 + s) exactly. A multiply and a shift
+// where the device's own division is some twenty instructions at each of its many places.
+struct KvDiv {
+    uint32_t m;
+    int32_t shift;
+    KvDiv() = default;
+    explicit KvDiv(uint32_t d) {
+        int s = 0;
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)((1ull << (31 + s)) / d + (d > 1 ? 1 : 0));
+        shift = 31 + s;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int32_t of(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * m) >> shift); }
+#endif
+};
+
 enum KvType : int32_t { kKvF32 = 0, kKvBf16 = 1, kKvE4m3 = 2 };  // the API's dtype codes
 enum KvSeqStatus : int32_t { kKvOk = 0, kKvBadKv = 2, kKvBadLayout = 4, kKvTimeout = 6 };
 
@@ -25,6 +43,7 @@ struct KvView {
     int64_t block_bytes, token_bytes, head_bytes, layer_bytes;
     int64_t scale_layer;  // scales of a layer
     int32_t B, H, D, bs, num_blocks, max_blocks, layers;
+    KvDiv by_bs;
     int32_t esz;  // bytes of an element: 2 or 1
 };
 
@@ -64,6 +83,7 @@ struct KvMove {
 struct KvAttend {
     KvView c;
     int32_t Hq, G, t_max;  // G = Hq / H
+    KvDiv by_G;
     int64_t rows;
     const int64_t* row_off;
     const int32_t* kv_lens;

@@ -61,6 +61,7 @@ KvView view(const spec_kv_cache_t* c, int32_t layer) {
     v.H = c->kv_heads;
     v.D = c->head_dim;
     v.bs = c->block_size;
+    v.by_bs = KvDiv((uint32_t)c->block_size);
     v.num_blocks = c->num_blocks;
     v.max_blocks = c->max_blocks;
     v.layers = c->layers;
@@ -191,6 +192,7 @@ SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* c, const spec_kv_at
     p.c = view(c, a->layer);
     p.Hq = a->q_heads;
     p.G = a->q_heads / c->kv_heads;
+    p.by_G = KvDiv((uint32_t)p.G);
     p.t_max = a->t_max;
     p.rows = a->rows;
     p.row_off = a->row_off;
