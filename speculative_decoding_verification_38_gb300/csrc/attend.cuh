@@ -203,8 +203,8 @@ struct __align__(16) Seg {
     int32_t b, h, rt, tile0, n;  // n tiles from tile0; n = 0: no more
     int32_t tiles;               // of the whole entry
     int32_t T, L;                // new tokens, length
-    int64_t first;  // the entry's first tile in the flat list
-    int64_t lo;     // the sequence's first query row
+    int64_t lo;                  // the sequence's first query row
+    int32_t c0, c1;              // the CTAs that share the entry
 };
 
 // ------------------------------------------------------------------ layout
@@ -251,47 +251,76 @@ struct Shape {
     static_assert(aux_ring > SK + SB, "aux ring");
 };
 
+// The flat list of tiles. An entry counts kOver more than its tiles, at its front, for what opening and closing it
+// costs; CTA i has [i * per, (i + 1) * per).
+constexpr int kOver = 5;
+
+// Kept out of line: the few places that divide 64-bit numbers do so once in a while, and their code is large.
+__device__ __noinline__ int64_t divide(int64_t a, int64_t b) { return a / b; }
+
 template <int N>
 struct Walk {
     const KvAttend& a;
-    int64_t u, u1, base, units;
-    int32_t b;
+    int64_t u, u1, per, first;  // place, end; where the entry at hand begins
+    int32_t b, h, rt;           // the entry
     KvSeq s;
     int32_t tiles, nrt;
 
     __device__ __forceinline__ static int64_t count(const KvAttend& a, int32_t b, KvSeq& s, int32_t& tiles,
                                                     int32_t& nrt) {
         s = kv_seq(b, a.row_off, a.t_max, a.rows, a.kv_lens, a.c.bs, a.c.max_blocks, true);
+        tiles = nrt = 0;
         if (s.st != kKvOk || s.T == 0) return 0;
         tiles = (s.L + kTileTok - 1) / kTileTok;
         nrt = (s.T * a.G + N - 1) / N;
-        return (int64_t)tiles * nrt * a.c.H;
+        return (int64_t)(tiles + kOver) * nrt * a.c.H;
     }
-    __device__ __forceinline__ Walk(const KvAttend& a_, int64_t u0, int64_t u1_, int32_t b0, int64_t base0)
-        : a(a_), u(u0), u1(u1_), base(base0), b(b0) {
-        units = u < u1 ? count(a, b, s, tiles, nrt) : 0;
+    // base0: where sequence b0 begins, which has u0 in it
+    __device__ __forceinline__ Walk(const KvAttend& a_, int64_t u0, int64_t u1_, int64_t per_, int32_t b0, int64_t base0)
+        : a(a_), u(u0), u1(u1_), per(per_), b(b0), h(0), rt(0) {
+        if (u >= u1) return;
+        count(a, b, s, tiles, nrt);
+        const int64_t e = divide(u - base0, tiles + kOver);
+        h = (int32_t)divide(e, nrt);
+        rt = (int32_t)(e - (int64_t)h * nrt);
+        first = base0 + e * (tiles + kOver);
     }
     __device__ __forceinline__ void next(Seg& g) {
         g.n = 0;
-        if (u >= u1) return;
-        while (u >= base + units) {
-            base += units;
-            if (++b >= a.c.B) return;  // lengths that change under the call
-            units = count(a, b, s, tiles, nrt);
+        while (u < u1) {
+            const int64_t end = first + kOver + tiles;
+            const int64_t from = max(u, first + kOver), to = min(end, u1);
+            if (from < to) {
+                g.tile0 = (int32_t)(from - first - kOver);
+                g.n = (int32_t)(to - from);
+                g.h = h;
+                g.rt = rt;
+                g.tiles = tiles;
+                g.b = b;
+                g.lo = s.lo;
+                g.T = s.T;
+                g.L = s.L;
+                if (g.n != tiles) {
+                    g.c0 = (int32_t)divide(first + kOver, per);
+                    g.c1 = (int32_t)divide(end - 1, per);
+                }
+            }
+            u = to > from ? to : min(end, u1);
+            if (u == end) {  // on to the next entry
+                first = end;
+                if (++rt >= nrt) rt = 0, ++h;
+                if (h >= a.c.H) {
+                    h = 0;
+                    do {
+                        if (++b >= a.c.B) {  // (before u1 only with lengths that change under the call)
+                            u = u1;
+                            break;
+                        }
+                    } while (count(a, b, s, tiles, nrt) == 0);
+                }
+            }
+            if (g.n) return;
         }
-        const int64_t rem = u - base;
-        const int64_t e = rem / tiles;
-        g.tile0 = (int32_t)(rem - e * tiles);
-        g.n = (int32_t)min((int64_t)(tiles - g.tile0), u1 - u);
-        g.h = (int32_t)(e / nrt);
-        g.rt = (int32_t)(e - (int64_t)g.h * nrt);
-        g.first = u - g.tile0;
-        g.tiles = tiles;
-        g.b = b;
-        g.lo = s.lo;
-        g.T = s.T;
-        g.L = s.L;
-        u += g.n;
     }
 };
 
@@ -435,7 +464,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         W += x;
     }
     const int64_t pre = before + incl - mine;
-    const int64_t per = (W + p.grid - 1) / p.grid;
+    const int64_t per = divide(W + p.grid - 1, p.grid);
     const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(u0 + per, W);
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
         int64_t at = pre;
@@ -754,7 +783,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         }
     } else if (warp == kSegWarp) {
         // ============================================================ segments, K
-        Walk<N> walk(a, u0, u1, b0, base0);
+        Walk<N> walk(a, u0, u1, per, b0, base0);
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.k_map) : "memory");
         uint32_t kt = 0;
         for (uint32_t s = 0;; ++s) {
@@ -763,7 +792,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             if (s >= R) wait_seg(seg_empty + s % R, (s / R - 1) & 1);
             if (lane == 0) {
                 segs[s % R] = g;
-                *last_seq = (uint32_t)walk.b;
+                *last_seq = (uint32_t)min(walk.b, c.B - 1);
                 mbar_arrive(seg_full + s % R);
             }
             if (!g.n) break;
@@ -1324,7 +1353,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             }
             if (!whole) {
                 // ---- join: the entry's parts lie with CTAs c0 (its second place) and c0 + 1 .. c1 (their first)
-                const int32_t c0 = (int32_t)(g->first / per), c1 = (int32_t)((g->first + g->tiles - 1) / per);
+                const int32_t c0 = g->c0, c1 = g->c1;
                 __threadfence();
                 bar_sync(bar_all, kSoftThreads);
                 if (tid == 0) {
