@@ -214,9 +214,10 @@ struct Shape {
     static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory and TMEM are full
     // Teams of softmax groups take the tiles in turn, each with sums of its own, so that a tile may take a team as
     // long as `TM` tiles take the loads; the groups of a team share the rows.
-    static constexpr int TM = N <= 32 ? 4 : N == 48 || (Q8 && N == 80) ? 2 : 1;
+    static constexpr int TM = N <= 32 ? 4 : N == 48 ? 2 : 1;
     static constexpr int GT = kGroups / TM;                // groups of a team
     static constexpr int SB = TM == 1 ? 2 : TM;            // score tiles in TMEM
+    static constexpr int PS = Q8 && N == 80 ? 2 : TM;      // P tiles: one for each team, or two to take turns
     static constexpr int MC = (N / 8 + GT - 1) / GT;       // 8-row pieces of a group
     static constexpr int NP = Q8 ? N : 2 * N;              // P's columns: one f16, or two bf16 parts
     static constexpr int O_at = SB * N, K_at = O_at + TM * NP, columns = K_at + (Q8 ? DP : 0);  // TMEM
@@ -227,7 +228,7 @@ struct Shape {
     static constexpr int RK = N == 32 || N >= 80 ? 2 : 3, RV = N == 128 ? 2 : 3;  // e4m3 tiles as they are
     static constexpr uint32_t raw_bytes = Q8 ? (RK + RV) * kTileTok * 128 : 0;  // rows of 128 bytes, whatever DP
     static constexpr uint32_t q_bytes = N * DP * 2;
-    static constexpr uint32_t p_bytes = NP * kTileTok * 2;      // of a team
+    static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
     static constexpr int aux_ring = TM == 4 ? 16 : 8;           // tiles of them: more than the K ring and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
@@ -237,14 +238,14 @@ struct Shape {
     static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
                                      (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 64) +
                                      (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * (RK + RV) : 0)) * 8 +
-                                     (2 * SB + 2 * TM + 5 + aux_ring + 2 * segs) * 8;
-    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - TM * p_bytes - misc) / slot_bytes);
+                                     (2 * SB + 2 * PS + 5 + aux_ring + 2 * segs) * 8;
+    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc) / slot_bytes);
     // tiles of the K ring (e4m3: in TMEM) and of the V ring; a V tile is held longer
     static constexpr int SK = Q8 ? 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
     static constexpr int rest = Q8 ? fit : fit - SK;
     static constexpr int SV = rest > kMaxSlots ? kMaxSlots : rest;
     static constexpr uint32_t ring_bytes = (Q8 ? SV : SK + SV) * slot_bytes;
-    static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + TM * p_bytes + misc;
+    static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + PS * p_bytes + misc;
     static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
     static_assert(2 * (SK + SV) <= (tight ? 8 : 4 * kMaxSlots) && total <= kSmemMax && columns <= 512, "memory");
     // a tile's masks and scales are written while those of the last SK + SB tiles may be in use
@@ -327,15 +328,15 @@ struct Walk {
 template <int NN, int DP, bool Q8>
 __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using X = Shape<NN, DP, Q8>;
-    constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, kAuxRing = X::aux_ring;
+    constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, PS = X::PS, kAuxRing = X::aux_ring;
     constexpr uint32_t SK = X::SK, SV = X::SV, RK = X::RK, RV = X::RV;
     constexpr int kAttThreads = X::threads;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const v_sm = smem + (Q8 ? 0 : SK * X::slot_bytes);  // the V ring; the K ring, if any, is before it
     unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [RK] K and [RV] V tiles as they are
     unsigned char* const q_sm = raw_sm + X::raw_bytes;
-    unsigned char* const p_sm = q_sm + QB * X::q_bytes;                // [TM]
-    unsigned char* const aux_sm = p_sm + TM * X::p_bytes;
+    unsigned char* const p_sm = q_sm + QB * X::q_bytes;                // [PS]
+    unsigned char* const aux_sm = p_sm + PS * X::p_bytes;
     float* const mref_all = (float*)(aux_sm + kAuxRing * X::aux_bytes);  // [TM][N] references
     // [TM][N] each: weight sums and factors of the teams, used between segments (tight: in P, free then)
     float* const lsum = X::tight ? (float*)(p_sm + (N / 8 + 4) * 2048) : mref_all + TM * N;
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     uint64_t* const s_full = v_empty + SV;
     uint64_t* const s_empty = s_full + SB;
     uint64_t* const p_full = s_empty + SB;
-    uint64_t* const pv_done = p_full + TM;
-    uint64_t* const drain = pv_done + TM;
+    uint64_t* const pv_done = p_full + PS;
+    uint64_t* const drain = pv_done + PS;
     uint64_t* const q_full = drain + 1;
     uint64_t* const q_empty = q_full + 2;
     uint64_t* const aux_full = q_empty + 2;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, 4 * X::GT);
         }
-        for (int i = 0; i < TM; ++i) {
+        for (int i = 0; i < PS; ++i) {
             mbar_init(p_full + i, 4 * X::GT);
             mbar_init(pv_done + i, 1);
         }
@@ -572,20 +573,28 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     const uint32_t from = kt % RK, slot = kt % SK;
                     wait(raw_full + from, (kt / RK) & 1);
                     const uint32_t at = tmem + X::K_at + slot * (DP / 2) + ((uint32_t)fw << 21);
-                    uint4 d[chunks];
-#pragma unroll
-                    for (int u = 0; u < chunks; ++u) d[u] = lds16(raw_at(from, lane, u));
+                    // (a short loop, two units at a time and the next two on their way: straight code of this length
+                    // waits for its own instructions)
+                    uint4 x = lds16(raw_at(from, lane, 0)), y = lds16(raw_at(from, lane, 1));
                     if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
                     tc_after();
-#pragma unroll
-                    for (int u = 0; u < chunks; ++u) {
-                        const uint4 w = d[u];
-                        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at + u * 8),
-                                     "r"(e4m3_f16x2(w.x & 0xFFFF)), "r"(e4m3_f16x2(w.x >> 16)),
-                                     "r"(e4m3_f16x2(w.y & 0xFFFF)), "r"(e4m3_f16x2(w.y >> 16)),
-                                     "r"(e4m3_f16x2(w.z & 0xFFFF)), "r"(e4m3_f16x2(w.z >> 16)),
-                                     "r"(e4m3_f16x2(w.w & 0xFFFF)), "r"(e4m3_f16x2(w.w >> 16))
-                                     : "memory");
+#pragma unroll 1
+                    for (int u = 0; u < chunks; u += 2) {
+                        const uint4 v = x, w = y;
+                        if (u + 2 < chunks) {
+                            x = lds16(raw_at(from, lane, u + 2));
+                            y = lds16(raw_at(from, lane, u + 3));
+                        }
+                        asm volatile(
+                            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                            ::"r"(at + u * 8),
+                            "r"(e4m3_f16x2(v.x & 0xFFFF)), "r"(e4m3_f16x2(v.x >> 16)), "r"(e4m3_f16x2(v.y & 0xFFFF)),
+                            "r"(e4m3_f16x2(v.y >> 16)), "r"(e4m3_f16x2(v.z & 0xFFFF)), "r"(e4m3_f16x2(v.z >> 16)),
+                            "r"(e4m3_f16x2(v.w & 0xFFFF)), "r"(e4m3_f16x2(v.w >> 16)), "r"(e4m3_f16x2(w.x & 0xFFFF)),
+                            "r"(e4m3_f16x2(w.x >> 16)), "r"(e4m3_f16x2(w.y & 0xFFFF)), "r"(e4m3_f16x2(w.y >> 16)),
+                            "r"(e4m3_f16x2(w.z & 0xFFFF)), "r"(e4m3_f16x2(w.z >> 16)), "r"(e4m3_f16x2(w.w & 0xFFFF)),
+                            "r"(e4m3_f16x2(w.w >> 16))
+                            : "memory");
                     }
                     unsigned char* const aux = aux_of(kt);
                     const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
@@ -606,17 +615,23 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     const uint32_t from = kt % RV, slot = kt % SV;
                     wait(raw_full + RK + from, (kt / RV) & 1);
                     const uint32_t base = at0 + slot * X::slot_bytes;
-                    uint4 d[chunks];
-#pragma unroll
-                    for (int r = 0; r < chunks; ++r) d[r] = lds16(raw_at(from, r * rpr + my_row, my_chunk));
+                    auto unit_at = [&](int r) { return lds16(raw_at(from, r * rpr + my_row, my_chunk)); };
+                    uint4 x = unit_at(0), y = unit_at(1);
                     if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
+#pragma unroll 1
+                    for (int r = 0; r < chunks; r += 2) {
+                        const uint4 u[2] = {x, y};
+                        if (r + 2 < chunks) {
+                            x = unit_at(r + 2);
+                            y = unit_at(r + 3);
+                        }
 #pragma unroll
-                    for (int r = 0; r < chunks; ++r) {
-                        const uint4 w = d[r];
-                        sts16(swizzled(base, r, 0), make_uint4(e4m3_f16x2(w.x & 0xFFFF), e4m3_f16x2(w.x >> 16),
-                                                               e4m3_f16x2(w.y & 0xFFFF), e4m3_f16x2(w.y >> 16)));
-                        sts16(swizzled(base, r, 1), make_uint4(e4m3_f16x2(w.z & 0xFFFF), e4m3_f16x2(w.z >> 16),
-                                                               e4m3_f16x2(w.w & 0xFFFF), e4m3_f16x2(w.w >> 16)));
+                        for (int i = 0; i < 2; ++i) {
+                            sts16(swizzled(base, r + i, 0), make_uint4(e4m3_f16x2(u[i].x & 0xFFFF), e4m3_f16x2(u[i].x >> 16),
+                                                                       e4m3_f16x2(u[i].y & 0xFFFF), e4m3_f16x2(u[i].y >> 16)));
+                            sts16(swizzled(base, r + i, 1), make_uint4(e4m3_f16x2(u[i].z & 0xFFFF), e4m3_f16x2(u[i].z >> 16),
+                                                                       e4m3_f16x2(u[i].w & 0xFFFF), e4m3_f16x2(u[i].w >> 16)));
+                        }
                     }
                     fence_async();
                     __syncwarp();
@@ -686,18 +701,18 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++t) {
                 if (TM == 1) scores();
-                const uint32_t team = t % TM;
+                const uint32_t team = t % TM, ps = t % PS;
                 wait(v_full + vs, vr & 1);
-                wait(p_full + team, (t / TM) & 1);
+                wait(p_full + ps, (t / PS) & 1);
                 tc_after();
                 if (elect()) {
-                    const uint64_t va = v_desc + vs * (X::slot_bytes >> 4), pd = p_desc + team * (X::p_bytes >> 4);
+                    const uint64_t va = v_desc + vs * (X::slot_bytes >> 4), pd = p_desc + ps * (X::p_bytes >> 4);
                     const uint32_t d = tmem + X::O_at + team * X::NP;
 #pragma unroll
                     for (int k = 0; k < kTileTok / 16; ++k)
                         tc_mma(d, va + ((k * 2048) >> 4), pd + ((k * 256) >> 4), id_pv, k > 0 || i >= TM);
                     tc_commit(v_empty + vs);
-                    tc_commit(pv_done + team);
+                    tc_commit(pv_done + ps);
                 }
                 __syncwarp();
                 if (++vs == SV) vs = 0, ++vr;
@@ -916,7 +931,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t team = gr % TM, sub = gr / TM;
         const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;
-        unsigned char* const pw = p_sm + team * X::p_bytes + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
+        unsigned char* const pw0 = p_sm + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
         float* const mref = mref_all + team * N;
         // the group's scratch [5][MC * 8]: its own, or in its second part of P while P is free
         float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
@@ -999,7 +1014,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             const int first = (int)((team - gt) & (TM - 1));  // this team's first tile of the segment
 #pragma unroll 1
             for (int i = first; i < n; i += TM) {
-                const uint32_t t = gt + i, buf = t % SB, turn = t / TM;
+                const uint32_t t = gt + i, buf = t % SB, ps = t % PS, turn = t / PS;
+                unsigned char* const pw = pw0 + ps * X::p_bytes;
                 if (live) {
                     wait(aux_full + t % kAuxRing, (t / kAuxRing) & 1);
                     const unsigned char* aux = aux_sm + (t % kAuxRing) * X::aux_bytes;
@@ -1093,6 +1109,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         bar_sync(bar_gr, 128);
                         lv += up;
                         if (i != first) {
+                            if (PS != TM) {
+                                wait(pv_done + (t - 1) % PS, ((t - 1) / PS) & 1);
+                                tc_after();
+                            }
                             const float shrink = Q8 ? (up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23)) : 1.f;
 #pragma unroll
                             for (int m = 0; m < MC; ++m)
@@ -1116,7 +1136,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         }
                         bar_sync(bar_gr, 128);  // the scratch may be P again
                     };
-                    if (turn) wait(pv_done + team, (turn - 1) & 1);  // the team's P and O are free
+                    if (turn) wait(pv_done + ps, (turn - 1) & 1);  // P is free, and O where P is one for each team
                     tc_after();
                     // ---- weights. When a score passes the reference by too much, they leave the row sums again
                     // (exactly enough: what rounding leaves behind is within an ulp of that score's weight), the
@@ -1204,7 +1224,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         // rows that do see it at the end.
                         // (The last tile's product first: before it the ring may be two rounds behind, and a round two
                         // behind looks done.)
-                        if (TM > 1 && t) wait(pv_done + (t - 1) % TM, ((t - 1) / TM) & 1);
+                        if (TM > 1 && t) wait(pv_done + (t - 1) % PS, ((t - 1) / PS) & 1);
                         wait(v_full + t % SV, (t / SV) & 1);
                         unsigned char* const v_row = v_sm + t % SV * X::slot_bytes + wt * 128;
                         constexpr uint32_t ex = Q8 ? 0x7C00u : 0x7F80u;
@@ -1236,10 +1256,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 if (lane == 0) {
                     if (!live) {  // in step with the tiles: one arrival in each phase
                         wait(s_full + buf, (t / SB) & 1);
-                        if (turn) wait(pv_done + team, (turn - 1) & 1);
+                        if (turn) wait(pv_done + ps, (turn - 1) & 1);
                     }
                     mbar_arrive(s_empty + buf);
-                    mbar_arrive(p_full + team);
+                    mbar_arrive(p_full + ps);
                 }
             }
             gt += n;
@@ -1255,7 +1275,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             // the last product of a team with a tile here
             auto finished = [&](uint32_t tm) {
                 const int f = (int)((tm - (gt - n)) & (TM - 1));
-                if (f < n) wait(pv_done + tm, ((gt - n + f + (n - 1 - f) / TM * TM) / TM) & 1);
+                const uint32_t last = gt - n + f + (n - 1 - f) / TM * TM;
+                if (f < n) wait(pv_done + last % PS, (last / PS) & 1);
                 return f < n;
             };
             if (X::tight) finished(0);  // the scratch is P's
