@@ -243,21 +243,44 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
+def _types():
+    """torch's types by the names the checks use (torch is imported with the first tensor, not with the package)."""
+    global _T
+    if _T is None:
+        import torch as _T
+    return _T
+
+
+_T = None
+
+
+def _current_stream() -> int:
+    """The current stream's handle. torch's own getters for it where they are there: building a Stream object for
+    every call took 3 us, as long as the call itself."""
+    global _current_stream
     import torch
 
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        torch.cuda.init()
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype_code(t) -> int:
-    import torch
-
-    if t.dtype == torch.float32:
-        return SPEC_F32
-    if t.dtype == torch.bfloat16:
+    T = _types()
+    if t.dtype is T.bfloat16:
         return SPEC_BF16
+    if t.dtype is T.float32:
+        return SPEC_F32
     raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
 
 
@@ -395,6 +418,8 @@ def _check_typed(t, name, dtype, numel=None, optional=True):
         if not optional:
             raise ValueError(f"{name} is required")
         return
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
+        return  # one look in the usual case: these calls are short
     _check_dev(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -447,6 +472,7 @@ class KVCache:
         c.k_scale, c.v_scale = _ptr(k_scale), _ptr(v_scale)
         c.block_table = block_table.data_ptr()
         self.struct = c
+        self.ref = ctypes.byref(c)
 
 
 class AttendArgs:
@@ -487,6 +513,7 @@ class AttendArgs:
         a.scale = float(scale)
         a.out, a.lse, a.seq_status = out.data_ptr(), _ptr(lse), _ptr(seq_status)
         self.struct = a
+        self.ref = ctypes.byref(a)
         self.workspace = None
         if workspace is not None:
             self.set_workspace(workspace)
@@ -604,63 +631,67 @@ def spec_kv_rollback(kv_in, kv_out, accepted, gammas, gamma_max, block_size=0, o
                                   _stream(stream))
 
 
+def _entry_rows(t, name, c) -> tuple:
+    """(rows, row stride) of a CUDA tensor [rows, kv_heads, head_dim] with a row's heads packed."""
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, {c.kv_heads}, {c.head_dim}]")
+    rows, heads, dim = t.shape
+    if heads != c.kv_heads or dim != c.head_dim:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, {c.kv_heads}, {c.head_dim}]")
+    a, b, e = t.stride()
+    if e != 1 or (heads > 1 and b != dim):
+        raise ValueError(f"{name} must have packed heads")
+    return rows, (a if rows > 1 else 0)
+
+
 def spec_kv_append(cache: KVCache, k_new, v_new, kv_lens, row_off=None, t_max=None, layer=0, seq_status=None,
                    stream=None) -> int:
     """New tokens' keys and values [rows, kv_heads, head_dim] (bfloat16 or
     float32, a row's heads packed, equal row strides) into one layer: the last
     positions of each sequence's kv_lens. row_off int64 [B+1], or None for
     t_max rows each (then t_max is required)."""
-    import torch
-
-    c = cache.struct
-    rows = k_new.shape[0]
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if not t.is_cuda or tuple(t.shape) != (rows, c.kv_heads, c.head_dim):
-            raise ValueError(f"{name} must be a CUDA tensor [rows, {c.kv_heads}, {c.head_dim}]")
-        if t.stride(2) != 1 or (c.kv_heads > 1 and t.stride(1) != c.head_dim):
-            raise ValueError(f"{name} must have packed heads")
-    if v_new.dtype != k_new.dtype or (rows > 1 and v_new.stride(0) != k_new.stride(0)):
-        raise ValueError("k_new and v_new must have one type and row stride")
-    _check_typed(kv_lens, "kv_lens", torch.int32, c.batch, optional=False)
-    _check_typed(row_off, "row_off", torch.int64, c.batch + 1)
-    _check_typed(seq_status, "seq_status", torch.int32, c.batch)
-    return lib().spec_kv_append(ctypes.byref(c), int(layer), k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new),
-                                k_new.stride(0) if rows > 1 else 0, rows, _ptr(row_off), int(t_max or 0),
-                                kv_lens.data_ptr(), _ptr(seq_status), _stream(stream))
+    T, c = _types(), cache.struct
+    rows = _entry_rows(k_new, "k_new", c)
+    if v_new.dtype is not k_new.dtype or _entry_rows(v_new, "v_new", c) != rows:
+        raise ValueError("k_new and v_new must have one type, shape and row stride")
+    _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
+    _check_typed(row_off, "row_off", T.int64, c.batch + 1)
+    _check_typed(seq_status, "seq_status", T.int32, c.batch)
+    return (_lib or lib()).spec_kv_append(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), rows[1],
+                                          rows[0], _ptr(row_off), t_max or 0, kv_lens.data_ptr(), _ptr(seq_status),
+                                          _stream(stream))
 
 
 def spec_kv_gather(cache: KVCache, kv_lens, out_off, k_out, v_out, layer=0, seq_status=None, stream=None) -> int:
     """One layer of every sequence's cache as rows [rows, kv_heads, head_dim]
     (bfloat16 or float32): row out_off[b] + j is position j of sequence b."""
-    import torch
-
-    c = cache.struct
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _check_typed(t, name, k_out.dtype, k_out.shape[0] * c.kv_heads * c.head_dim, optional=False)
-    _check_typed(kv_lens, "kv_lens", torch.int32, c.batch, optional=False)
-    _check_typed(out_off, "out_off", torch.int64, c.batch + 1, optional=False)
-    _check_typed(seq_status, "seq_status", torch.int32, c.batch)
-    return lib().spec_kv_gather(ctypes.byref(c), int(layer), kv_lens.data_ptr(), out_off.data_ptr(), k_out.shape[0],
-                                k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), _ptr(seq_status),
-                                _stream(stream))
+    T, c = _types(), cache.struct
+    rows = k_out.shape[0]
+    _check_typed(k_out, "k_out", k_out.dtype, rows * c.kv_heads * c.head_dim, optional=False)
+    _check_typed(v_out, "v_out", k_out.dtype, rows * c.kv_heads * c.head_dim, optional=False)
+    _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
+    _check_typed(out_off, "out_off", T.int64, c.batch + 1, optional=False)
+    _check_typed(seq_status, "seq_status", T.int32, c.batch)
+    return (_lib or lib()).spec_kv_gather(cache.ref, layer, kv_lens.data_ptr(), out_off.data_ptr(), rows, k_out.data_ptr(),
+                                          v_out.data_ptr(), _dtype_code(k_out), _ptr(seq_status), _stream(stream))
 
 
 def spec_kv_compact(cache: KVCache, node_off, path, accepted, kv_lens_in, kv_lens_out, out_num_blocks=None,
                     seq_status=None, stream=None) -> int:
     """Keep the accepted path's entries of each sequence's tree, in every
     layer (path and accepted: spec_tree_verify's out_path and out_accepted)."""
-    import torch
-
-    c = cache.struct
-    _check_typed(node_off, "node_off", torch.int64, c.batch + 1, optional=False)
-    _check_typed(path, "path", torch.int32, optional=False)
-    for name, t in (("accepted", accepted), ("kv_lens_in", kv_lens_in), ("kv_lens_out", kv_lens_out)):
-        _check_typed(t, name, torch.int32, c.batch, optional=False)
-    for name, t in (("out_num_blocks", out_num_blocks), ("seq_status", seq_status)):
-        _check_typed(t, name, torch.int32, c.batch)
-    return lib().spec_kv_compact(ctypes.byref(c), node_off.data_ptr(), path.numel(), path.data_ptr(),
-                                 accepted.data_ptr(), kv_lens_in.data_ptr(), kv_lens_out.data_ptr(),
-                                 _ptr(out_num_blocks), _ptr(seq_status), _stream(stream))
+    T, c = _types(), cache.struct
+    B = c.batch
+    _check_typed(node_off, "node_off", T.int64, B + 1, optional=False)
+    _check_typed(path, "path", T.int32, optional=False)
+    _check_typed(accepted, "accepted", T.int32, B, optional=False)
+    _check_typed(kv_lens_in, "kv_lens_in", T.int32, B, optional=False)
+    _check_typed(kv_lens_out, "kv_lens_out", T.int32, B, optional=False)
+    _check_typed(out_num_blocks, "out_num_blocks", T.int32, B)
+    _check_typed(seq_status, "seq_status", T.int32, B)
+    return (_lib or lib()).spec_kv_compact(cache.ref, node_off.data_ptr(), path.numel(), path.data_ptr(),
+                                           accepted.data_ptr(), kv_lens_in.data_ptr(), kv_lens_out.data_ptr(),
+                                           _ptr(out_num_blocks), _ptr(seq_status), _stream(stream))
 
 
 def spec_kv_attend_workspace_size(args: AttendArgs) -> int:
@@ -669,7 +700,7 @@ def spec_kv_attend_workspace_size(args: AttendArgs) -> int:
 
 def spec_kv_attend(args: AttendArgs, stream=None) -> int:
     """Attention of every sequence's new tokens over its cache (see AttendArgs)."""
-    return lib().spec_kv_attend(ctypes.byref(args.cache.struct), ctypes.byref(args.struct), _stream(stream))
+    return (_lib or lib()).spec_kv_attend(args.cache.ref, args.ref, _stream(stream))
 
 
 def spec_debug_philox(seed, rnd, seq_offset, batch, npos, out, stream=None) -> int:

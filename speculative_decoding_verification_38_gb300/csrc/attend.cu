@@ -77,6 +77,7 @@ cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
     AttParams p;
     p.a = a;
     p.grid = grid;
+    p.device = dev;
     p.box = 1;
     p.box_log = 0;
     while (p.box < kTileTok && a.c.bs % (2 * p.box) == 0) p.box *= 2, ++p.box_log;

@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -31,7 +32,7 @@ struct AttParams {
     float2* part_ml;   // [grid * 2][N] their maxima (log2) and weights' sums
     uint32_t* arrive;  // [grid] parts arrived, zero between calls
     uint32_t* err;
-    int32_t grid;
+    int32_t grid, device;
 };
 
 // Attention with row tiles of n query rows (16, 32, 48, 80 or 128).
@@ -179,12 +180,6 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t two) {  // the low 16 bits: two codes
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
-    return r;
-}
-
 // Shared-memory operand descriptor: start, leading and stride byte offsets,
 // swizzle (0 none, 2 128-byte).
 __device__ __forceinline__ uint64_t operand(uint32_t start, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -1448,8 +1443,13 @@ cudaError_t launch(const AttParams& p, cudaStream_t s) {
     auto* f = attend_kernel<N, DP, Q8>;
     // more than half of an SM's shared memory, whatever the ring took: one CTA on an SM owns its TMEM
     constexpr int bytes = (int)(X::total > kSmemMax / 2 + 1024 ? X::total : kSmemMax / 2 + 1024);
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> known{0};  // devices on which the kernel may use that much
+    const uint64_t bit = 1ull << (p.device & 63);
+    if (!(known.load() & bit) || p.device >= 64) {
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        known.fetch_or(bit);
+    }
     f<<<p.grid, X::threads, bytes, s>>>(p);
     return cudaGetLastError();
 }

@@ -102,12 +102,50 @@ __device__ __forceinline__ void write_entry(const float (&x)[8], bool live, unsi
     if (i == 0) *scale = pow2(e);
 }
 
-// New tokens into the cache. A flat range of entries (row, head), `lanes`
-// threads each; a CTA finds its first row's sequence by a warp search over
-// the offsets and steps on from there. The grid's last CTAs write the
-// statuses, one warp for each sequence.
+constexpr int kRows = 2;  // entries (row, head) of a thread: their loads are under way together
+
+// The same for eight bf16 values as they come (w), where all of the warp's are
+// finite: their magnitudes compare as 16-bit integers, two at a time, and a
+// power of two scales them exactly in bf16 (what falls below its normal range
+// is zero in e4m3 too). A third of write_entry's instructions, which were what
+// bounded the append of a prompt.
+__device__ __forceinline__ void write_codes(const uint32_t (&w)[4], bool live, unsigned char* dst, float* scale, int i,
+                                            int lanes) {
+    constexpr uint32_t mag = 0x7FFF7FFFu;
+    uint32_t m = live ? __vmaxu2(__vmaxu2(w[0] & mag, w[1] & mag), __vmaxu2(w[2] & mag, w[3] & mag)) : 0u;
+    for (int o = lanes >> 1; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);
+    if (__any_sync(0xFFFFFFFFu, top >= 0x7F80u)) {  // a NaN or an infinity somewhere
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16_lo(w[j]);
+            x[2 * j + 1] = bf16_hi(w[j]);
+        }
+        write_entry<kKvBf16, true>(x, live, dst, scale, i, lanes);
+        return;
+    }
+    if (!live) return;
+    const int32_t e = scale_exponent(__uint_as_float(top << 16));
+    const uint32_t f = (uint32_t)(127 - e) << 7, f2 = f | f << 16;
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t y;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[j]), "r"(f2));
+        c[j] = pack_e4m3(bf16_lo(y), bf16_hi(y));
+    }
+    *(uint2*)(dst + 8 * i) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (i == 0) *scale = pow2(e);
+}
+
+// New tokens into the cache. A flat range of entries (row, head), 2^lanes_log
+// threads each; a CTA finds its first row's sequence by a warp search over the
+// offsets and steps on from there. A thread asks for its values first, so that
+// the offsets, lengths and page numbers, each needing the last, come in their
+// shadow. The grid's last CTAs write the statuses, one warp for each sequence.
 template <int DT, bool Q8>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const KvNew n, int lanes, int64_t ctas) {
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const KvNew n, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
     const int warp = threadIdx.x >> 5;
     if ((int64_t)blockIdx.x >= ctas) {
@@ -119,56 +157,77 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
         if ((threadIdx.x & 31) == 0) n.seq_status[b] = st;
         return;
     }
-    const int per = kThreads / lanes;  // entries of a CTA
-    const int64_t first = (int64_t)blockIdx.x * per;
-    if (n.row_off) {
-        if (warp == 0) {
-            const int32_t b = kv_find(n.row_off, c.B, first / c.H);
-            if (threadIdx.x == 0) b_first = b;
-        }
-        __syncthreads();
-    }
-    const int64_t e = first + threadIdx.x / lanes;
-    const int i = threadIdx.x % lanes;
-    const int64_t r = e / c.H;
-    const int32_t h = (int32_t)(e - r * c.H);
-    bool live = r < n.rows && i * 8 < c.D;
-    int64_t at = 0, sc = 0;
-    if (r < n.rows) {
-        int32_t b;
-        if (n.row_off) {
-            b = b_first;
-            while (b < c.B && n.row_off[b + 1] <= r) ++b;
-        } else {
-            b = (int32_t)(r / n.t_max);
-        }
-        bool ok = false;
-        if (b < c.B) {
-            const KvSeq s = kv_seq(b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
-            if (s.st == kKvOk && r >= s.lo) {
-                const int32_t pos = s.L - s.T + (int32_t)(r - s.lo);
-                const int32_t pg = c.table[(int64_t)b * c.max_blocks + pos / c.bs];
-                const int32_t sl = pos % c.bs;
-                ok = pg >= 0 && pg < c.num_blocks;
-                at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
-                sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+    const int lanes = 1 << lanes_log, per = kThreads >> lanes_log;  // entries of a round
+    const int32_t first = blockIdx.x * (per * kRows);               // entries of a launch: fewer than 2^31
+    const int i = threadIdx.x & (lanes - 1);
+    const bool column = i * 8 < c.D;
+    constexpr bool packed = DT == kKvBf16 && Q8;
+    int32_t r[kRows], h[kRows];
+    float xk[packed ? 1 : kRows][8], xv[packed ? 1 : kRows][8];
+    uint32_t wk[packed ? kRows : 1][4], wv[packed ? kRows : 1][4];
+    bool live[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const int32_t e = first + u * per + (int)(threadIdx.x >> lanes_log);
+        r[u] = c.by_H.of(e);
+        h[u] = e - r[u] * c.H;
+        live[u] = r[u] < n.rows && column;
+        if (live[u]) {
+            const int64_t src = r[u] * n.row_bytes + (int64_t)h[u] * c.D * (DT == kKvBf16 ? 2 : 4);
+            if constexpr (packed) {
+                *(uint4*)wk[u] = *(const uint4*)(n.k + src + 16 * i);
+                *(uint4*)wv[u] = *(const uint4*)(n.v + src + 16 * i);
+            } else {
+                load8<DT>(n.k + src, i, xk[u]);
+                load8<DT>(n.v + src, i, xv[u]);
             }
         }
-        live = live && ok;
     }
-    float xk[8], xv[8];
-    if (live) {
-        const int64_t src = r * n.row_bytes + (int64_t)h * c.D * (DT == kKvBf16 ? 2 : 4);
-        load8<DT>(n.k + src, i, xk);
-        load8<DT>(n.v + src, i, xv);
+    int32_t b = 0;
+    if (n.row_off) {
+        if (warp == 0) {
+            const int32_t x = kv_find(n.row_off, c.B, c.by_H.of(first));
+            if (threadIdx.x == 0) b_first = x;
+        }
+        __syncthreads();
+        b = b_first;
     }
-    write_entry<DT, Q8>(xk, live, c.k + at, Q8 ? c.ks + sc : nullptr, i, lanes);
-    write_entry<DT, Q8>(xv, live, c.v + at, Q8 ? c.vs + sc : nullptr, i, lanes);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        int64_t at = 0, sc = 0;
+        if (r[u] < n.rows) {
+            if (n.row_off)
+                while (b < c.B && n.row_off[b + 1] <= r[u]) ++b;
+            else
+                b = r[u] / n.t_max;
+            bool ok = false;
+            if (b < c.B) {
+                const KvSeq s = kv_seq(b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
+                if (s.st == kKvOk && r[u] >= s.lo) {
+                    const int32_t pos = s.L - s.T + (int32_t)(r[u] - s.lo);
+                    const int32_t j = c.by_bs.of(pos), sl = pos - j * c.bs;
+                    const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+                    ok = pg >= 0 && pg < c.num_blocks;
+                    at = pg * c.block_bytes + sl * c.token_bytes + h[u] * c.head_bytes;
+                    sc = ((int64_t)pg * c.H + h[u]) * c.bs + sl;
+                }
+            }
+            live[u] = live[u] && ok;
+        }
+        if constexpr (packed) {
+            write_codes(wk[u], live[u], c.k + at, c.ks + sc, i, lanes);
+            write_codes(wv[u], live[u], c.v + at, c.vs + sc, i, lanes);
+        } else {
+            write_entry<DT, Q8>(xk[u], live[u], c.k + at, Q8 ? c.ks + sc : nullptr, i, lanes);
+            write_entry<DT, Q8>(xv[u], live[u], c.v + at, Q8 ? c.vs + sc : nullptr, i, lanes);
+        }
+    }
 }
 
-// The cache back as rows: value = code * scale.
+// The cache back as rows: value = code * scale. Threads and entries as above;
+// a thread's entries are all looked up, then all asked for, then written.
 template <bool Q8, int ODT>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, const KvRead g, int lanes, int64_t ctas) {
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, const KvRead g, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
     const int warp = threadIdx.x >> 5;
     if ((int64_t)blockIdx.x >= ctas) {
@@ -186,59 +245,93 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, con
         if ((threadIdx.x & 31) == 0) g.seq_status[b] = st;
         return;
     }
-    const int per = kThreads / lanes;
-    const int64_t first = (int64_t)blockIdx.x * per;
+    const int lanes = 1 << lanes_log, per = kThreads >> lanes_log;
+    const int32_t first = blockIdx.x * (per * kRows);
     if (warp == 0) {
-        const int32_t b = kv_find(g.out_off, c.B, first / c.H);
-        if (threadIdx.x == 0) b_first = b;
+        const int32_t x = kv_find(g.out_off, c.B, c.by_H.of(first));
+        if (threadIdx.x == 0) b_first = x;
     }
     __syncthreads();
-    const int64_t e = first + threadIdx.x / lanes;
-    const int i = threadIdx.x % lanes;
-    const int64_t r = e / c.H;
-    const int32_t h = (int32_t)(e - r * c.H);
-    if (r >= g.rows || i * 8 >= c.D) return;
+    const int i = threadIdx.x & (lanes - 1);
+    if (i * 8 >= c.D) return;
     int32_t b = b_first;
-    while (b < c.B && g.out_off[b + 1] <= r) ++b;
-    if (b >= c.B) return;
-    const int64_t lo = g.out_off[b], hi = g.out_off[b + 1];
-    const int32_t L = g.kv_lens[b];
-    if (lo < 0 || hi > g.rows || hi - lo != L || r < lo || L > (int64_t)c.bs * c.max_blocks) return;
-    const int32_t pos = (int32_t)(r - lo);
-    const int32_t pg = c.table[(int64_t)b * c.max_blocks + pos / c.bs];
-    const int32_t sl = pos % c.bs;
-    const bool ok = pg >= 0 && pg < c.num_blocks;
-    const int64_t at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
-    const int64_t sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+    int64_t at[kRows], sc[kRows];  // at: -1 no row of a sequence, -2 a page outside the pool
+    int32_t e[kRows];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        const unsigned char* src = (kv ? c.v : c.k) + at;
-        unsigned char* dst = (kv ? g.v : g.k) + (r * c.H + h) * (int64_t)c.D * (ODT == kKvBf16 ? 2 : 4);
-        float x[8];
-        if (!ok) {
+    for (int u = 0; u < kRows; ++u) {
+        e[u] = first + u * per + (int)(threadIdx.x >> lanes_log);
+        at[u] = -1;
+        sc[u] = 0;
+        const int32_t r = c.by_H.of(e[u]), h = e[u] - r * c.H;
+        if (r >= g.rows) continue;
+        while (b < c.B && g.out_off[b + 1] <= r) ++b;
+        if (b >= c.B) continue;
+        const int64_t lo = g.out_off[b], hi = g.out_off[b + 1];
+        const int32_t L = g.kv_lens[b];
+        if (lo < 0 || hi > g.rows || hi - lo != L || r < lo || L > (int64_t)c.bs * c.max_blocks) continue;
+        const int32_t pos = (int32_t)(r - lo);
+        const int32_t j = c.by_bs.of(pos), sl = pos - j * c.bs;
+        const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+        at[u] = -2;
+        if (pg < 0 || pg >= c.num_blocks) continue;
+        at[u] = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
+        sc[u] = ((int64_t)pg * c.H + h) * c.bs + sl;
+    }
+    uint4 w[kRows][2];
+    float s[kRows][2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        } else if (Q8) {
-            const uint2 w = *(const uint2*)(src + 8 * i);
-            const float s = (kv ? c.vs : c.ks)[sc];
+    for (int u = 0; u < kRows; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = kv_e4m3((uint8_t)(w.x >> (8 * j))) * s;
-                x[4 + j] = kv_e4m3((uint8_t)(w.y >> (8 * j))) * s;
+        for (int kv = 0; kv < 2; ++kv) {
+            w[u][kv] = make_uint4(0, 0, 0, 0);
+            s[u][kv] = 0.f;
+            if (at[u] < 0) continue;
+            const unsigned char* src = (kv ? c.v : c.k) + at[u];
+            if (Q8) {
+                const uint2 x = *(const uint2*)(src + 8 * i);
+                w[u][kv].x = x.x;
+                w[u][kv].y = x.y;
+                s[u][kv] = (kv ? c.vs : c.ks)[sc[u]];
+            } else {
+                w[u][kv] = *(const uint4*)(src + 16 * i);
             }
-        } else {
-            load8<kKvBf16>(src, i, x);
         }
-        if (ODT == kKvBf16) {
-            uint4 w;
-            w.x = pack_bf16(x[0], x[1]);
-            w.y = pack_bf16(x[2], x[3]);
-            w.z = pack_bf16(x[4], x[5]);
-            w.w = pack_bf16(x[6], x[7]);
-            *(uint4*)(dst + 16 * i) = w;
-        } else {
-            *(float4*)(dst + 32 * i) = make_float4(x[0], x[1], x[2], x[3]);
-            *(float4*)(dst + 32 * i + 16) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        if (at[u] == -1) continue;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            unsigned char* dst = (kv ? g.v : g.k) + e[u] * ((int64_t)c.D * (ODT == kKvBf16 ? 2 : 4));
+            const uint4 y = w[u][kv];
+            if (!Q8 && ODT == kKvBf16) {
+                *(uint4*)(dst + 16 * i) = y;
+                continue;
+            }
+            float x[8];
+            if (Q8) {
+                const uint32_t h2[4] = {e4m3_f16x2(y.x & 0xFFFF), e4m3_f16x2(y.x >> 16), e4m3_f16x2(y.y & 0xFFFF),
+                                        e4m3_f16x2(y.y >> 16)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __half22float2(*(const __half2*)&h2[j]);
+                    x[2 * j] = f.x * s[u][kv];
+                    x[2 * j + 1] = f.y * s[u][kv];
+                }
+            } else {
+                const uint32_t q[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[2 * j] = bf16_lo(q[j]);
+                    x[2 * j + 1] = bf16_hi(q[j]);
+                }
+            }
+            if (ODT == kKvBf16) {
+                *(uint4*)(dst + 16 * i) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                                     pack_bf16(x[6], x[7]));
+            } else {
+                *(float4*)(dst + 32 * i) = make_float4(x[0], x[1], x[2], x[3]);
+                *(float4*)(dst + 32 * i + 16) = make_float4(x[4], x[5], x[6], x[7]);
+            }
         }
     }
 }
@@ -270,7 +363,7 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, co
             if (v <= u || v >= N) {
                 bad = true;
             } else {
-                const int32_t ps = table[(base + v) / c.bs], pd = table[(base + 1 + i) / c.bs];
+                const int32_t ps = table[c.by_bs.of(base + v)], pd = table[c.by_bs.of(base + 1 + i)];
                 bad |= ps < 0 || ps >= c.num_blocks || pd < 0 || pd >= c.num_blocks;
             }
         }
@@ -433,17 +526,17 @@ __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const
     if (p.lse && lane == 0) p.lse[row * p.Hq + hq] = l == 0.f ? none : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-int lanes_of(int32_t D) {
-    int n = 1;
-    while (n * 8 < D) n <<= 1;
+int lanes_log_of(int32_t D) {
+    int n = 0;
+    while ((8 << n) < D) ++n;
     return n;  // D <= 256: at most a warp
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s) {
-    const int lanes = lanes_of(c.D);
-    const int per = kThreads / lanes;
+    const int lanes = lanes_log_of(c.D);
+    const int per = (kThreads >> lanes) * kRows;
     const int64_t ctas = (n.rows * c.H + per - 1) / per;
     const int64_t grid = ctas + (n.seq_status ? (c.B + kThreads / 32 - 1) / (kThreads / 32) : 0);
     if (grid == 0) return cudaSuccess;
@@ -456,8 +549,8 @@ cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_gather(const KvView& c, const KvRead& g, cudaStream_t s) {
-    const int lanes = lanes_of(c.D);
-    const int per = kThreads / lanes;
+    const int lanes = lanes_log_of(c.D);
+    const int per = (kThreads >> lanes) * kRows;
     const int64_t ctas = (g.rows * c.H + per - 1) / per;
     const int64_t grid = ctas + (g.seq_status ? (c.B + kThreads / 32 - 1) / (kThreads / 32) : 0);
     if (grid == 0) return cudaSuccess;

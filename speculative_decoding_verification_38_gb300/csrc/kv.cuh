@@ -53,6 +53,11 @@ __device__ __forceinline__ int32_t kv_find(const int64_t* off, int32_t n, int64_
     return lo;
 }
 
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t two) {  // the low 16 bits: two codes, exact as f16
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
 __device__ __forceinline__ float kv_e4m3(uint8_t code) {
     __nv_fp8_e4m3 x;
     x.__x = code;

@@ -43,7 +43,7 @@ struct KvView {
     int64_t block_bytes, token_bytes, head_bytes, layer_bytes;
     int64_t scale_layer;  // scales of a layer
     int32_t B, H, D, bs, num_blocks, max_blocks, layers;
-    KvDiv by_bs;
+    KvDiv by_bs, by_H;
     int32_t esz;  // bytes of an element: 2 or 1
 };
 

@@ -14,6 +14,7 @@ static_assert(SPEC_SEQ_BAD_KV == kKvBadKv && SPEC_SEQ_BAD_LAYOUT == kKvBadLayout
               "status codes");
 
 constexpr int64_t kMaxPositions = (int64_t)1 << 30;  // positions are 32-bit in the kernels
+constexpr int64_t kMaxEntries = ((int64_t)1 << 31) - 65536;  // (row, head) of one launch: 32-bit in the kernels
 constexpr int32_t kMaxBlockSize = 65536;
 constexpr int32_t kMaxHeads = 65535;
 
@@ -62,6 +63,7 @@ KvView view(const spec_kv_cache_t* c, int32_t layer) {
     v.D = c->head_dim;
     v.bs = c->block_size;
     v.by_bs = KvDiv((uint32_t)c->block_size);
+    v.by_H = KvDiv((uint32_t)c->kv_heads);
     v.num_blocks = c->num_blocks;
     v.max_blocks = c->max_blocks;
     v.layers = c->layers;
@@ -105,7 +107,7 @@ SPEC_API spec_status_t spec_kv_append(const spec_kv_cache_t* c, int32_t layer, c
         return SPEC_ERR_ALIGNMENT;
     if ((row_off && !aligned(row_off, 8)) || !aligned(kv_lens, 4) || (seq_status && !aligned(seq_status, 4)))
         return SPEC_ERR_ALIGNMENT;
-    if (rows > ((int64_t)1 << 31) / c->kv_heads) return SPEC_ERR_UNSUPPORTED;  // entries of one launch
+    if (rows > kMaxEntries / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
     KvNew n;
     n.k = (const unsigned char*)k_new;
     n.v = (const unsigned char*)v_new;
@@ -130,7 +132,7 @@ SPEC_API spec_status_t spec_kv_gather(const spec_kv_cache_t* c, int32_t layer, c
     if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(out_off, 8) || !aligned(kv_lens, 4) ||
         (seq_status && !aligned(seq_status, 4)))
         return SPEC_ERR_ALIGNMENT;
-    if (rows > ((int64_t)1 << 31) / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
+    if (rows > kMaxEntries / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
     KvRead g;
     g.k = (unsigned char*)k_out;
     g.v = (unsigned char*)v_out;
