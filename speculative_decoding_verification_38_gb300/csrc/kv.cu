@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, con
 // later entry: taken in order, each thread's column moves in place. A thread
 // owns one 16-byte column (or one scale) of one layer and head, and takes the
 // path kMove entries at a time: loads together, then stores.
-constexpr int kMove = 8;
-__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, const KvMove m) {
+constexpr int kMove = 4;
+__global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c, const KvMove m) {
     __shared__ int64_t from[kMove], to[kMove];    // page * block + slot * token, bytes
     __shared__ int64_t sfrom[kMove], sto[kMove];  // scales: page * H * bs + slot
     const int32_t b = blockIdx.x;
@@ -356,10 +356,12 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, co
     const int32_t N = (int32_t)(hi - lo);
     const int32_t base = L - N;
     const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+    bool moves = false;
     if (st == kKvOk) {
         bool bad = false;
         for (int32_t i = threadIdx.x; i < a; i += kThreads) {
             const int32_t v = m.path[lo + i], u = i ? m.path[lo + i - 1] : 0;
+            moves |= v != i + 1;
             if (v <= u || v >= N) {
                 bad = true;
             } else {
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, co
             }
         }
         if (__syncthreads_or(bad)) st = kKvBadLayout;
+        moves = __syncthreads_or(moves);
     }
     if (blockIdx.y == 0 && threadIdx.x == 0) {
         const int32_t out = st == kKvOk ? L - (N - 1 - a) : L;
@@ -375,17 +378,17 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, co
         if (m.out_blocks) m.out_blocks[b] = (int32_t)(((int64_t)out + c.bs - 1) / c.bs);
         if (m.seq_status) m.seq_status[b] = st;
     }
-    if (st != kKvOk) return;
+    if (st != kKvOk || !moves) return;  // the first children all the way: every entry is in its place
     const int32_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);  // 16-byte columns of an entry, and its scale
-    const int64_t all = (int64_t)c.layers * c.H * 2 * cols;
-    const int64_t t = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+    const uint32_t all = (uint32_t)c.layers * c.H * 2 * cols;  // the host keeps it below 2^31
+    const uint32_t t = blockIdx.y * kThreads + threadIdx.x;
     const bool live = t < all;
-    const int32_t col = (int32_t)(t % cols);
-    int64_t x = t / cols;
-    const int32_t kv = (int32_t)(x & 1);
+    uint32_t x = t / cols;
+    const uint32_t col = t - x * cols;
+    const uint32_t kv = x & 1;
     x >>= 1;
-    const int32_t h = (int32_t)(x % c.H);
     const int64_t layer = x / c.H;
+    const uint32_t h = x - (uint32_t)layer * c.H;
     unsigned char* p = (kv ? c.v : c.k) + layer * c.layer_bytes + h * c.head_bytes + 16 * col;
     const bool scale = c.ks && col == cols - 1;
     float* sp = scale && live ? (kv ? c.vs : c.ks) + layer * c.scale_layer + (int64_t)h * c.bs : nullptr;
@@ -395,11 +398,12 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, co
         if (threadIdx.x < k) {
             const int32_t i = i0 + threadIdx.x;
             const int32_t s = base + m.path[lo + i], d = base + 1 + i;
-            const int64_t ps = table[s / c.bs], pd = table[d / c.bs];
-            from[threadIdx.x] = ps * c.block_bytes + (s % c.bs) * c.token_bytes;
-            to[threadIdx.x] = pd * c.block_bytes + (d % c.bs) * c.token_bytes;
-            sfrom[threadIdx.x] = ps * c.H * c.bs + s % c.bs;
-            sto[threadIdx.x] = pd * c.H * c.bs + d % c.bs;
+            const int32_t js = c.by_bs.of(s), jd = c.by_bs.of(d);
+            const int64_t ps = table[js], pd = table[jd];
+            from[threadIdx.x] = ps * c.block_bytes + (s - js * c.bs) * c.token_bytes;
+            to[threadIdx.x] = pd * c.block_bytes + (d - jd * c.bs) * c.token_bytes;
+            sfrom[threadIdx.x] = ps * c.H * c.bs + s - js * c.bs;
+            sto[threadIdx.x] = pd * c.H * c.bs + d - jd * c.bs;
         }
         __syncthreads();
         if (!live) continue;
