@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     float* const fac = lsum + TM * N;
     float* const arow_all = mref_all + X::state / 4;  // Q8: [R][N] a query row's power of two times scale * log2(e)
     unsigned char* const red_sm = (unsigned char*)(arow_all + (Q8 ? R * N : 0));
-    uint32_t* const anc = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] ancestors of a tree's tokens
-    Seg* const segs = (Seg*)(anc + kKvMaxQueries * 4);
+    uint32_t* const seen_by = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] the tokens that see a tree's token
+    Seg* const segs = (Seg*)(seen_by + kKvMaxQueries * 4);
     uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then:
     volatile uint32_t* const aborted = poison + 4;   // a wait gave up
     uint32_t* const tmem_at = poison + 5;
@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             done_seg(si);  // at once: the cursor ahead, which has read it, may have to wait for its place
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++t) {
-                if (TM == 1) scores();
                 const uint32_t team = t % TM, ps = t % PS;
+                if (TM == 1) scores();
                 wait(v_full + vs, vr & 1);
                 wait(p_full + ps, (t / PS) & 1);
                 tc_after();
@@ -737,12 +737,15 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 return q0 + t * a.q_row_bytes + (int64_t)(rr - t * a.G) * c.D * 2;
             };
             if (QB == 1)  // into L2 while the last products still need the place
-                for (int r = sub; r < rows; r += rpq)
-                    if (piece * 8 < c.D && (piece & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(r)));
+#pragma unroll 1
+                for (int r = lane; r < rows; r += 32)
+#pragma unroll
+                    for (int d = 0; d < DP / 64; ++d)
+                        if (d * 64 < c.D) asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(r) + d * 128 - piece * 16));
             if (si >= QB) wait(q_empty + si % QB, (si / QB - 1) & 1);
             const uint32_t q_at = smem_addr(q_sm) + (si % QB) * X::q_bytes + (piece >> 3) * (N * 128);
             if constexpr (!Q8) {
-#pragma unroll 1
+#pragma unroll 8
                 for (int r = sub; r < N; r += rpq) {
                     const bool in = r < rows && piece * 8 < c.D;
                     cp16(q_at + r * 128 + ((piece ^ r) & 7) * 16, in ? row_of(r) : a.q, in ? 16u : 0u);
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             return op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 1));
         };
         uint32_t gt = 0;
-        int32_t anc_of = -1;  // the sequence whose ancestors are known
+        int32_t tree_of = -1;  // the sequence whose ancestors are known
         for (uint32_t si = 0;; ++si) {
             const Seg* const g = get_seg(si);
             const int n = g->n;
@@ -960,8 +963,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             if (tid < TM * N) mref_all[tid] = kNoMax;
             if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
             if (tid < 4) poison[tid] = 0;
-            if (a.parent && g->b != anc_of) {
-                anc_of = g->b;
+            if (a.parent && g->b != tree_of) {
+                tree_of = g->b;
                 // ancestors by doubling: after k rounds a token knows those up to 2^k - 1 above it
                 int32_t jump = -1;
                 bool bad = false;
@@ -974,7 +977,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (bad) jump = -1;
                         m[tid >> 5] = 1u << (tid & 31);
                     }
-                    *(uint4*)(anc + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
+                    *(uint4*)(seen_by + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
                     jumps[tid] = (uint32_t)jump;
                 }
                 const bool any = bar_or(bar_all, kSoftThreads, bad);
@@ -984,18 +987,32 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     uint4 up = make_uint4(0, 0, 0, 0);
                     int32_t far = -1;
                     if (jump >= 0) {
-                        up = *(const uint4*)(anc + jump * 4);
+                        up = *(const uint4*)(seen_by + jump * 4);
                         far = (int32_t)jumps[jump];
                     }
                     bar_sync(bar_all, kSoftThreads);
                     if (jump >= 0) {
                         m[0] |= up.x, m[1] |= up.y, m[2] |= up.z, m[3] |= up.w;
-                        *(uint4*)(anc + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
+                        *(uint4*)(seen_by + tid * 4) = make_uint4(m[0], m[1], m[2], m[3]);
                         jumps[tid] = (uint32_t)far;
                     }
                     jump = far;
                     bar_sync(bar_all, kSoftThreads);
                 }
+                // and turned round: those that a token's entry is seen by, which is what a position's thread asks for
+                if (tid < kKvMaxQueries) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t by = 0;
+#pragma unroll 1
+                        for (int k = 0; k < 32; ++k) {
+                            const uint32_t x = __ballot_sync(0xFFFFFFFFu, m[j] >> k & 1);
+                            if (lane == k) by = x;
+                        }
+                        seen_by[(j * 32 + lane) * 4 + warp] = by;
+                    }
+                }
+                bar_sync(bar_all, kSoftThreads);
             } else {
                 bar_sync(bar_all, kSoftThreads);
             }
@@ -1030,14 +1047,20 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         vis = 0;
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
-                            int32_t tk = a.by_G.of(row0 + (sub + X::GT * m) * 8);
-                            int32_t left = (tk + 1) * a.G - (row0 + (sub + X::GT * m) * 8);  // rows of token tk from here
-#pragma unroll 1
+                            const int32_t r = row0 + (sub + X::GT * m) * 8, tk = a.by_G.of(r), w = tk >> 5;
+                            int32_t left = (tk + 1) * a.G - r;  // rows of token tk from here
+                            uint32_t see;                       // tokens tk, tk + 1, ..
+                            if (a.parent)
+                                see = __funnelshift_r(w < 4 ? seen_by[u * 4 + w] : 0, w < 3 ? seen_by[u * 4 + w + 1] : 0, tk & 31);
+                            else
+                                see = tk >= u ? ~0u : u - tk >= 8 ? 0u : ~0u << (u - tk);
+                            uint32_t bits = 0;
+#pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                const bool see = a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u;
-                                vis |= (Rows)see << (m * 8 + k);
-                                if (--left == 0) left = a.G, ++tk;
+                                bits |= (see & 1) << k;
+                                if (--left == 0) left = a.G, see >>= 1;
                             }
+                            vis |= (Rows)bits << (m * 8);
                         }
                     }
                     const bool masked = tail || __any_sync(0xFFFFFFFFu, !in);
@@ -1348,7 +1371,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int32_t tk = a.by_G.of(row0 + r0 + k);
-                            if (a.parent ? tk < T && (anc[tk * 4 + (u >> 5)] >> (u & 31) & 1) : tk >= u) o[k] += x;
+                            if (a.parent ? tk < T && (seen_by[u * 4 + (tk >> 5)] >> (tk & 31) & 1) : tk >= u) o[k] += x;
                         }
                     }
                 }
