@@ -52,7 +52,7 @@ constexpr int kMmaWarp = kSoftWarps;      // issues the products
 constexpr int kSegWarp = kMmaWarp + 1;    // makes the segments, loads K
 constexpr int kValueWarp = kSegWarp + 1;  // loads V, checks the sequences
 constexpr int kQueryWarp = kValueWarp + 1;
-constexpr int kTurnWarp = kQueryWarp + 1; // e4m3: four warps turn K tiles to f16, four V tiles
+constexpr int kTurnWarp = kQueryWarp + 1; // e4m3: four warps for queries and scales, four turn V tiles to f16
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 4;                  // tiles of the K ring, and of the V ring
 constexpr uint32_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
@@ -81,11 +81,11 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 __device__ __forceinline__ void tc_ld8(uint32_t at, float (&x)[8]) {
@@ -180,6 +180,11 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {  // a in the low byte
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
 // Shared-memory operand descriptor: start, leading and stride byte offsets,
 // swizzle (0 none, 2 128-byte).
 __device__ __forceinline__ uint64_t operand(uint32_t start, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -191,6 +196,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t start, uint32_t lbo, uint32
 __host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool a_mn, bool b_mn, int n) {
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
            (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+// The same for A of e4m3 and B of e5m2.
+__host__ __device__ constexpr uint32_t instr_desc_f8(int n) {
+    return 1u << 4 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
 // A run of tiles of one (sequence, head, row tile).
@@ -215,31 +224,33 @@ struct Shape {
     static constexpr int PS = Q8 && N == 80 ? 2 : TM;      // P tiles: one for each team, or two to take turns
     static constexpr int MC = (N / 8 + GT - 1) / GT;       // 8-row pieces of a group
     static constexpr int NP = Q8 ? N : 2 * N;              // P's columns: one f16, or two bf16 parts
-    static constexpr int O_at = SB * N, K_at = O_at + TM * NP, columns = K_at + (Q8 ? DP : 0);  // TMEM
+    static constexpr int O_at = SB * N, columns = O_at + TM * NP;  // TMEM
     static constexpr int QB = N == 128 || (Q8 && N == 80) ? 1 : 2;  // row tiles of queries held
     static constexpr int segs = tight ? 2 : 4;             // segments known ahead
     static constexpr int threads = (kTurnWarp + (Q8 ? 8 : 0)) * 32;
     static constexpr uint32_t slot_bytes = kTileTok * DP * 2;
-    static constexpr int RK = N == 32 || N >= 80 ? 2 : 3, RV = N == 128 ? 2 : 3;  // e4m3 tiles as they are
-    static constexpr uint32_t raw_bytes = Q8 ? (RK + RV) * kTileTok * 128 : 0;  // rows of 128 bytes, whatever DP
-    static constexpr uint32_t q_bytes = N * DP * 2;
+    static constexpr uint32_t raw_tile = kTileTok * 128;   // an e4m3 tile as it is: rows of 128 bytes, whatever DP
+    static constexpr uint32_t k_bytes = Q8 ? raw_tile : slot_bytes;
+    static constexpr int RV = N > 16 ? 2 : 3;              // V tiles as they are
+    static constexpr uint32_t raw_bytes = Q8 ? RV * raw_tile : 0;
+    static constexpr uint32_t q_bytes = Q8 ? 3 * N * 128 : N * DP * 2;  // e4m3: three parts
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
-    static constexpr int aux_ring = TM == 4 ? 16 : 8;           // tiles of them: more than the K ring and scores can hold
+    static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 6 : 8;  // tiles of them: more than the K ring and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
     // after the tiles, Q and P: aux ring, per team and row the reference, weight sum and factor, row factors of Q,
     // scratch, ancestors, segments, poison, barriers
     static constexpr uint32_t state = tight ? N * 4 : 3 * TM * N * 4;
     static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
                                      (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 64) +
-                                     (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * (RK + RV) : 0)) * 8 +
+                                     (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * RV : 0)) * 8 +
                                      (2 * SB + 2 * PS + 5 + aux_ring + 2 * segs) * 8;
-    static constexpr int fit = (int)((kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc) / slot_bytes);
-    // tiles of the K ring (e4m3: in TMEM) and of the V ring; a V tile is held longer
-    static constexpr int SK = Q8 ? 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
-    static constexpr int rest = Q8 ? fit : fit - SK;
+    static constexpr int room = (int)(kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc), fit = room / slot_bytes;
+    // tiles of the K ring and of the V ring; a V tile is held longer
+    static constexpr int SK = Q8 ? (room - 3 * (int)k_bytes) / (int)slot_bytes >= 2 ? 3 : 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
+    static constexpr int rest = Q8 ? (room - SK * (int)k_bytes) / (int)slot_bytes : fit - SK;
     static constexpr int SV = rest > kMaxSlots ? kMaxSlots : rest;
-    static constexpr uint32_t ring_bytes = (Q8 ? SV : SK + SV) * slot_bytes;
+    static constexpr uint32_t ring_bytes = SK * k_bytes + SV * slot_bytes;
     static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + PS * p_bytes + misc;
     static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
     static_assert(2 * (SK + SV) <= (tight ? 8 : 4 * kMaxSlots) && total <= kSmemMax && columns <= 512, "memory");
@@ -324,11 +335,11 @@ template <int NN, int DP, bool Q8>
 __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using X = Shape<NN, DP, Q8>;
     constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, PS = X::PS, kAuxRing = X::aux_ring;
-    constexpr uint32_t SK = X::SK, SV = X::SV, RK = X::RK, RV = X::RV;
+    constexpr uint32_t SK = X::SK, SV = X::SV, RV = X::RV;
     constexpr int kAttThreads = X::threads;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char* const v_sm = smem + (Q8 ? 0 : SK * X::slot_bytes);  // the V ring; the K ring, if any, is before it
-    unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [RK] K and [RV] V tiles as they are
+    unsigned char* const v_sm = smem + SK * X::k_bytes;                // the V ring, after the K ring
+    unsigned char* const raw_sm = smem + X::ring_bytes;                // Q8: [RV] V tiles as they are
     unsigned char* const q_sm = raw_sm + X::raw_bytes;
     unsigned char* const p_sm = q_sm + QB * X::q_bytes;                // [PS]
     unsigned char* const aux_sm = p_sm + PS * X::p_bytes;
@@ -361,8 +372,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     uint64_t* const aux_full = q_empty + 2;
     uint64_t* const seg_full = aux_full + kAuxRing;
     uint64_t* const seg_empty = seg_full + R;
-    uint64_t* const raw_full = seg_empty + R;       // Q8: [RK] of K, [RV] of V
-    uint64_t* const raw_empty = raw_full + RK + RV;
+    uint64_t* const raw_full = seg_empty + R;       // Q8: [RV]
+    uint64_t* const raw_empty = raw_full + RV;
 
     const KvAttend& a = p.a;
     const KvView& c = a.c;
@@ -398,15 +409,15 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     // ------------------------------------------------- this CTA's run of tiles
     if (tid == 0) {
         for (uint32_t i = 0; i < SK; ++i) {
-            mbar_init(k_full + i, Q8 ? 4 : 1);
-            mbar_init(k_empty + i, 1);
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, Q8 ? 5 : 1);
         }
         for (uint32_t i = 0; i < SV; ++i) {
             mbar_init(v_full + i, Q8 ? 4 : 1);
             mbar_init(v_empty + i, 1);
         }
         if (Q8)
-            for (uint32_t i = 0; i < RK + RV; ++i) {
+            for (uint32_t i = 0; i < RV; ++i) {
                 mbar_init(raw_full + i, 1);
                 mbar_init(raw_empty + i, 4);
             }
@@ -419,14 +430,14 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             mbar_init(pv_done + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 1);
+            mbar_init(q_full + i, Q8 ? 4 : 1);
             mbar_init(q_empty + i, 1);
         }
         mbar_init(drain, 1);
         for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, Q8 ? 4 : 1);
         for (int i = 0; i < R; ++i) {
             mbar_init(seg_full + i, 1);
-            mbar_init(seg_empty + i, kSoftWarps + 3 + (Q8 ? 8 : 0));
+            mbar_init(seg_empty + i, kSoftWarps + (Q8 ? 2 + 8 : 3));
         }
         *aborted = 0;
         fence_barrier_init();
@@ -520,77 +531,103 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     // rest with 64. e4m3: 7 groups with 72; softmax 80, the turning warps (2) 64, the rest 56.
     if (Q8 && warp >= kTurnWarp) {
         fewer_regs<64>();
-        // ============================================================ e4m3 to f16
-        // Exactly, 32 rows to a warp: V tiles from shared memory to the V ring, K tiles to TMEM as the scores' first
-        // operand (lane = row = TMEM lane, two elements to a column). The K warps also bring the tile's scales.
-        const bool is_k = warp < kTurnWarp + 4;
         const int fw = warp & 3;
-        const uint32_t raw = smem_addr(raw_sm) + (is_k ? 0 : RK * kTileTok * 128) + fw * 32 * 128;
-        // 16-byte unit u of row r, as the load exchanged them: a column of them lies in different banks
-        auto raw_at = [&](uint32_t tile, int r, int u) {
-            return raw + tile * (kTileTok * 128) + r * 128 + ((u ^ r) & 7) * 16;
-        };
-        constexpr int chunks = DP / 16, rpr = 32 / chunks;  // 16-byte units of a row, rows of a warp's access
-        const int my_chunk = lane % chunks, my_row = lane / chunks;
-        // where this lane's unit of row `my_row + r * rpr` goes in a V tile: an exclusive or and an offset away from
-        // row my_row's, as 16-byte units are exchanged within a row by its row's number
-        const uint32_t at0 = smem_addr(v_sm) + fw * 32 * 128 + (my_chunk >> 2) * (kTileTok * 128) + my_row * 128 +
-                             ((2 * my_chunk ^ my_row) & 7) * 16;
-        auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
         uint32_t kt = 0;
-        for (uint32_t si = 0;; ++si) {
-            const Seg* const g = get_seg(si);
-            const int n = g->n;
-            if (!n) break;
-            const int32_t L = g->L, h = g->h;
-            int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
-            const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
-            done_seg(si);
-            int32_t pg = is_k && pos < L ? table[c.by_bs.of(pos)] : -1;
-            float sk = 0.f, sv = 0.f;
-            bool in = false;
-            // scales of the row at pos, its page known; on to the next tile's page
-            auto scales = [&]() {
-                in = pg >= 0 && pg < c.num_blocks;
-                sk = sv = 0.f;
-                if (in) {
-                    const int64_t i = ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs);
-                    sk = c.ks[i];
-                    sv = c.vs[i];
-                }
-                pos += kTileTok;
-                pg = pos < L ? table[c.by_bs.of(pos)] : -1;
-            };
-            if (is_k) scales();
-#pragma unroll 1
-            for (int t = 0; t < n; ++t, ++kt) {
-                if (is_k) {
-                    const uint32_t from = kt % RK, slot = kt % SK;
-                    wait(raw_full + from, (kt / RK) & 1);
-                    const uint32_t at = tmem + X::K_at + slot * (DP / 2) + ((uint32_t)fw << 21);
-                    // (a short loop, two units at a time and the next two on their way: straight code of this length
-                    // waits for its own instructions)
-                    uint4 x = lds16(raw_at(from, lane, 0)), y = lds16(raw_at(from, lane, 1));
-                    if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
-                    tc_after();
-#pragma unroll 1
-                    for (int u = 0; u < chunks; u += 2) {
-                        const uint4 v = x, w = y;
-                        if (u + 2 < chunks) {
-                            x = lds16(raw_at(from, lane, u + 2));
-                            y = lds16(raw_at(from, lane, u + 3));
-                        }
-                        asm volatile(
-                            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                            ::"r"(at + u * 8),
-                            "r"(e4m3_f16x2(v.x & 0xFFFF)), "r"(e4m3_f16x2(v.x >> 16)), "r"(e4m3_f16x2(v.y & 0xFFFF)),
-                            "r"(e4m3_f16x2(v.y >> 16)), "r"(e4m3_f16x2(v.z & 0xFFFF)), "r"(e4m3_f16x2(v.z >> 16)),
-                            "r"(e4m3_f16x2(v.w & 0xFFFF)), "r"(e4m3_f16x2(v.w >> 16)), "r"(e4m3_f16x2(w.x & 0xFFFF)),
-                            "r"(e4m3_f16x2(w.x >> 16)), "r"(e4m3_f16x2(w.y & 0xFFFF)), "r"(e4m3_f16x2(w.y >> 16)),
-                            "r"(e4m3_f16x2(w.z & 0xFFFF)), "r"(e4m3_f16x2(w.z >> 16)), "r"(e4m3_f16x2(w.w & 0xFFFF)),
-                            "r"(e4m3_f16x2(w.w >> 16))
-                            : "memory");
+        if (warp < kTurnWarp + 4) {
+            // ======================================================== e4m3: queries, scales
+            // A K tile is the scores' first operand as it is; the queries are its equal in three e5m2 parts, each
+            // the rest's first three bits. A row counts in a power of two that brings its largest element to [2^14,
+            // 2^15): the parts hold all 8 bits of what is 2^-24 of it or more, and the rest to 2^-31 of it.
+            const float k2 = a.scale * kLog2e;
+            constexpr int qc = DP / 8, rpq = 32 / qc;  // 8-element pieces of a row, rows of one load
+            static_assert(N / 4 % rpq == 0, "rows of a warp");
+            const int piece = lane % qc, sub = lane / qc;
+            for (uint32_t si = 0;; ++si) {
+                const Seg* const g = get_seg(si);
+                const int n = g->n;
+                if (!n) break;
+                const int32_t L = g->L, h = g->h, row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
+                int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
+                const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
+                const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)h * a.G * c.D * 2 + piece * 16;
+                done_seg(si);
+                int32_t pg = pos < L ? table[c.by_bs.of(pos)] : -1;
+                float sk = 0.f, sv = 0.f;
+                bool in = false;
+                // scales of the row at pos, its page known; on to the next tile's page
+                auto scales = [&]() {
+                    in = pg >= 0 && pg < c.num_blocks;
+                    sk = sv = 0.f;
+                    if (in) {
+                        const int64_t i = ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs);
+                        sk = c.ks[i];
+                        sv = c.vs[i];
                     }
+                    pos += kTileTok;
+                    pg = pos < L ? table[c.by_bs.of(pos)] : -1;
+                };
+                scales();
+                const uint32_t q_at = smem_addr(q_sm) + (si % QB) * X::q_bytes + (piece & 1) * 8;
+                float* const arow = arow_all + (si % R) * N;
+                auto load_q = [&](int r) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (r < rows && piece * 8 < c.D) {
+                        const int32_t rr = row0 + r, t = a.by_G.of(rr);
+                        w = *(const uint4*)(q0 + t * a.q_row_bytes + (int64_t)(rr - t * a.G) * c.D * 2);
+                    }
+                    return w;
+                };
+                const int r_end = (fw + 1) * (N / 4);
+                int r = fw * (N / 4) + sub;
+                uint4 next = load_q(r);
+                if (si >= QB) wait(q_empty + si % QB, (si / QB - 1) & 1);
+#pragma unroll 1
+                for (; r < r_end; r += rpq) {
+                    const uint4 w = next;
+                    if (r + rpq < r_end) next = load_q(r + rpq);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t m = 0;  // magnitudes compare as integers; what is not finite does not count
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = u[j] & 0x7FFFu, hi = u[j] >> 16 & 0x7FFFu;
+                        m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                    }
+#pragma unroll
+                    for (int o = qc / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                    const int e = m ? max(-126, min(113, (int)(m >> 7) - 127 - 14)) : 0;  // x / 2^e
+                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[2 * j] = bf16_lo(u[j]) * f;
+                        x[2 * j + 1] = bf16_hi(u[j]) * f;
+                        // (an infinity as NaN, as e5m2 conversions saturate: the row's weights are NaN either way)
+                        if ((u[j] & 0x7F80u) == 0x7F80u) x[2 * j] = __uint_as_float(0x7FC00000u);
+                        if ((u[j] & 0x7F800000u) == 0x7F800000u) x[2 * j + 1] = __uint_as_float(0x7FC00000u);
+                    }
+#pragma unroll 1
+                    for (int part = 0; part < 3; ++part) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            b[j] = e5m2x2(x[2 * j], x[2 * j + 1]);
+                            // an e5m2 number is the first byte of the fp16 one
+                            x[2 * j] -= __half2float(__ushort_as_half((unsigned short)(b[j] << 8)));
+                            x[2 * j + 1] -= __half2float(__ushort_as_half((unsigned short)(b[j] & 0xFF00u)));
+                        }
+                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(q_at + (part * N + r) * 128 + (((piece >> 1) ^ r) & 7) * 16),
+                                     "r"(b[0] | b[1] << 16), "r"(b[2] | b[3] << 16)
+                                     : "memory");
+                    }
+                    if (piece == 0) arow[r] = k2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + si % QB);
+#pragma unroll 1
+                for (int t = 0; t < n; ++t, ++kt) {
+                    const uint32_t slot = kt % SK;
+                    wait(k_full + slot, (kt / SK) & 1);  // in step with the K ring, so that the scales' is not overrun
                     unsigned char* const aux = aux_of(kt);
                     const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
                     if (lane == 0) ((uint32_t*)aux)[fw] = bits;
@@ -598,19 +635,38 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     ((float*)(aux + 16))[kTileTok + fw * 32 + lane] = sv;
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(raw_empty + from);
+                        mbar_arrive(k_empty + slot);
                         mbar_arrive(aux_full + kt % kAuxRing);
                     }
                     if (t + 1 < n) scales();
-                    tc_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(k_full + slot);
-                } else {
+                }
+            }
+        } else {
+            // ======================================================== e4m3: V to f16
+            // Exactly, 32 rows to a warp, from a tile as it is to the V ring.
+            const uint32_t raw = smem_addr(raw_sm) + fw * 32 * 128;
+            constexpr int chunks = DP / 16, rpr = 32 / chunks;  // 16-byte units of a row, rows of a warp's access
+            const int my_chunk = lane % chunks, my_row = lane / chunks;
+            // where this lane's unit of row `my_row + r * rpr` goes in a V tile: an exclusive or and an offset away from
+            // row my_row's, as 16-byte units are exchanged within a row by its row's number
+            const uint32_t at0 = smem_addr(v_sm) + fw * 32 * 128 + (my_chunk >> 2) * (kTileTok * 128) + my_row * 128 +
+                                 ((2 * my_chunk ^ my_row) & 7) * 16;
+            auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
+            for (uint32_t si = 0;; ++si) {
+                const int n = get_seg(si)->n;
+                if (!n) break;
+                done_seg(si);
+#pragma unroll 1
+                for (int t = 0; t < n; ++t, ++kt) {
                     const uint32_t from = kt % RV, slot = kt % SV;
-                    wait(raw_full + RK + from, (kt / RV) & 1);
+                    wait(raw_full + from, (kt / RV) & 1);
                     const uint32_t base = at0 + slot * X::slot_bytes;
-                    auto unit_at = [&](int r) { return lds16(raw_at(from, r * rpr + my_row, my_chunk)); };
+                    auto unit_at = [&](int r) {
+                        const int row = r * rpr + my_row;
+                        return lds16(raw + from * X::raw_tile + row * 128 + ((my_chunk ^ row) & 7) * 16);
+                    };
+                    // (a short loop, two units at a time and the next two on their way: straight code of this length
+                    // waits for its own instructions)
                     uint4 x = unit_at(0), y = unit_at(1);
                     if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
 #pragma unroll 1
@@ -631,7 +687,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     fence_async();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(raw_empty + RK + from);
+                        mbar_arrive(raw_empty + from);
                         mbar_arrive(v_full + slot);
                     }
                 }
@@ -641,7 +697,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         fewer_regs<Q8 ? 56 : 64>();
         if (warp == kMmaWarp) {
         // ============================================================ products
-        constexpr uint32_t id_qk = instr_desc(!Q8, false, false, N);
+        constexpr uint32_t id_qk = Q8 ? instr_desc_f8(N) : instr_desc(true, false, false, N);
         constexpr uint32_t id_pv = instr_desc(!Q8, true, true, X::NP);
         const uint64_t k_desc = operand(smem_addr(smem), 16, 1024, 2);
         const uint64_t v_desc = operand(smem_addr(v_sm), DP == 128 ? kTileTok * 128 : 0, 1024, 2);
@@ -666,16 +722,20 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             tc_after();
             ++qi;
             if (elect()) {
-                const uint64_t ka = k_desc + ks * (X::slot_bytes >> 4);
+                const uint64_t ka = k_desc + ks * (X::k_bytes >> 4);
                 const uint64_t qd = q_desc + (qs % QB) * (X::q_bytes >> 4);
-                const uint32_t kt = tmem + X::K_at + ks * (DP / 2), d = tmem + buf * N;
+                const uint32_t d = tmem + buf * N;
+                if constexpr (Q8) {
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint64_t qk = qd + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4);
-                    if constexpr (Q8)
-                        tc_mma_ts(d, kt + k * 8, qk, id_qk, k > 0);
-                    else
-                        tc_mma(d, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4), qk, id_qk, k > 0);
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int k = 0; k < DP / 32; ++k)
+                            tc_mma_f8(d, ka + (k * 32 >> 4), qd + ((part * N * 128 + k * 32) >> 4), id_qk, part + k > 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        tc_mma(d, ka + (((k >> 2) * (kTileTok * 128) + (k & 3) * 32) >> 4),
+                               qd + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
                 }
                 tc_commit(k_empty + ks);
                 tc_commit(s_full + buf);
@@ -721,13 +781,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         __syncwarp();
     } else if (warp == kQueryWarp) {
         // ============================================================ queries
-        // Row tiles of queries, a segment ahead where there is room for two.
-        const float k2 = a.scale * kLog2e;
+        // Row tiles of queries, a segment ahead where there is room for two (e4m3: see above).
         constexpr int qc = DP / 8, rpq = 32 / qc;  // 16-byte pieces of a row, rows of one load
-        constexpr int step = 4;
-        static_assert(N % (step * rpq) == 0, "rows of a round of loads");
         const int piece = lane % qc, sub = lane / qc;
-        for (uint32_t si = 0;; ++si) {
+        for (uint32_t si = 0; !Q8; ++si) {
             const Seg* const g = get_seg(si);
             if (!g->n) break;
             const int32_t row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
@@ -744,51 +801,12 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (d * 64 < c.D) asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(r) + d * 128 - piece * 16));
             if (si >= QB) wait(q_empty + si % QB, (si / QB - 1) & 1);
             const uint32_t q_at = smem_addr(q_sm) + (si % QB) * X::q_bytes + (piece >> 3) * (N * 128);
-            if constexpr (!Q8) {
 #pragma unroll 8
-                for (int r = sub; r < N; r += rpq) {
-                    const bool in = r < rows && piece * 8 < c.D;
-                    cp16(q_at + r * 128 + ((piece ^ r) & 7) * 16, in ? row_of(r) : a.q, in ? 16u : 0u);
-                }
-                cp_wait_all();
-            } else {
-            float* const arow = arow_all + (si % R) * N;
-#pragma unroll 1
-            for (int r0 = 0; r0 < N; r0 += step * rpq) {
-                uint4 w[step];
-#pragma unroll
-                for (int i = 0; i < step; ++i) {
-                    const int r = r0 + i * rpq + sub;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows && piece * 8 < c.D) w[i] = *(const uint4*)row_of(r);
-                }
-#pragma unroll
-                for (int i = 0; i < step; ++i) {
-                    const int r = r0 + i * rpq + sub;
-                    // bf16 to f16 under a power of two for the row: its largest element goes to [2^14, 2^15),
-                    // so that only what is 2^-28 of it or less loses bits
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    float x[8], top = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[2 * j] = bf16_lo(u[j]);
-                        x[2 * j + 1] = bf16_hi(u[j]);
-                        const float m0 = fabsf(x[2 * j]), m1 = fabsf(x[2 * j + 1]);
-                        top = m0 < __uint_as_float(0x7F800000u) ? fmaxf(top, m0) : top;
-                        top = m1 < __uint_as_float(0x7F800000u) ? fmaxf(top, m1) : top;
-                    }
-#pragma unroll
-                    for (int o = qc / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;  // x / 2^e
-                    e = max(-126, min(113, top == 0.f ? 0 : e));
-                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                    w[i] = make_uint4(f16x2(x[0] * f, x[1] * f), f16x2(x[2] * f, x[3] * f), f16x2(x[4] * f, x[5] * f),
-                                      f16x2(x[6] * f, x[7] * f));
-                    if (piece == 0) arow[r] = k2 * __uint_as_float((uint32_t)(127 + e) << 23);
-                    sts16(q_at + r * 128 + ((piece ^ r) & 7) * 16, w[i]);
-                }
+            for (int r = sub; r < N; r += rpq) {
+                const bool in = r < rows && piece * 8 < c.D;
+                cp16(q_at + r * 128 + ((piece ^ r) & 7) * 16, in ? row_of(r) : a.q, in ? 16u : 0u);
             }
-            }
+            cp_wait_all();
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + si % QB);
@@ -817,14 +835,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
                 const int32_t pages = next;
                 if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, g.L);
-                if constexpr (Q8) {
-                    const uint32_t slot = kt % RK;
-                    if (kt >= RK) wait(raw_empty + slot, (kt / RK - 1) & 1);
-                    bring(&p.k_map, smem_addr(raw_sm) + slot * (kTileTok * 128), raw_full + slot, table, at, g.L, g.h, pages);
-                } else {
-                    const uint32_t slot = kt % SK;
-                    if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
-                    bring(&p.k_map, smem_addr(smem) + slot * X::slot_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                const uint32_t slot = kt % SK;
+                if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
+                bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                if constexpr (!Q8) {
                     // which positions are there
                     uint32_t* const aux = (uint32_t*)aux_of(kt);
 #pragma unroll
@@ -900,9 +914,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, L);
                         if constexpr (Q8) {
                             const uint32_t slot = kt % RV;
-                            if (kt >= RV) wait(raw_empty + RK + slot, (kt / RV - 1) & 1);
-                            bring(&p.v_map, smem_addr(raw_sm) + (RK + slot) * (kTileTok * 128), raw_full + RK + slot, table, at, L, h,
-                                  pages);
+                            if (kt >= RV) wait(raw_empty + slot, (kt / RV - 1) & 1);
+                            bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages);
                         } else {
                             const uint32_t slot = kt % SV;
                             if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
