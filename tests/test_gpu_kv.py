@@ -300,6 +300,38 @@ def test_attend_growing_scores(sv, dtype):
         c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_queries_of_wide_range(sv, dtype, D):
+    """An element far above a row's others takes nothing from them: keys are zero where it stands, so that the scores
+    are the small ones' alone, and the bound counts those."""
+    c = Case(lens=[150, 40], tokens=[9, 3], H=2, G=4, D=D, dtype=dtype)
+    spike = torch.randint(D, (c.rows, 8), generator=c.g)
+    c.q.scatter_(2, spike[..., None], torch.full((c.rows, 8, 1), 2.0**16, dtype=torch.bfloat16))
+    for row in range(c.rows):
+        for head in range(8):
+            c.k[..., head // 4, spike[row, head]] = 0
+    c.attend(sv)
+    assert c.status.tolist() == [0, 0]
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_attend_query_that_is_not_finite(sv, dtype, value):
+    """Its own row is NaN, and no other."""
+    make = lambda: Case(lens=[150, 40], tokens=[9, 3], H=2, G=4, D=128, dtype=dtype, q_scale=2.0)  # noqa: E731
+    clean, c = make(), make()
+    c.q[4, 5, 77] = value
+    c.attend(sv)
+    out, lse, av, mag, spread = clean.expected()
+    got = c.out.double().cpu().numpy()
+    keep = np.ones(got.shape[:2], dtype=bool)
+    keep[4, 5] = False
+    assert np.isnan(got[4, 5]).all()
+    assert (np.abs(got - out) <= clean.bound(out, av, mag, spread))[keep].all()
+
+
 def _unseen_values(c, value):
     """`value` in the keys and values of the last new token of every sequence (which only it sees)."""
     code = 127 if c.dtype == "e4m3" else value
