@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int64_t before = 0, W = 0;
+    const int32_t holders = (c.B + 32 * per_thr - 1) / (32 * per_thr);  // warps with sequences
 #pragma unroll 1
-    for (int w = 0; w < kAttThreads / 32; ++w) {
+    for (int w = 0; w < holders; ++w) {
         const int64_t x = scan[w];
         before += w < warp ? x : 0;
         W += x;
@@ -475,18 +476,17 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(u0 + per, W);
     if (u0 < u1 && pre <= u0 && u0 < pre + mine) {
         int64_t at = pre;
+        int32_t b = bt0;
 #pragma unroll 1
-        for (int32_t b = bt0; b < bt1; ++b) {
+        for (; b + 1 < bt1; ++b) {
             KvSeq s;
             int32_t tiles, nrt;
             const int64_t k = Walk<N>::count(a, b, s, tiles, nrt);
-            if (u0 < at + k) {
-                scan[32] = b;
-                scan[33] = at;
-                break;
-            }
+            if (u0 < at + k) break;
             at += k;
         }
+        scan[32] = b;
+        scan[33] = at;
     }
     tc_before();
     __syncthreads();

@@ -1,6 +1,8 @@
 // kv.cu -- the paged key-value cache: writing new tokens (with quantisation),
 // reading back, keeping a tree's accepted path, and the plain attention that
 // takes the shapes attend.cu does not.
+#include <algorithm>
+
 #include "kv.cuh"
 
 namespace specv {
@@ -428,20 +430,36 @@ __global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c,
 }
 
 // ------------------------------------------------------------ plain attention
-// One warp for each query row (token, query head), float32 throughout: 32
-// positions at a time, a lane's position's product with the query in shared
-// memory, the running maximum and sum over the warp, then the weighted values
-// with the head's columns spread over the lanes.
-constexpr int kPlainWarps = 4;
+// For head_dim above 128. A CTA for each query row (token, query head), float32
+// throughout: its warps take 32 positions at a time in turn, a lane's
+// position's product with the query in shared memory, the running maximum and
+// sum over the warp, then the weighted values with eight of the head's columns
+// to a lane; the warps' sums are joined at the end. Bound by its 16-byte loads'
+// latency and by every query row reading the cache for itself.
+constexpr int kPlainWarps = 8;
 
-__device__ __forceinline__ float entry_at(const KvView& c, const unsigned char* row, int d) {
-    return c.esz == 2 ? bf16_lo(*(const uint16_t*)(row + 2 * d)) : kv_e4m3(row[d]);
+// Eight elements of an entry from `d` on.
+__device__ __forceinline__ void entry_at(const KvView& c, const unsigned char* row, int d, float (&x)[8]) {
+    if (c.esz == 2) {
+        load8<kKvBf16>(row, d / 8, x);
+        return;
+    }
+    const uint2 w = *(const uint2*)(row + d);
+    const uint32_t h2[4] = {e4m3_f16x2(w.x & 0xFFFF), e4m3_f16x2(w.x >> 16), e4m3_f16x2(w.y & 0xFFFF), e4m3_f16x2(w.y >> 16)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*(const __half2*)&h2[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+    }
 }
 
 __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const KvAttend p) {
-    __shared__ float q_sh[kPlainWarps][kKvMaxDim];
-    __shared__ uint32_t anc[kPlainWarps][kKvMaxQueries / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) float q_sh[kKvMaxDim];
+    __shared__ float o_sh[kPlainWarps][kKvMaxDim], m_sh[kPlainWarps], l_sh[kPlainWarps];
+    __shared__ uint32_t anc[kKvMaxQueries / 32];
+    static_assert(kKvMaxDim == 256 && kPlainWarps * 32 == kKvMaxDim, "eight columns to a lane, one to a thread");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const KvView& c = p.c;
     const int32_t b = blockIdx.x;
     const KvSeq s = kv_seq(b, p.row_off, p.t_max, p.rows, p.kv_lens, c.bs, c.max_blocks, true);
@@ -458,76 +476,98 @@ __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const
         const int32_t st2 = st == kKvOk ? check_pages(c, b, 0, s.T ? s.L : 0) : st;
         if (lane == 0) p.seq_status[b] = st2;
     }
-    const int64_t w = (int64_t)blockIdx.y * kPlainWarps + warp;
-    if (s.lo < 0 || w >= (int64_t)s.T * p.Hq) return;
-    const int32_t t = (int32_t)(w / p.Hq), hq = (int32_t)(w % p.Hq), h = hq / p.G;
-    const int64_t row = s.lo + t;
-    unsigned char* out = p.out + (row * p.Hq + hq) * (int64_t)c.D * 2;
+    if (s.lo < 0) return;
     const float none = __uint_as_float(0xFF800000u);
-    if (st != kKvOk) {
-        for (int d = lane; d < c.D; d += 32) *(uint16_t*)(out + 2 * d) = 0;
-        if (p.lse && lane == 0) p.lse[row * p.Hq + hq] = none;
-        return;
-    }
-    const unsigned char* q = p.q + row * p.q_row_bytes + (int64_t)hq * c.D * 2;
-    for (int d = lane; d < c.D; d += 32) q_sh[warp][d] = bf16_lo(*(const uint16_t*)(q + 2 * d));
-    if (lane < kKvMaxQueries / 32) anc[warp][lane] = 0;
-    __syncwarp();
+    const bool column = lane * 8 < c.D;
     const int32_t ctx = s.L - s.T;
-    if (p.parent && lane == 0)
-        for (int32_t v = t; v >= 0; v = p.parent[s.lo + v]) anc[warp][v >> 5] |= 1u << (v & 31);
-    __syncwarp();
-    float m = none, l = 0.f, o[kKvMaxDim / 32];
-#pragma unroll
-    for (int j = 0; j < kKvMaxDim / 32; ++j) o[j] = 0.f;
     const float k2 = p.scale * kLog2e;
-    const int32_t last = p.parent ? s.L : ctx + t + 1;  // positions past it are not seen
-    for (int32_t j0 = 0; j0 < last; j0 += 32) {
-        const int32_t j = j0 + lane;
-        float x = none, vscale = 1.f;
-        int64_t at = -1;
-        if (j < last && (!p.parent || j < ctx || (anc[warp][(j - ctx) >> 5] >> ((j - ctx) & 31) & 1))) {
-            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j / c.bs];
-            const int32_t sl = j % c.bs;
-            if (pg >= 0 && pg < c.num_blocks) {
-                at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
-                float acc = 0.f;
-                for (int d = 0; d < c.D; ++d) acc = fmaf(q_sh[warp][d], entry_at(c, c.k + at, d), acc);
-                if (c.ks) {
-                    const int64_t sc = ((int64_t)pg * c.H + h) * c.bs + sl;
-                    acc *= c.ks[sc];
-                    vscale = c.vs[sc];
+    for (int64_t w = blockIdx.y; w < (int64_t)s.T * p.Hq; w += gridDim.y) {
+        const int32_t t = (int32_t)(w / p.Hq), hq = (int32_t)(w % p.Hq), h = hq / p.G;
+        const int64_t row = s.lo + t;
+        unsigned char* out = p.out + (row * p.Hq + hq) * (int64_t)c.D * 2;
+        if (st != kKvOk) {
+            if (tid < c.D) *(uint16_t*)(out + 2 * tid) = 0;
+            if (p.lse && tid == 0) p.lse[row * p.Hq + hq] = none;
+            continue;
+        }
+        const unsigned char* q = p.q + row * p.q_row_bytes + (int64_t)hq * c.D * 2;
+        __syncthreads();  // the last row is done
+        if (tid < c.D) q_sh[tid] = bf16_lo(*(const uint16_t*)(q + 2 * tid));
+        if (tid < kKvMaxQueries / 32) anc[tid] = 0;
+        __syncthreads();
+        if (p.parent && tid == 0)
+            for (int32_t v = t; v >= 0; v = p.parent[s.lo + v]) anc[v >> 5] |= 1u << (v & 31);
+        __syncthreads();
+        float m = none, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int32_t last = p.parent ? s.L : ctx + t + 1;  // positions past it are not seen
+        for (int32_t j0 = warp * 32; j0 < last; j0 += kPlainWarps * 32) {
+            const int32_t j = j0 + lane;
+            float x = none, vscale = 1.f;
+            int64_t at = -1;
+            if (j < last && (!p.parent || j < ctx || (anc[(j - ctx) >> 5] >> ((j - ctx) & 31) & 1))) {
+                const int32_t pg = c.table[(int64_t)b * c.max_blocks + c.by_bs.of(j)];
+                const int32_t sl = j - c.by_bs.of(j) * c.bs;
+                if (pg >= 0 && pg < c.num_blocks) {
+                    at = pg * c.block_bytes + sl * c.token_bytes + h * c.head_bytes;
+                    float acc = 0.f;
+#pragma unroll 4
+                    for (int d = 0; d < c.D; d += 8) {
+                        float e[8];
+                        entry_at(c, c.k + at, d, e);
+                        const float4 q0 = *(const float4*)(q_sh + d), q1 = *(const float4*)(q_sh + d + 4);
+                        const float f[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) acc = fmaf(f[k], e[k], acc);
+                    }
+                    if (c.ks) {
+                        const int64_t sc = ((int64_t)pg * c.H + h) * c.bs + sl;
+                        acc *= c.ks[sc];
+                        vscale = c.vs[sc];
+                    }
+                    x = acc * k2;
                 }
-                x = acc * k2;
+            }
+            float mt = x;
+            for (int sh = 16; sh; sh >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, sh));
+            const float mn = fmaxf(m, mt);
+            const float mr = mn == none ? 0.f : mn;
+            const float f = exp2f(m - mr);
+            const float w2 = at >= 0 ? exp2f(x - mr) : 0.f;
+            float lt = w2;
+            for (int sh = 16; sh; sh >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, sh);
+            l = l * f + lt;
+            m = mn;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] *= f;
+            const float wv = w2 * vscale;
+#pragma unroll 4
+            for (int src = 0; src < 32; ++src) {
+                const int64_t a = __shfl_sync(0xFFFFFFFFu, at, src);
+                const float wt = __shfl_sync(0xFFFFFFFFu, wv, src);
+                if (a < 0 || !column) continue;
+                float e[8];
+                entry_at(c, c.v + a, lane * 8, e);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(wt, e[k], o[k]);
             }
         }
-        float mt = x;
-        for (int sh = 16; sh; sh >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, sh));
-        const float mn = fmaxf(m, mt);
-        const float mr = mn == none ? 0.f : mn;
-        const float f = exp2f(m - mr);
-        const float w2 = at >= 0 ? exp2f(x - mr) : 0.f;
-        float lt = w2;
-        for (int sh = 16; sh; sh >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, sh);
-        l = l * f + lt;
-        m = mn;
+        // the warps' sums, in their order
 #pragma unroll
-        for (int k = 0; k < kKvMaxDim / 32; ++k) o[k] *= f;
-        const float wv = w2 * vscale;
-        for (int src = 0; src < 32; ++src) {
-            const int64_t a = __shfl_sync(0xFFFFFFFFu, at, src);
-            const float wt = __shfl_sync(0xFFFFFFFFu, wv, src);
-            if (a < 0) continue;
-#pragma unroll
-            for (int k = 0; k < kKvMaxDim / 32; ++k)
-                if (k * 32 + lane < c.D) o[k] = fmaf(wt, entry_at(c, c.v + a, k * 32 + lane), o[k]);
+        for (int k = 0; k < 8; ++k) o_sh[warp][lane * 8 + k] = o[k];
+        if (lane == 0) m_sh[warp] = m, l_sh[warp] = l;
+        __syncthreads();
+        m = none;
+        for (int i = 0; i < kPlainWarps; ++i) m = fmaxf(m, m_sh[i]);
+        const float mr = m == none ? 0.f : m;
+        float sum = 0.f, x = 0.f;
+        for (int i = 0; i < kPlainWarps; ++i) {
+            const float f = exp2f(m_sh[i] - mr);
+            sum += f * l_sh[i];
+            x = fmaf(f, o_sh[i][tid], x);
         }
+        if (tid < c.D) *(uint16_t*)(out + 2 * tid) = (uint16_t)pack_bf16(sum == 0.f ? 0.f : x / sum, 0.f);
+        if (p.lse && tid == 0) p.lse[row * p.Hq + hq] = sum == 0.f ? none : (m + log2f(sum)) * 0.69314718055994531f;
     }
-    const float r = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int k = 0; k < kKvMaxDim / 32; ++k)
-        if (k * 32 + lane < c.D) *(uint16_t*)(out + 2 * (k * 32 + lane)) = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[k] * r, 0.f);
-    if (p.lse && lane == 0) p.lse[row * p.Hq + hq] = l == 0.f ? none : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 int lanes_log_of(int32_t D) {
@@ -575,8 +615,7 @@ cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s) 
 }
 
 cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s) {
-    const int64_t y = ((int64_t)p.t_max * p.Hq + kPlainWarps - 1) / kPlainWarps;
-    if (y > 65535) return cudaErrorInvalidValue;
+    const int64_t y = std::min<int64_t>((int64_t)p.t_max * p.Hq, 65535);
     kv_attend_plain_kernel<<<dim3((unsigned)p.c.B, (unsigned)y), kPlainWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
