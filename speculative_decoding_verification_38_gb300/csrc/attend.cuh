@@ -170,6 +170,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_warp(float x) {  // a NaN wins
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // a in the low half
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -330,6 +335,135 @@ struct Walk {
         }
     }
 };
+
+// Parts are joined in groups of kJoin, groups of groups and so on, each by whoever of its group comes last: joined by
+// one CTA alone, the 26 parts of 128 rows took it 50 us, as an SM has few bytes under way. Fewer rows, larger groups.
+template <int N>
+constexpr int kJoinLog = N <= 16 ? 5 : N <= 32 ? 4 : N <= 48 ? 3 : 2;
+
+// Joins `n` parts of an entry, CTAs c0 + i, c0 + i + step, .., into the first or (all of them) into the output. By the
+// softmax warps, a row each at a time, four columns to a lane. Out of line: its registers are not taken from the loop
+// over the tiles. Factors of the parts: with few rows a row's warp makes them beside its first loads (a single
+// sequence's call 14.2 us, 16.6 with the other way); with many, all of them are made first, in f_sm [n + 1][N], so that
+// the loads of two rows run together (calls of 25 to 55 us with 80 and 128 rows took 2 to 6 us less).
+struct Join {
+    const AttParams& p;
+    int32_t c0, i, step, n;
+    bool all;
+    int32_t rows, row0;
+    int64_t lo;
+    int32_t h;
+    __device__ __forceinline__ int64_t place(int32_t k, int N) const {
+        return ((int64_t)(c0 + i + k * step) * 2 + (i + k * step == 0)) * N;
+    }
+    __device__ __forceinline__ int64_t out_row(int r) const {
+        const int32_t rr = row0 + r, tk = p.a.by_G.of(rr);
+        return (lo + tk) * p.a.Hq + (int64_t)h * p.a.G + (rr - tk * p.a.G);
+    }
+    __device__ __forceinline__ void sums(int r, float M, float sum, int N) const {
+        if (!all)
+            p.part_ml[place(0, N) + r] = make_float2(M, sum);
+        else if (p.a.lse)
+            p.a.lse[out_row(r)] = sum == 0.f ? __uint_as_float(0xFF800000u) : (M + log2f(sum)) * 0.69314718055994531f;
+    }
+    __device__ __forceinline__ void row(int r, int lane, float4 o, float inv, int N) const {
+        if (!all) {
+            *((float4*)(p.part_o + (place(0, N) + r) * 128) + lane) = o;
+            return;
+        }
+        if (inv == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        *(uint2*)(p.a.out + (out_row(r) * p.a.c.D + lane * 4) * 2) =
+            make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+    }
+};
+__device__ __forceinline__ float larger(float x, float y) { return x > y || x != x ? x : y; }  // a NaN wins
+__device__ __forceinline__ void add(float4& o, float f, float4 x) {
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+}
+
+template <int N, bool Q8>
+__device__ __noinline__ void join_few(Join w) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool column = lane * 4 < w.p.a.c.D;
+    constexpr int UN = Q8 ? 4 : 8;  // parts at a time
+#pragma unroll 1
+    for (int r = warp; r < w.rows; r += kSoftWarps) {
+        const float2 ml = lane < w.n ? __ldcg(w.p.part_ml + w.place(lane, N) + r) : make_float2(kNoMax, 0.f);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f), x[UN];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < UN; ++k)  // (past the last one: the last again, not counted)
+                if (column) x[k] = __ldcg((const float4*)(w.p.part_o + (w.place(min(k0 + k, w.n - 1), N) + r) * 128) + lane);
+        };
+        load(0);
+        float M = ml.x;
+#pragma unroll
+        for (int b = 16; b; b >>= 1) M = larger(__shfl_xor_sync(0xFFFFFFFFu, M, b), M);
+        const float f = ex2(ml.x - M);
+        float sum = lane < w.n ? f * ml.y : 0.f;
+#pragma unroll
+        for (int b = 16; b; b >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, b);
+#pragma unroll 1
+        for (int k0 = 0;;) {
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+                if (k0 + k >= w.n) break;
+                add(o, __shfl_sync(0xFFFFFFFFu, f, k0 + k), x[k]);
+            }
+            if ((k0 += UN) >= w.n) break;
+            load(k0);
+        }
+        if (column) w.row(r, lane, o, sum == 0.f ? 0.f : 1.f / sum, N);
+        if (lane == 0) w.sums(r, M, sum, N);
+    }
+}
+
+template <int N>
+__device__ __noinline__ void join_many(Join w, float* f_sm) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    {
+        constexpr int lg = kJoinLog<N>;
+        static_assert((N << lg) <= kSoftThreads, "a thread for each (row, part)");
+        const int row = tid >> lg, r = min(row, w.rows - 1), k = tid & ((1 << lg) - 1);
+        const float2 ml = k < w.n ? __ldcg(w.p.part_ml + w.place(k, N) + r) : make_float2(kNoMax, 0.f);
+        float M = ml.x;
+#pragma unroll
+        for (int b = 1 << lg >> 1; b; b >>= 1) M = larger(__shfl_xor_sync(0xFFFFFFFFu, M, b), M);
+        const float f = ex2(ml.x - M);
+        float sum = k < w.n ? f * ml.y : 0.f;
+#pragma unroll
+        for (int b = 1 << lg >> 1; b; b >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, b);
+        if (row < w.rows) {
+            if (k < w.n) f_sm[k * N + r] = f;
+            if (k == 0) {
+                f_sm[w.n * N + r] = sum == 0.f ? 0.f : 1.f / sum;
+                w.sums(r, M, sum, N);
+            }
+        }
+    }
+    bar_sync(1 + kGroups, kSoftThreads);
+    if (lane * 4 >= w.p.a.c.D) return;
+#pragma unroll 2
+    for (int r = warp; r < w.rows; r += kSoftWarps) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = 0; k0 < w.n; k0 += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // (past the last one: the last again, not counted)
+                x[k] = __ldcg((const float4*)(w.p.part_o + (w.place(min(k0 + k, w.n - 1), N) + r) * 128) + lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= w.n) break;
+                add(o, f_sm[(k0 + k) * N + r], x[k]);
+            }
+        }
+        w.row(r, lane, o, f_sm[w.n * N + r], N);
+    }
+}
 
 template <int NN, int DP, bool Q8>
 __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
@@ -948,7 +1082,6 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
         const float k2 = a.scale * kLog2e;
         const float none = __uint_as_float(0xFF800000u);
-        auto larger = [](float x, float y) { return x > y || x != x ? x : y; };  // a NaN wins
         // eight values of each lane to one: lane's value (lane >> 2) over the warp, by halving what a lane holds
         auto over_warp = [&](float (&x)[8], auto op) {
 #pragma unroll
@@ -1016,8 +1149,9 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 if (tid < kKvMaxQueries) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        if (j * 32 >= T) break;
                         uint32_t by = 0;
-#pragma unroll 1
+#pragma unroll 4
                         for (int k = 0; k < 32; ++k) {
                             const uint32_t x = __ballot_sync(0xFFFFFFFFu, m[j] >> k & 1);
                             if (lane == k) by = x;
@@ -1119,9 +1253,14 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             tc_ld8(s_at + X::GT * m * 8, z);
                             tc_wait_ld(z);
                             relative(m, z, true);
-                            float y[8] = {z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y};
-                            const float x = over_warp(y, larger);
-                            if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = x;
+                            const float y[8] = {z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y};
+                            float x = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float top = max_warp(y[k]);
+                                x = lane == k ? top : x;
+                            }
+                            if (lane < 8) red[wq * MC * 8 + m * 8 + lane] = x;
                         }
                         bar_sync(bar_gr, 128);
                         if (Q8) {
@@ -1400,58 +1539,37 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (r0 + k < rows) p.part_o[(part * N + r0 + k) * 128 + wt] = o[k];
+                        if (r0 + k < rows && wt < c.D) p.part_o[(part * N + r0 + k) * 128 + wt] = o[k];
                 }
             }
             if (!whole) {
-                // ---- join: the entry's parts lie with CTAs c0 (its second place) and c0 + 1 .. c1 (their first)
-                const int32_t c0 = g->c0, c1 = g->c1;
-                __threadfence();
-                bar_sync(bar_all, kSoftThreads);
-                if (tid == 0) {
-                    const uint32_t k = atomicAdd(p.arrive + c0, 1u);
-                    *last_in = k == (uint32_t)(c1 - c0);
-                    if (k == (uint32_t)(c1 - c0)) p.arrive[c0] = 0;  // for the next call
+                // ---- join: the entry's parts lie with CTAs c0 (its second place) and c0 + 1 .. c1 (their first). A group
+                // counts its arrivals at its second member.
+                constexpr int lg = kJoinLog<N>;
+                const int32_t c0 = g->c0, parts = g->c1 - c0 + 1;
+                int32_t i = (int32_t)blockIdx.x - c0;
+#pragma unroll 1
+                for (int at = 0; 1 << at < parts; at += lg) {
+                    i = i >> (at + lg) << (at + lg);
+                    const int32_t k = min(1 << lg, (parts - i + (1 << at) - 1) >> at);
+                    if (k == 1) continue;
                     __threadfence();
-                }
-                bar_sync(bar_all, kSoftThreads);
-                if (*last_in && !skip) {
-                    // a warp for each row, four columns to a lane
-#pragma unroll 1
-                    for (int r = warp; r < rows; r += kSoftWarps) {
-                        float M = kNoMax;
-#pragma unroll 1
-                        for (int32_t j = c0 + lane; j <= c1; j += 32) {
-                            const float x = __ldcg(&p.part_ml[((int64_t)j * 2 + (j == c0)) * N + r].x);
-                            M = x > M || x != x ? x : M;
-                        }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) {
-                            const float x = __shfl_xor_sync(0xFFFFFFFFu, M, o);
-                            M = x > M || x != x ? x : M;
-                        }
-                        float sum = 0.f;
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                        for (int32_t j = c0; j <= c1; ++j) {
-                            const int64_t at = ((int64_t)j * 2 + (j == c0)) * N + r;
-                            const float2 ml = __ldcg(p.part_ml + at);
-                            const float4 x = __ldcg((const float4*)(p.part_o + at * 128) + lane);
-                            const float f = ex2(ml.x - M);
-                            sum = fmaf(f, ml.y, sum);
-                            o.x = fmaf(f, x.x, o.x);
-                            o.y = fmaf(f, x.y, o.y);
-                            o.z = fmaf(f, x.z, o.z);
-                            o.w = fmaf(f, x.w, o.w);
-                        }
-                        const float f = sum == 0.f ? 0.f : 1.f / sum;
-                        if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const int64_t out = out_row(r);
-                        if (lane * 4 < c.D)
-                            *(uint2*)(a.out + (out * c.D + lane * 4) * 2) =
-                                make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
-                        if (a.lse && lane == 0) a.lse[out] = sum == 0.f ? none : (M + log2f(sum)) * 0.69314718055994531f;
+                    bar_sync(bar_all, kSoftThreads);
+                    if (tid == 0) {
+                        uint32_t* const arrive = p.arrive + c0 + i + (1 << at);
+                        const bool last = atomicAdd(arrive, 1u) == (uint32_t)k - 1;
+                        *last_in = last;
+                        if (last) *arrive = 0;  // for the next call
+                        __threadfence();
                     }
+                    bar_sync(bar_all, kSoftThreads);
+                    if (!*last_in) break;
+                    if (skip) continue;
+                    const Join w{p, c0, i, 1 << at, k, 1 << (at + lg) >= parts, rows, row0, g->lo, g->h};
+                    if constexpr (N <= 16)
+                        join_few<N, Q8>(w);
+                    else
+                        join_many<N>(w, (float*)p_sm);
                 }
             }
             bar_sync(bar_all, kSoftThreads);  // scratch and row state are the next segment's
