@@ -487,9 +487,11 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64
  * the new tokens that are itself or an ancestor by parent (local node
  * indices, -1 for node 0, as spec_tree_verify's). What a token does not see
  * has no effect on it, a NaN or an infinity there included. A token whose
- * every s_j is -inf gets zeros and lse -inf. Statistics and sums are float32;
- * products run on the tensor cores with a query and a weight each rounded to
- * 16 bits or held as a sum of parts no less exact.
+ * every s_j is -inf gets zeros and lse -inf. Statistics and sums are float32.
+ * Up to head_dim 128 the products run on the tensor cores: SPEC_BF16 with
+ * queries as they are and weights as two bf16 parts (16 bits); SPEC_E4M3 with
+ * queries exact down to 2^-24 of their row's largest element (the rest to
+ * 2^-31 of it) and weights in fp16.
  * seq_status (may be NULL): LAYOUT (offsets outside [0, rows] or falling,
  * T_b > t_max, a bad parent, or a page outside the pool, whose positions are
  * then left out), KV (kv_lens[b] < T_b or past the table), TIMEOUT (a bounded

@@ -5,13 +5,36 @@
 // the matrix instruction, S^T = K Q^T [128 x N] and O^T += V^T P^T [head_dim x
 // N], N being the query rows (new tokens times the query heads of a key-value
 // head). So the long side fills the instruction whatever the number of query
-// rows, one token to a whole tree, and work grows with N only.
+// rows, one token to a whole tree, and work grows with N only: 16 rows of one
+// token would use an eighth of an instruction that has them as its rows.
 //
 // The flat list of tiles over (sequence, head, row tile) is cut into one equal
 // run for each CTA (one CTA on each SM). A CTA that holds a whole (sequence,
 // head, row tile) writes its rows; one that holds a part leaves its sums in the
-// workspace, and the last CTA of that list entry to arrive joins the parts in
-// their order.
+// workspace, and groups of parts are joined by whoever comes last, in a fixed
+// order.
+//
+// Arithmetic. Scores, maxima, sums and outputs are float32. bf16 caches: a
+// weight goes to the second product as two bf16 parts, 16 bits of it, so that
+// the result has the output's own rounding and no second one; the second
+// product has twice the columns for it. e4m3 caches: K is the first product's
+// operand as it is and the queries its equal in three e5m2 parts, which hold
+// all 8 bits of a bf16 number; V turns to f16, exactly, in shared memory, and
+// weights are f16 (11 bits). Scales of K go to the scores and of V to the
+// weights.
+//
+// Bounds (8 heads of 128, pages of 16). Nine bf16 tokens of each of 64
+// sequences over 146,153 positions: 118 us for 608 MB, 0.76 of the copy
+// bandwidth; of two over 262,142: 182 us, 0.87. The difference is the ends of
+// entries, where a CTA's groups wait for the last of its tiles (about 12,000
+// cycles, four or five times in a run). Trees of 29 (116 rows): 180 us, 0.52;
+// the softmax groups' instructions (about 65 for eight weights) and one place
+// for P, as two parts of 128 rows take 64 KB. e4m3, one token of each of the
+// 64: 105 us for 310 MB, 0.43, and ragged chains of up to 72 rows 939 us for
+// 2.2 GB, 0.35: the same instructions and ends, and half the bytes for each
+// weight. A single sequence of 4,111: 14 us, of which launch, start (the list,
+// TMEM) and the chain page number - tile - score - weight - product - join are
+// latency.
 #pragma once
 
 #include <cuda.h>
@@ -222,7 +245,10 @@ struct Shape {
     static constexpr int N = NN;                           // query rows of a row tile
     static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory and TMEM are full
     // Teams of softmax groups take the tiles in turn, each with sums of its own, so that a tile may take a team as
-    // long as `TM` tiles take the loads; the groups of a team share the rows.
+    // long as `TM` tiles take the loads; the groups of a team share the rows. With few rows a tile is mostly latency
+    // (teams took 9 tokens x 64 from 166 to 155 us, one e4m3 token x 64 from 174 to 120); with 80 e4m3 rows two teams
+    // of five pieces a thread were slower than one of three (1212 us against 1019), and 80 bf16 rows have no place for
+    // two teams' P.
     static constexpr int TM = N <= 32 ? 4 : N == 48 ? 2 : 1;
     static constexpr int GT = kGroups / TM;                // groups of a team
     static constexpr int SB = TM == 1 ? 2 : TM;            // score tiles in TMEM
@@ -264,7 +290,7 @@ struct Shape {
 };
 
 // The flat list of tiles. An entry counts kOver more than its tiles, at its front, for what opening and closing it
-// costs; CTA i has [i * per, (i + 1) * per).
+// costs; CTA i has [i * per, (i + 1) * per). (Counting tiles only: trees of 64 sequences 258 us, with this 199.)
 constexpr int kOver = 5;
 
 // Kept out of line: the few places that divide 64-bit numbers do so once in a while, and their code is large.
@@ -1068,7 +1094,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         // every GT-th 8-row piece of the query rows. A weight is 2^(score - m) with m a
         // reference that starts as the row's maximum in its first tile and moves
         // only when a later score passes it by 2^grow: a weight in bf16 parts or
-        // float32 sums may be that large (2^60), one in f16 less (2^8).
+        // float32 sums may be that large (2^60), one in f16 less (2^8: its 2^14
+        // below f16's largest, 2^-30 of a row's largest weight above f16's least).
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
@@ -1082,17 +1109,17 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
         const float k2 = a.scale * kLog2e;
         const float none = __uint_as_float(0xFF800000u);
-        // eight values of each lane to one: lane's value (lane >> 2) over the warp, by halving what a lane holds
-        auto over_warp = [&](float (&x)[8], auto op) {
+        // eight sums over the warp, lane's the one of value lane >> 2, by halving what a lane holds
+        auto over_warp = [&](float (&x)[8]) {
 #pragma unroll
             for (int h = 4; h; h >>= 1) {
                 const bool hi = lane & (4 * h);
 #pragma unroll
                 for (int k = 0; k < h; ++k)
-                    x[k] = op(hi ? x[k + h] : x[k], __shfl_xor_sync(0xFFFFFFFFu, hi ? x[k] : x[k + h], 4 * h));
+                    x[k] = (hi ? x[k + h] : x[k]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? x[k] : x[k + h], 4 * h);
             }
-            x[0] = op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 2));
-            return op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], 1));
+            x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 2);
+            return x[0] + __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
         };
         uint32_t gt = 0;
         int32_t tree_of = -1;  // the sequence whose ancestors are known
@@ -1456,7 +1483,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 for (int m = 0; m < MC; ++m)
                     if (m < live) {
                         float x[8] = {l[m][0].x, l[m][0].y, l[m][1].x, l[m][1].y, l[m][2].x, l[m][2].y, l[m][3].x, l[m][3].y};
-                        const float sum = over_warp(x, [](float u, float v) { return u + v; });
+                        const float sum = over_warp(x);
                         if ((lane & 3) == 0) red[wq * MC * 8 + m * 8 + (lane >> 2)] = sum;
                     }
                 bar_sync(bar_gr, 128);

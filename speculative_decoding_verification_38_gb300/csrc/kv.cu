@@ -104,7 +104,9 @@ __device__ __forceinline__ void write_entry(const float (&x)[8], bool live, unsi
     if (i == 0) *scale = pow2(e);
 }
 
-constexpr int kRows = 2;  // entries (row, head) of a thread: their loads are under way together
+// Entries (row, head) of a thread: their loads are under way together. Append of 130,238 e4m3 prompt tokens and gather
+// of 146,153 tokens: two 178 and 142 us, four 184 and 145.
+constexpr int kRows = 2;
 
 // The same for eight bf16 values as they come (w), where all of the warp's are
 // finite: their magnitudes compare as 16-bit integers, two at a time, and a
@@ -146,6 +148,9 @@ __device__ __forceinline__ void write_codes(const uint32_t (&w)[4], bool live, u
 // offsets and steps on from there. A thread asks for its values first, so that
 // the offsets, lengths and page numbers, each needing the last, come in their
 // shadow. The grid's last CTAs write the statuses, one warp for each sequence.
+// bf16 to bf16 HBM bounds it; to e4m3 the instructions of the conversion do:
+// 130,238 tokens of 8 heads in 178 us, 4.5 TB/s (0.67 of the copy bandwidth).
+// A round's 576 tokens: 3.8 us of latency (offsets, length, page, store).
 template <int DT, bool Q8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const KvNew n, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
@@ -228,6 +233,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
 
 // The cache back as rows: value = code * scale. Threads and entries as above;
 // a thread's entries are all looked up, then all asked for, then written.
+// Bound by HBM: 146,153 tokens of 8 heads from e4m3 in 142 us, 6.4 TB/s (0.94).
 template <bool Q8, int ODT>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, const KvRead g, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
@@ -342,7 +348,8 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, con
 // rise (path[i] >= i + 1), so entry i's target, slot 1 + i, is read by no
 // later entry: taken in order, each thread's column moves in place. A thread
 // owns one 16-byte column (or one scale) of one layer and head, and takes the
-// path kMove entries at a time: loads together, then stores.
+// path kMove entries at a time: loads together, then stores (of 64 trees in 32
+// layers 8.3 us; one at a time 12.3). Bound by latency: path, pages, entries.
 constexpr int kMove = 4;
 __global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c, const KvMove m) {
     __shared__ int64_t from[kMove], to[kMove];    // page * block + slot * token, bytes
