@@ -283,6 +283,20 @@ def test_attend_many_short_sequences(sv, dtype, G, D, t):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,D,t", [(4, 128, 4), (8, 64, 4), (3, 96, 15), (5, 128, 16), (4, 128, 32), (2, 64, 64)])
+def test_attend_one_entry_over_many_processors(sv, dtype, G, D, t):
+    """Every size of row tile with an entry in 40 parts and one in a few: groups of parts, and groups of groups."""
+    c = Case(lens=[5003, 390], tokens=[t, t], H=1, G=G, D=D, dtype=dtype, q_scale=2.0)
+    c.attend(sv)
+    assert c.status.tolist() == [0, 0]
+    c.check()
+    first = c.out.clone()
+    for _ in range(3):
+        c.attend(sv)
+        assert torch.equal(first, c.out)  # whoever joins them: the same bits
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attend_growing_scores(sv, dtype):
     """Scores that rise along the cache (every tile a new maximum), then fall."""
     for sign in (1, -1):
