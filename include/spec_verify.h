@@ -470,7 +470,9 @@ SPEC_API spec_status_t spec_kv_gather(const spec_kv_cache_t* cache, int32_t laye
  * seq_status (may be NULL): LAYOUT (offsets, N_b < 1, accepted outside
  * [0, N_b), a path that does not rise or leaves the tree, a page outside the
  * pool), KV (kv_lens_in[b] < N_b or past the table); such a sequence moves
- * nothing and keeps its length. kv_lens_out may alias kv_lens_in. */
+ * nothing and keeps its length. kv_lens_out may be kv_lens_in (the lengths are
+ * then written by a second launch where a sequence takes several CTAs), but
+ * must not overlap it otherwise. */
 SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64_t* node_off, int64_t nodes,
                                        const int32_t* path, const int32_t* accepted, const int32_t* kv_lens_in,
                                        int32_t* kv_lens_out, int32_t* out_num_blocks, int32_t* seq_status,

@@ -350,6 +350,8 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, con
 // owns one 16-byte column (or one scale) of one layer and head, and takes the
 // path kMove entries at a time: loads together, then stores (of 64 trees in 32
 // layers 8.3 us; one at a time 12.3). Bound by latency: path, pages, entries.
+// Each CTA of a sequence reads its old length; the first writes the new one
+// (m.part says whether that is this launch's to do, see launch_kv_compact).
 constexpr int kMove = 4;
 __global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c, const KvMove m) {
     __shared__ int64_t from[kMove], to[kMove];    // page * block + slot * token, bytes
@@ -381,13 +383,13 @@ __global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c,
         if (__syncthreads_or(bad)) st = kKvBadLayout;
         moves = __syncthreads_or(moves);
     }
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (m.part != kMoveEntries && blockIdx.y == 0 && threadIdx.x == 0) {
         const int32_t out = st == kKvOk ? L - (N - 1 - a) : L;
         m.kv_out[b] = out;
         if (m.out_blocks) m.out_blocks[b] = (int32_t)(((int64_t)out + c.bs - 1) / c.bs);
         if (m.seq_status) m.seq_status[b] = st;
     }
-    if (st != kKvOk || !moves) return;  // the first children all the way: every entry is in its place
+    if (st != kKvOk || !moves || m.part == kMoveLengths) return;  // the first children all the way: every entry is in its place
     const int32_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);  // 16-byte columns of an entry, and its scale
     const uint32_t all = (uint32_t)c.layers * c.H * 2 * cols;  // the host keeps it below 2^31
     const uint32_t t = blockIdx.y * kThreads + threadIdx.x;
@@ -617,7 +619,16 @@ cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s) 
     const int64_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);
     const int64_t y = ((int64_t)c.layers * c.H * 2 * cols + kThreads - 1) / kThreads;
     if (y > 65535) return cudaErrorInvalidValue;
-    kv_compact_kernel<<<dim3((unsigned)c.B, (unsigned)y), kThreads, 0, s>>>(c, m);
+    // Lengths cut in place: a CTA of the sequence that starts after the new length is written would take it for the old
+    // one and move other entries. With several CTAs to a sequence a launch of its own writes them, behind the moves.
+    const bool apart = y > 1 && m.kv_out == m.kv_in;
+    KvMove w = m;
+    w.part = apart ? kMoveEntries : kMoveAll;
+    kv_compact_kernel<<<dim3((unsigned)c.B, (unsigned)y), kThreads, 0, s>>>(c, w);
+    if (apart) {
+        w.part = kMoveLengths;
+        kv_compact_kernel<<<dim3((unsigned)c.B, 1), kThreads, 0, s>>>(c, w);
+    }
     return cudaGetLastError();
 }
 

@@ -69,7 +69,10 @@ struct KvRead {
     int32_t* seq_status;
 };
 
+enum KvMovePart : int32_t { kMoveAll = 0, kMoveEntries = 1, kMoveLengths = 2 };  // what a compaction's launch does
+
 struct KvMove {
+    int32_t part;  // KvMovePart, set by launch_kv_compact
     const int64_t* node_off;
     int64_t nodes;
     const int32_t* path;

@@ -1,0 +1,66 @@
+"""The paged cache's operators where they could go wrong and the other GPU tests do not reach, against the float64 oracle
+(oracle/kv.py); bounds from tests/kv_cases.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as okv
+from tests.kv_cases import Case, random_tree, tree  # noqa: F401
+from tests.test_gpu_kv import _append, _same_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verification_38_gb300 as sv
+
+    sv.build()
+    return sv
+
+
+# ------------------------------------------------------------------ compaction
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_lengths_in_place_with_more_ctas_than_are_resident(sv, dtype, in_place):
+    """kv_lens_out is kv_lens_in: every CTA of a sequence has to take the old length. 256 trees of 7 nodes in 32 layers
+    are 2,048 (bf16) CTAs and more, several waves of them."""
+    B, N = 256, 7
+    paths = [[6], [2, 6], [], [1, 3, 5], [4], [3, 4, 5, 6], [1, 2], [5, 6]]
+    paths = [paths[b % 8] for b in range(B)]
+    c = Case(lens=[N + (5 * b) % 11 for b in range(B)], tokens=[N] * B, H=4, D=64 if dtype == "bf16" else 112, bs=4,
+             dtype=dtype, layers=32)
+    c.to_device(sv)
+    flat = np.full(c.rows, -1, np.int32)
+    for b, p in enumerate(paths):
+        flat[b * N:b * N + len(p)] = p
+    acc = np.array([len(p) for p in paths], np.int32)
+    lens = c.dlens.clone()
+    out = lens if in_place else torch.full_like(lens, -7)
+    blocks, status = (torch.full((B,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    sv.check(sv.spec_kv_compact(c.cache, c.doff, torch.from_numpy(flat).cuda(), torch.from_numpy(acc).cuda(), lens, out,
+                                out_num_blocks=blocks, seq_status=status), "compact")
+    k, v, ks, vs = c.host()
+    want = okv.compact((k, v), (ks, vs), c.table, c.row_off, flat, acc, c.lens)
+    assert status.tolist() == [0] * B
+    assert out.tolist() == want.tolist() and blocks.tolist() == [-(-x // 4) for x in want.tolist()]
+    _same_cache(c, (k, v, ks, vs))
+
+
+def test_compact_in_place_keeps_the_length_of_a_bad_sequence(sv):
+    """Statuses and lengths of the second launch: a path that does not rise, a length too short, a page outside the pool."""
+    c = Case(lens=[20] * 5, tokens=[6] * 5, H=4, D=64, bs=4, layers=16)
+    c.to_device(sv)
+    before = c.raw(c.dk), c.raw(c.dv)
+    path = torch.tensor([[2, 2], [2, 4], [2, 4], [1, 2], [2, 9]], dtype=torch.int32, device="cuda")
+    path = torch.cat([path, torch.full((5, 4), -1, dtype=torch.int32, device="cuda")], 1).reshape(-1)
+    acc = torch.full((5,), 2, dtype=torch.int32, device="cuda")
+    lens = c.dlens.clone()
+    lens[1] = 5
+    c.dtable[2, 4] = 10**8
+    status = torch.full((5,), -7, dtype=torch.int32, device="cuda")
+    sv.check(sv.spec_kv_compact(c.cache, c.doff, path, acc, lens, lens, seq_status=status), "compact")
+    assert status.tolist() == [4, 2, 4, 0, 4]
+    assert lens.tolist() == [20, 5, 20, 17, 20]
+    np.testing.assert_array_equal(before[0], c.raw(c.dk))
+    np.testing.assert_array_equal(before[1], c.raw(c.dv))
