@@ -472,7 +472,8 @@ SPEC_API spec_status_t spec_kv_gather(const spec_kv_cache_t* cache, int32_t laye
  * pool), KV (kv_lens_in[b] < N_b or past the table); such a sequence moves
  * nothing and keeps its length. kv_lens_out may be kv_lens_in (the lengths are
  * then written by a second launch where a sequence takes several CTAs), but
- * must not overlap it otherwise. */
+ * must not overlap it otherwise. The 16-byte columns and scales of a token in
+ * all layers may number up to 65535 * 256 (more: SPEC_ERR_UNSUPPORTED). */
 SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64_t* node_off, int64_t nodes,
                                        const int32_t* path, const int32_t* accepted, const int32_t* kv_lens_in,
                                        int32_t* kv_lens_out, int32_t* out_num_blocks, int32_t* seq_status,

@@ -9,7 +9,7 @@ namespace specv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kKvThreads;
 
 // Status of each sequence, one warp each: the offsets and length by `st`,
 // then every page of positions [p0, L).
@@ -616,9 +616,8 @@ cudaError_t launch_kv_gather(const KvView& c, const KvRead& g, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s) {
-    const int64_t cols = c.D * c.esz / 16 + (c.ks ? 1 : 0);
-    const int64_t y = ((int64_t)c.layers * c.H * 2 * cols + kThreads - 1) / kThreads;
-    if (y > 65535) return cudaErrorInvalidValue;
+    const int64_t y = kv_compact_ctas(c.layers, c.H, c.D * c.esz, c.ks != nullptr);
+    if (y > kKvCompactMaxCtas) return cudaErrorInvalidValue;  // (refused by the caller)
     // Lengths cut in place: a CTA of the sequence that starts after the new length is written would take it for the old
     // one and move other entries. With several CTAs to a sequence a launch of its own writes them, behind the moves.
     const bool apart = y > 1 && m.kv_out == m.kv_in;

@@ -99,6 +99,12 @@ struct KvAttend {
     int32_t* seq_status;
 };
 
+// CTAs that a compaction gives each sequence: a thread for each 16-byte column, and each scale, of a token in all layers.
+constexpr int kKvThreads = 256;
+inline int64_t kv_compact_ctas(int64_t layers, int64_t kv_heads, int64_t entry_bytes, bool scales) {
+    return (layers * kv_heads * 2 * (entry_bytes / 16 + (scales ? 1 : 0)) + kKvThreads - 1) / kKvThreads;
+}
+constexpr int64_t kKvCompactMaxCtas = 65535;  // a grid's second axis
 cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvView& c, const KvRead& r, cudaStream_t s);
 cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s);

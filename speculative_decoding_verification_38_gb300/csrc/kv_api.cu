@@ -156,7 +156,9 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* c, const int64_t* 
     for (const void* p : {(const void*)path, (const void*)accepted, (const void*)kv_lens_in, (const void*)kv_lens_out,
                           (const void*)out_num_blocks, (const void*)seq_status})
         if (!aligned(p, 4)) return SPEC_ERR_ALIGNMENT;
-    if ((int64_t)c->layers * c->kv_heads > (1 << 18)) return SPEC_ERR_UNSUPPORTED;  // one launch's columns
+    const bool q8 = c->dtype == SPEC_E4M3;
+    if (kv_compact_ctas(c->layers, c->kv_heads, c->head_dim * (q8 ? 1 : 2), q8) > kKvCompactMaxCtas)
+        return SPEC_ERR_UNSUPPORTED;
     KvMove m;
     m.node_off = node_off;
     m.nodes = nodes;

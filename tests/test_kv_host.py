@@ -176,6 +176,19 @@ def test_compact_refusals(sv, at, value, status):  # noqa: F811
     assert sv.lib().spec_kv_compact(*a) == status
 
 
+@pytest.mark.parametrize("kw,columns", [
+    (dict(head_dim=256), 32), (dict(head_dim=8), 1), (dict(head_dim=256, dtype=2, k_scale=FAKE, v_scale=FAKE), 17),
+    (dict(head_dim=16, dtype=2, k_scale=FAKE, v_scale=FAKE), 2),
+])
+def test_compact_refuses_more_columns_than_a_launch_has(sv, kw, columns):  # noqa: F811
+    """A launch has 65535 CTAs of 256 threads for a sequence, one thread for each column of K and V, layer and head."""
+    most = 65535 * 256 // (2 * columns)
+    L = sv.lib()
+    for layers, heads in ((most + 1, 1), (most // 4 + 1, 4), (1 << 18, 65535)):
+        c = _cache(sv, layers=layers, kv_heads=heads, **kw)
+        assert L.spec_kv_compact(ctypes.byref(c), FAKE, 36, FAKE, FAKE, FAKE, FAKE, None, None, None) == 5
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(struct_size=8), 1), (dict(layer=2), 1), (dict(layer=-1), 1), (dict(q_heads=0), 1), (dict(q_heads=7), 1),
     (dict(t_max=0), 1), (dict(rows=37), 1), (dict(rows=-1), 1), (dict(row_off=None, rows=35), 1), (dict(kv_lens=None), 1),
