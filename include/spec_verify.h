@@ -494,7 +494,8 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64
  * Up to head_dim 128 the products run on the tensor cores: SPEC_BF16 with
  * queries as they are and weights as two bf16 parts (16 bits); SPEC_E4M3 with
  * queries exact down to 2^-24 of their row's largest element (the rest to
- * 2^-31 of it) and weights in fp16.
+ * 2^-31 of it) and weights times V's scales in fp16: 11 bits of what is 2^-19
+ * of the largest V scale the token sees or more (the rest to 2^-30 of that).
  * seq_status (may be NULL): LAYOUT (offsets outside [0, rows] or falling,
  * T_b > t_max, a bad parent, or a page outside the pool, whose positions are
  * then left out), KV (kv_lens[b] < T_b or past the table), TIMEOUT (a bounded

@@ -21,7 +21,7 @@
 // operand as it is and the queries its equal in three e5m2 parts, which hold
 // all 8 bits of a bf16 number; V turns to f16, exactly, in shared memory, and
 // weights are f16 (11 bits). Scales of K go to the scores and of V to the
-// weights.
+// weights, in units that go by the scales that a row sees.
 //
 // Bounds (8 heads of 128, pages of 16). Nine bf16 tokens of each of 64
 // sequences over 146,153 positions: 118 us for 608 MB, 0.76 of the copy
@@ -268,12 +268,12 @@ struct Shape {
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
     static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 6 : 8;  // tiles of them: more than the K ring and scores can hold
-    static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + 16;  // a group's scratch
-    // after the tiles, Q and P: aux ring, per team and row the reference, weight sum and factor, row factors of Q,
-    // scratch, ancestors, segments, poison, barriers
-    static constexpr uint32_t state = tight ? N * 4 : 3 * TM * N * 4;
+    static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + (Q8 ? 4 * MC * 8 : 0);  // a group's scratch
+    // after the tiles, Q and P: aux ring, per team and row the reference, weight sum, factor and (e4m3) unit, row factors
+    // of Q, scratch, ancestors, segments, poison, barriers
+    static constexpr uint32_t state = tight ? N * 4 : (Q8 ? 4 : 3) * TM * N * 4;
     static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
-                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 64) +
+                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 48) +
                                      (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * RV : 0)) * 8 +
                                      (2 * SB + 2 * PS + 5 + aux_ring + 2 * segs) * 8;
     static constexpr int room = (int)(kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc), fit = room / slot_bytes;
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     // [TM][N] each: weight sums and factors of the teams, used between segments (tight: in P, free then)
     float* const lsum = X::tight ? (float*)(p_sm + (N / 8 + 4) * 2048) : mref_all + TM * N;
     float* const fac = lsum + TM * N;
+    float* const unit_all = fac + TM * N;  // Q8: [TM][N] what a row's weights times V's scales are multiplied by for f16
     float* const arow_all = mref_all + X::state / 4;  // Q8: [R][N] a query row's power of two times scale * log2(e)
     unsigned char* const red_sm = (unsigned char*)(arow_all + (Q8 ? R * N : 0));
     uint32_t* const seen_by = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] the tokens that see a tree's token
@@ -517,8 +518,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     uint32_t* const last_in = poison + 6;
     uint32_t* const tree_bad = poison + 7;
     uint32_t* const last_seq = poison + 8;           // the last sequence of the run
-    float* const unit_of = (float*)(poison + 12);    // [kGroups] Q8: what a group's sums count in
-    uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 10 : 16));
+    uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 10 : 12));
     uint64_t* const v_full = k_full + SK;
     uint64_t* const k_empty = v_full + SV;
     uint64_t* const v_empty = k_empty + SK;
@@ -1094,8 +1094,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         // every GT-th 8-row piece of the query rows. A weight is 2^(score - m) with m a
         // reference that starts as the row's maximum in its first tile and moves
         // only when a later score passes it by 2^grow: a weight in bf16 parts or
-        // float32 sums may be that large (2^60), one in f16 less (2^8: its 2^14
-        // below f16's largest, 2^-30 of a row's largest weight above f16's least).
+        // float32 sums may be that large (2^60), one in f16 less (2^8). e4m3: a weight goes to f16 times V's scale and
+        // the row's unit u = 2^(6 - v), 2^v the smallest power of two that no scale the row has seen passes: at most
+        // 2^14 (f16's largest is 2^16), and f16's least is 2^-30 of a weight of one with that scale. The unit is a row's
+        // own, so that the scale of a new token that the row does not see leaves no trace in it.
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
@@ -1105,6 +1107,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;
         unsigned char* const pw0 = p_sm + (wt >> 3) * 128 + (wt & 7) * 16;  // this thread's P, piece 0
         float* const mref = mref_all + team * N;
+        float* const unit = unit_all + team * N;
+        constexpr float first_unit = 0x1p106f;  // v = -100
         // the group's scratch [5][MC * 8]: its own, or in its second part of P while P is free
         float* const red = (float*)(X::tight ? p_sm + (N / 8 + gr) * 2048 : red_sm + gr * X::red_bytes);
         const float k2 = a.scale * kLog2e;
@@ -1135,6 +1139,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             // ---- per-row state
             if (tid < TM * N) mref_all[tid] = kNoMax;
             if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
+            if (Q8 && tid < TM * N) unit_all[tid] = first_unit;
             if (tid < 4) poison[tid] = 0;
             if (a.parent && g->b != tree_of) {
                 tree_of = g->b;
@@ -1195,8 +1200,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             for (int m = 0; m < MC; ++m)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) l[m][k] = make_float2(0.f, 0.f);
-            int32_t lv = -100;  // Q8: values count in units of 2^lv
 
+            // Q8: the rows' unit, which is one where every row sees every position: rows part only over new tokens, and no
+            // tile without those comes after them
+            float u_all = first_unit;
             const int first = (int)((team - gt) & (TM - 1));  // this team's first tile of the segment
 #pragma unroll 1
             for (int i = first; i < n; i += TM) {
@@ -1265,15 +1272,13 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         }
                     };
                     // the references to the maxima of this tile and before, the sums after them
+                    // (Q8: and the units to the scales seen)
                     auto refer = [&]() {
-                        int32_t up = 0;
-                        if (Q8) {
-                            // the smallest 2^lv that no scale passes
-                            const uint32_t w = __float_as_uint(fabsf(vs));
-                            int32_t e = (int32_t)(w >> 23) - 127 + ((w & 0x7FFFFFu) ? 1 : 0);
-                            e = __reduce_max_sync(0xFFFFFFFFu, e);
-                            if (lane == 0) ((int32_t*)red)[5 * MC * 8 + wq] = e;
-                        }
+                        unsigned char* const seen_e = (unsigned char*)(red + 5 * MC * 8);  // Q8: [4][MC * 8] 127 + exponents
+                        const uint32_t vw = __float_as_uint(fabsf(vs));
+                        // of the smallest power of two not below this position's scale, 0 to 253 (no scale, 2^126 or more)
+                        const uint32_t e = min(253u, (vw >> 23) + ((vw & 0x7FFFFFu) ? 1u : 0u));
+                        const uint32_t tile_e = Q8 ? __reduce_max_sync(0xFFFFFFFFu, e) : 0u;
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
                             float2 z[4];
@@ -1288,29 +1293,45 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                                 x = lane == k ? top : x;
                             }
                             if (lane < 8) red[wq * MC * 8 + m * 8 + lane] = x;
+                            if (Q8) {
+                                uint32_t row_e = tile_e;
+                                if (masked)
+#pragma unroll 1
+                                    for (int k = 0; k < 8; ++k) {
+                                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, (vis >> (m * 8 + k) & 1) ? e : 0u);
+                                        row_e = lane == k ? top : row_e;
+                                    }
+                                if (lane < 8) seen_e[wq * MC * 8 + m * 8 + lane] = (unsigned char)row_e;
+                            }
                         }
                         bar_sync(bar_gr, 128);
-                        if (Q8) {
-                            const int32_t* e = (const int32_t*)red + 5 * MC * 8;
-                            up = min(126, max(lv, max(max(e[0], e[1]), max(e[2], e[3])))) - lv;
-                        }
                         if (wt < live * 8) {
                             const int r = (sub + X::GT * (wt >> 3)) * 8 + (wt & 7);
                             const float old = mref[r];
                             float m = old;
 #pragma unroll
                             for (int w = 0; w < 4; ++w) m = larger(red[w * MC * 8 + wt], m);
-                            red[4 * MC * 8 + wt] = ex2(old - m);
+                            const float f = ex2(old - m);
+                            red[4 * MC * 8 + wt] = f;
                             mref[r] = m;
+                            if (Q8) {
+                                // exponents as they are held: the unit's is 127 + 6 - v
+                                const uint32_t at = 260 - (__float_as_uint(unit[r]) >> 23);
+                                uint32_t to = at;
+#pragma unroll
+                                for (int w = 0; w < 4; ++w) to = max(to, (uint32_t)seen_e[w * MC * 8 + wt]);
+                                unit[r] = __uint_as_float((260 - to) << 23);
+                                // the sums shrink with it
+                                red[wt] = to - at > 126 ? 0.f : f * __uint_as_float((127 - (to - at)) << 23);
+                            }
                         }
                         bar_sync(bar_gr, 128);
-                        lv += up;
+                        if (Q8) u_all = unit[sub * 8];
                         if (i != first) {
                             if (PS != TM) {
                                 wait(pv_done + (t - 1) % PS, ((t - 1) / PS) & 1);
                                 tc_after();
                             }
-                            const float shrink = Q8 ? (up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23)) : 1.f;
 #pragma unroll
                             for (int m = 0; m < MC; ++m)
                                 if (m < live)
@@ -1326,7 +1347,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                                     tc_ld8(at, o);
                                     tc_wait_ld(o);
 #pragma unroll
-                                    for (int k = 0; k < 8; ++k) o[k] *= red[4 * MC * 8 + m * 8 + k] * shrink;
+                                    for (int k = 0; k < 8; ++k) o[k] *= red[(Q8 ? 0 : 4 * MC * 8) + m * 8 + k];
                                     tc_st8(at, o);
                                 }
                             tc_wait_st();
@@ -1344,8 +1365,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (due) refer();
                         due = false;
                         float top = none;
-                        // Q8: f16 in units that bring the largest possible one, 2^grow, to 2^14
-                        const float wv = Q8 ? vs * __uint_as_float((uint32_t)(127 + 6 - lv) << 23) : 1.f;
+                        const float wv = Q8 ? vs * u_all : 1.f;
+                        bool over = Q8 && !masked && fabsf(wv) > 64.f && u_all > 0x1p-120f;  // (it goes no lower)
                         // two pieces at a time, so that one's latencies hide the other's
 #pragma unroll
                         for (int m0 = 0; m0 < MC; m0 += 2) {
@@ -1377,14 +1398,17 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                                     l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
                                 }
                                 if (Q8) {
+                                    if (!masked) {
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
-                                    if (masked) {
+                                        for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
+                                    } else {
 #pragma unroll
                                         for (int k = 0; k < 4; ++k) {
                                             const int at = (m < live ? m : m0) * 8 + 2 * k;
+                                            z[k] = mul2(z[k], mul2(make_float2(vs, vs), *(const float2*)(unit + piece * 8 + 2 * k)));
                                             z[k].x = (vis >> at & 1) ? z[k].x : 0.f;
                                             z[k].y = (vis >> (at + 1) & 1) ? z[k].y : 0.f;
+                                            over |= fmaxf(fabsf(z[k].x), fabsf(z[k].y)) > 16384.f;
                                         }
                                     }
                                     *(uint4*)(pw + piece * 2048) = make_uint4(f16x2(z[0].x, z[0].y), f16x2(z[1].x, z[1].y),
@@ -1410,9 +1434,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             sign = 1.f;
                             continue;
                         }
-                        const float v_unit = Q8 ? __uint_as_float((uint32_t)(lv + 127) << 23) : 0.f;
                         // (after a move nothing passes the reference, so that a second one is never due)
-                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || (Q8 && fabsf(vs) > v_unit && lv < 126))) break;
+                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || over)) break;
                         sign = -1.f;
                     }
                     if (tail && sub == 0 && (pos >= L || (in && pos >= ctx && T > 1))) {
@@ -1490,7 +1513,6 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 if (wt < live * 8)
                     lsum[team * N + (sub + X::GT * (wt >> 3)) * 8 + (wt & 7)] =
                         red[wt] + red[MC * 8 + wt] + red[2 * MC * 8 + wt] + red[3 * MC * 8 + wt];
-                if (Q8 && wt == 0) unit_of[gr] = __uint_as_float((uint32_t)(127 + lv) << 23) * 0.015625f;
             }
             bar_sync(bar_all, kSoftThreads);
             if (tid < rows) {
@@ -1506,7 +1528,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
                 for (int tm = 0; tm < TM; ++tm)
-                    fac[tm * N + tid] = f[tm] * (whole ? inv : 1.f) * (Q8 ? unit_of[tm + TM * ((tid >> 3) % X::GT)] : 1.f);
+                    fac[tm * N + tid] = f[tm] * (whole ? inv : 1.f) * (Q8 ? __uint_as_float((254u << 23) - __float_as_uint(unit_all[tm * N + tid])) : 1.f);
                 if (!whole)
                     p.part_ml[part * N + tid] = make_float2(M, sum);
                 else if (a.lse && !skip)

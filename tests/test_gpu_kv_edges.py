@@ -64,3 +64,55 @@ def test_compact_in_place_keeps_the_length_of_a_bad_sequence(sv):
     assert lens.tolist() == [20, 5, 20, 17, 20]
     np.testing.assert_array_equal(before[0], c.raw(c.dk))
     np.testing.assert_array_equal(before[1], c.raw(c.dv))
+
+
+# ------------------------------------------------------------------ attention: scales of what a row does not see
+def _last_token_scale(c, value):
+    """V's scale of each sequence's last new token, in every head."""
+    for b in range(c.B):
+        j = c.lens[b] - 1
+        c.vs[c.layer, int(c.table[b, j // c.bs]), :, j % c.bs] = value
+
+
+def _sees_last(c):
+    """Rows whose token is a sequence's last: a chain's or a tree's last token is seen by itself alone."""
+    return np.isin(np.arange(c.rows), c.row_off[1:] - 1)
+
+
+@pytest.mark.parametrize("value", [2.0**20, 2.0**31, 2.0**40, 2.0**100, float("inf"), float("nan")])
+@pytest.mark.parametrize("as_tree", [False, True])
+@pytest.mark.parametrize("H,G,D,t", [(2, 1, 64, 5), (1, 4, 128, 8), (2, 4, 128, 9), (1, 8, 64, 9), (1, 4, 128, 29),
+                                     (1, 2, 256, 6)])
+def test_attend_unseen_value_scale(sv, value, as_tree, H, G, D, t):
+    """A large or non-finite V scale leaves no trace in rows that do not see its token: at the front of a tile, inside
+    one, alone in the last one, after many. Its own row has the entry's value, or is not finite; every lse stays right."""
+    lens = [t, t + 3, 128 + t, 128 + t - 1, 129, 300, 1025, 2000]
+    trees = [random_tree(t, 7 + b) for b in range(len(lens))]
+    c = Case(lens=lens, tokens=[t] * len(lens), H=H, G=G, D=D, dtype="e4m3", q_scale=2.0,
+             parent=sum(trees, []) if as_tree else None)
+    _last_token_scale(c, value)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * c.B
+    with np.errstate(invalid="ignore"):
+        out, lse, av, mag, spread = c.expected()
+    got, mine = c.out.double().cpu().numpy(), _sees_last(c)
+    if np.isfinite(value):
+        c.check()
+        return
+    assert not np.isfinite(got[mine]).any()
+    with np.errstate(invalid="ignore"):
+        far = np.abs(got - out) - c.bound(out, av, mag, spread)
+    assert np.isfinite(got[~mine]).all() and (far[~mine] <= 0).all(), np.nanmax(far[~mine])
+    es = 2.0**-23 * (D + 8) * mag + 2.0**-20  # as in Case.check
+    assert (np.abs(c.lse.double().cpu().numpy() - lse) <= es + 2.0**-21 * (1 + np.abs(lse)) + max(lens) * 2.0**-24).all()
+
+
+@pytest.mark.parametrize("G,t", [(1, 4), (8, 9), (4, 32)])
+def test_attend_value_scales_of_a_wide_range(sv, G, t):
+    """Scales from 2^-60 to 2^60 all over the cache, new tokens among them: a row's unit goes by what it sees, tile after
+    tile."""
+    c = Case(lens=[t, 40 + t, 260, 1500, 3000], tokens=[t] * 5, H=2, G=G, D=128, dtype="e4m3", q_scale=2.0)
+    c.vs[:] = torch.exp2(torch.randint(-60, 61, c.vs.shape, generator=c.g).float())
+    c.attend(sv)
+    assert c.status.tolist() == [0] * 5
+    c.check()
