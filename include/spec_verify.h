@@ -499,7 +499,8 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64
  * seq_status (may be NULL): LAYOUT (offsets outside [0, rows] or falling,
  * T_b > t_max, a bad parent, or a page outside the pool, whose positions are
  * then left out), KV (kv_lens[b] < T_b or past the table), TIMEOUT (a bounded
- * wait gave up; outputs unspecified). Rows of a sequence with bad offsets are
+ * wait gave up; outputs unspecified, and the workspace needs
+ * spec_workspace_init before its next call). Rows of a sequence with bad offsets are
  * not written; with another LAYOUT or KV error than a bad page, they are
  * zeros with lse -inf. */
 typedef struct {

@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     uint32_t* const tmem_at = poison + 5;
     uint32_t* const last_in = poison + 6;
     uint32_t* const tree_bad = poison + 7;
+    volatile uint32_t* const lost = poison + 9;      // a segment did not come to one of the softmax warps
     uint32_t* const last_seq = poison + 8;           // the last sequence of the run
     uint64_t* const k_full = (uint64_t*)(poison + (X::tight ? 10 : 12));
     uint64_t* const v_full = k_full + SK;
@@ -539,27 +540,41 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     const KvView& c = a.c;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
         const uint32_t t0 = nanoseconds();
 #pragma unroll 1
         while (!mbar_try_wait(bar, parity)) {
-            if (*aborted) return;
+            if (*aborted) return false;
             if (nanoseconds() - t0 > kAttWaitNs) *aborted = 1;
         }
+        return true;
     };
     // Once a wait has given up, every wait but those for segments returns at once, so that all roles run out in
-    // step: the same segments, the same named barriers, whatever the data.
-    auto wait_seg = [&](uint64_t* bar, uint32_t parity) {
+    // step: the same segments, the same named barriers, whatever the data. A role whose own wait gave up issues no more
+    // loads or products and gives no place of a loads' ring back, so that none goes where an earlier one may still be due.
+    auto wait_seg = [&](uint64_t* bar, uint32_t parity) -> bool {
         const uint32_t t0 = nanoseconds();
 #pragma unroll 1
-        while (!mbar_try_wait(bar, parity) && nanoseconds() - t0 < 2 * kAttWaitNs) {
-        }
+        while (!mbar_try_wait(bar, parity))
+            if (nanoseconds() - t0 > 2 * kAttWaitNs) {
+                *aborted = 1;
+                return false;
+            }
+        return true;
     };
-    // Segment s of this CTA, by every warp that works on it; done_seg gives its place back.
-    auto get_seg = [&](uint32_t s) {
-        wait_seg(seg_full + s % R, (s / R) & 1);
-        return segs + s % R;
+    // Tiles of segment s of this CTA (at segs + s % R), by every warp that works on it; none past the last segment or
+    // where it did not come. done_seg gives its place back.
+    auto tiles_of = [&](uint32_t s) -> int {
+        const bool here = wait_seg(seg_full + s % R, (s / R) & 1);
+        return __all_sync(0xFFFFFFFFu, here) ? segs[s % R].n : 0;
+    };
+    // The last loads of a ring have landed (a load under way must not outlive the CTA).
+    auto land = [&](uint64_t* full, uint32_t ring, uint32_t loads) {
+        if (elect())
+#pragma unroll 1
+            for (uint32_t t = loads > ring ? loads - ring : 0; t < loads; ++t) wait_seg(full + t % ring, (t / ring) & 1);
+        __syncwarp();
     };
     auto done_seg = [&](uint32_t s) {
         __syncwarp();
@@ -600,6 +615,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             mbar_init(seg_empty + i, kSoftWarps + (Q8 ? 2 + 8 : 3));
         }
         *aborted = 0;
+        *lost = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -702,10 +718,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             constexpr int qc = DP / 8, rpq = 32 / qc;  // 8-element pieces of a row, rows of one load
             static_assert(N / 4 % rpq == 0, "rows of a warp");
             const int piece = lane % qc, sub = lane / qc;
+            bool dead = false;
             for (uint32_t si = 0;; ++si) {
-                const Seg* const g = get_seg(si);
-                const int n = g->n;
+                const int n = tiles_of(si);
                 if (!n) break;
+                const Seg* const g = segs + si % R;
                 const int32_t L = g->L, h = g->h, row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
                 int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
                 const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
@@ -787,7 +804,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll 1
                 for (int t = 0; t < n; ++t, ++kt) {
                     const uint32_t slot = kt % SK;
-                    wait(k_full + slot, (kt / SK) & 1);  // in step with the K ring, so that the scales' is not overrun
+                    // in step with the K ring, so that the scales' is not overrun
+                    if (!wait(k_full + slot, (kt / SK) & 1)) dead = true;
                     unsigned char* const aux = aux_of(kt);
                     const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
                     if (lane == 0) ((uint32_t*)aux)[fw] = bits;
@@ -795,7 +813,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     ((float*)(aux + 16))[kTileTok + fw * 32 + lane] = sv;
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(k_empty + slot);
+                        if (!dead) mbar_arrive(k_empty + slot);
                         mbar_arrive(aux_full + kt % kAuxRing);
                     }
                     if (t + 1 < n) scales();
@@ -812,14 +830,15 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             const uint32_t at0 = smem_addr(v_sm) + fw * 32 * 128 + (my_chunk >> 2) * (kTileTok * 128) + my_row * 128 +
                                  ((2 * my_chunk ^ my_row) & 7) * 16;
             auto swizzled = [&](uint32_t base, int r, int more) { return (base ^ ((((r * rpr) & 7) ^ more) * 16)) + r * rpr * 128; };
+            bool dead = false;
             for (uint32_t si = 0;; ++si) {
-                const int n = get_seg(si)->n;
+                const int n = tiles_of(si);
                 if (!n) break;
                 done_seg(si);
 #pragma unroll 1
                 for (int t = 0; t < n; ++t, ++kt) {
                     const uint32_t from = kt % RV, slot = kt % SV;
-                    wait(raw_full + from, (kt / RV) & 1);
+                    if (!wait(raw_full + from, (kt / RV) & 1)) dead = true;
                     const uint32_t base = at0 + slot * X::slot_bytes;
                     auto unit_at = [&](int r) {
                         const int row = r * rpr + my_row;
@@ -847,7 +866,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     fence_async();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(raw_empty + from);
+                        if (!dead) mbar_arrive(raw_empty + from);
                         mbar_arrive(v_full + slot);
                     }
                 }
@@ -867,21 +886,22 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         // cursors over the segments.
         uint32_t qs = 0, qt = 0, ks = 0, kr = 0, vs = 0, vr = 0;  // segment, tile, ring places and rounds
         int qi = 0, qn = -1;
-        auto count_of = [&](uint32_t seg) { return __shfl_sync(0xFFFFFFFFu, get_seg(seg)->n, 0); };
+        bool dead = false;
+        auto count_of = [&](uint32_t seg) { return __shfl_sync(0xFFFFFFFFu, tiles_of(seg), 0); };
         auto scores = [&]() {  // of the next tile, if there is one
             if (qn == 0) return;
             if (qi >= qn) {
                 qn = count_of(qs);
                 if (!qn) return;
                 qi = 0;
-                wait(q_full + qs % QB, (qs / QB) & 1);
+                if (!wait(q_full + qs % QB, (qs / QB) & 1)) dead = true;
             }
             const uint32_t buf = qt % SB;
-            wait(k_full + ks, kr & 1);
+            if (!wait(k_full + ks, kr & 1)) dead = true;
             if (qt >= SB) wait(s_empty + buf, (qt / SB - 1) & 1);
             tc_after();
             ++qi;
-            if (elect()) {
+            if (elect() && !dead) {
                 const uint64_t ka = k_desc + ks * (X::k_bytes >> 4);
                 const uint64_t qd = q_desc + (qs % QB) * (X::q_bytes >> 4);
                 const uint32_t d = tmem + buf * N;
@@ -917,10 +937,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             for (int i = 0; i < n; ++i, ++t) {
                 const uint32_t team = t % TM, ps = t % PS;
                 if (TM == 1) scores();
-                wait(v_full + vs, vr & 1);
-                wait(p_full + ps, (t / PS) & 1);
+                if (!wait(v_full + vs, vr & 1)) dead = true;
+                if (!wait(p_full + ps, (t / PS) & 1)) dead = true;
                 tc_after();
-                if (elect()) {
+                if (elect() && !dead) {
                     const uint64_t va = v_desc + vs * (X::slot_bytes >> 4), pd = p_desc + ps * (X::p_bytes >> 4);
                     const uint32_t d = tmem + X::O_at + team * X::NP;
 #pragma unroll
@@ -945,8 +965,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         constexpr int qc = DP / 8, rpq = 32 / qc;  // 16-byte pieces of a row, rows of one load
         const int piece = lane % qc, sub = lane / qc;
         for (uint32_t si = 0; !Q8; ++si) {
-            const Seg* const g = get_seg(si);
-            if (!g->n) break;
+            if (!tiles_of(si)) break;
+            const Seg* const g = segs + si % R;
             const int32_t row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
             const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)g->h * a.G * c.D * 2 + piece * 16;
             auto row_of = [&](int r) {
@@ -976,11 +996,12 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         // ============================================================ segments, K
         Walk<N> walk(a, u0, u1, per, b0, base0);
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.k_map) : "memory");
-        uint32_t kt = 0;
+        uint32_t kt = 0, loads = 0;  // (loads: fewer than tiles after a wait that gave up)
         for (uint32_t s = 0;; ++s) {
             Seg g;
             walk.next(g);
-            if (s >= R) wait_seg(seg_empty + s % R, (s / R - 1) & 1);
+            // (a place that does not come free: no more segments, and those who wait for them give up in their turn)
+            if (s >= R && !__all_sync(0xFFFFFFFFu, wait_seg(seg_empty + s % R, (s / R - 1) & 1))) break;
             if (lane == 0) {
                 segs[s % R] = g;
                 *last_seq = (uint32_t)min(walk.b, c.B - 1);
@@ -996,8 +1017,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 const int32_t pages = next;
                 if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, g.L);
                 const uint32_t slot = kt % SK;
-                if (kt >= SK) wait(k_empty + slot, (kt / SK - 1) & 1);
-                bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                const bool free = kt < SK || wait(k_empty + slot, (kt / SK - 1) & 1);
+                if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
+                    bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                    ++loads;
+                }
                 if constexpr (!Q8) {
                     // which positions are there
                     uint32_t* const aux = (uint32_t*)aux_of(kt);
@@ -1013,7 +1037,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 }
             }
         }
-        __syncwarp();
+        land(k_full, SK, loads);
     } else if (warp == kValueWarp) {
         // ============================================================ V, statuses
         // A sequence's status: its offsets, length, tree and pages; the rows of
@@ -1056,11 +1080,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 if (lane == 0) a.seq_status[b] = st;
             }
         };
-        uint32_t kt = 0, si = 0;
+        uint32_t kt = 0, si = 0, loads = 0;
         for (bool open = true; open || next_b < c.B;) {
             if (open) {
-                const Seg* const g = get_seg(si);
-                const int n = __shfl_sync(0xFFFFFFFFu, g->n, 0);
+                const Seg* const g = segs + si % R;
+                const int n = __shfl_sync(0xFFFFFFFFu, tiles_of(si), 0);
                 open = n != 0;
                 if (open) {
                     const int32_t L = g->L, h = g->h;
@@ -1074,18 +1098,28 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, L);
                         if constexpr (Q8) {
                             const uint32_t slot = kt % RV;
-                            if (kt >= RV) wait(raw_empty + slot, (kt / RV - 1) & 1);
-                            bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages);
+                            const bool free = kt < RV || wait(raw_empty + slot, (kt / RV - 1) & 1);
+                            if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
+                                bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages);
+                                ++loads;
+                            }
                         } else {
                             const uint32_t slot = kt % SV;
-                            if (kt >= SV) wait(v_empty + slot, (kt / SV - 1) & 1);
-                            bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages);
+                            const bool free = kt < SV || wait(v_empty + slot, (kt / SV - 1) & 1);
+                            if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
+                                bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages);
+                                ++loads;
+                            }
                         }
                     }
                 }
             }
             if (next_b < c.B) check_one();
         }
+        if constexpr (Q8)
+            land(raw_full, RV, loads);
+        else
+            land(v_full, SV, loads);
         }
     } else {
         more_regs<Q8 ? 80 : 104>();
@@ -1128,19 +1162,23 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         uint32_t gt = 0;
         int32_t tree_of = -1;  // the sequence whose ancestors are known
         for (uint32_t si = 0;; ++si) {
-            const Seg* const g = get_seg(si);
-            const int n = g->n;
+            const bool here = wait_seg(seg_full + si % R, (si / R) & 1);
+            // ---- per-row state
+            if (tid < TM * N) mref_all[tid] = kNoMax;
+            if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
+            if (Q8 && tid < TM * N) unit_all[tid] = first_unit;
+            if (tid < 4) poison[tid] = 0;
+            // (all of them go on or none does: they meet at barriers)
+            if (!here) *lost = 1;
+            bar_sync(bar_all, kSoftThreads);
+            const Seg* const g = segs + si % R;
+            const int n = *lost ? 0 : g->n;
             if (!n) break;
             const int32_t T = g->T, L = g->L, row0 = g->rt * N, ctx = L - T;
             const int32_t rows = min(N, T * a.G - row0);
             const int pieces = (rows + 7) / 8;
             const int live = (int)sub < pieces ? (pieces - (int)sub + X::GT - 1) / X::GT : 0;  // this group's pieces
             const float* const arow = arow_all + (si % R) * N;
-            // ---- per-row state
-            if (tid < TM * N) mref_all[tid] = kNoMax;
-            if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
-            if (Q8 && tid < TM * N) unit_all[tid] = first_unit;
-            if (tid < 4) poison[tid] = 0;
             if (a.parent && g->b != tree_of) {
                 tree_of = g->b;
                 // ancestors by doubling: after k rounds a token knows those up to 2^k - 1 above it
@@ -1191,8 +1229,6 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         seen_by[(j * 32 + lane) * 4 + warp] = by;
                     }
                 }
-                bar_sync(bar_all, kSoftThreads);
-            } else {
                 bar_sync(bar_all, kSoftThreads);
             }
             float2 l[MC][4];
@@ -1566,6 +1602,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (!(poison[u >> 5] >> (u & 31) & 1)) continue;
                         const int32_t pos = ctx + u;
                         const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + c.by_bs.of(pos)], sl = (pos - c.by_bs.of(pos) * c.bs);
+                        if (pg < 0 || pg >= c.num_blocks) continue;  // (only after a wait has given up)
                         const unsigned char* v = c.v + pg * c.block_bytes + sl * c.token_bytes + g->h * c.head_bytes;
                         const float x = Q8 ? kv_e4m3(v[wt]) : bf16_lo(*(const uint16_t*)(v + 2 * wt));
                         if (fabsf(x) < __uint_as_float(0x7F800000u)) continue;
