@@ -1,0 +1,100 @@
+"""What the attention does when a bounded wait gives up: a model of the rings that loads go through, on the CPU."""
+import random
+
+
+class Bar:
+    """An mbarrier: phases of `count` arrivals and the bytes announced with them."""
+
+    def __init__(self, count):
+        self.count = self.pending = count
+        self.due = self.phase = 0
+
+    def arrive(self, due=0):
+        self.due += due
+        self.pending -= 1
+        self._turn()
+
+    def land(self):
+        self.due -= 1
+        self._turn()
+
+    def _turn(self):
+        if self.pending == 0 and self.due == 0:
+            self.phase, self.pending = self.phase + 1, self.count
+
+    def done(self, parity):
+        return (self.phase & 1) != parity
+
+
+def rings(seed, careful):
+    """One loader, one or two readers (products, and the warps that turn or scale tiles), in any order, with waits that
+    give up now and then. careful: a role whose wait gave up loads nothing and gives no place back, and the loader waits
+    for its last loads. Returns what went wrong, or None."""
+    r = random.Random(seed)
+    tiles, places, readers, stall = r.randint(1, 40), r.choice([2, 3, 4]), r.choice([1, 2]), r.choice([0, 0.002, 0.02, 0.3])
+    full, empty = [Bar(1) for _ in range(places)], [Bar(readers) for _ in range(places)]
+    due, flying, aborted, wrong = [0] * places, [], [False], []
+
+    def wait(bar, parity):
+        while not bar.done(parity):
+            if aborted[0]:
+                return False
+            if r.random() < stall:
+                aborted[0] = True
+            yield
+        return True
+
+    def loader():
+        dead, loads = False, 0
+        for t in range(tiles):
+            s = t % places
+            if t >= places and not (yield from wait(empty[s], (t // places - 1) & 1)):
+                dead = True
+            if not (careful and dead):
+                if due[s]:
+                    wrong.append("a load into a place whose load is due")
+                due[s] += 1
+                loads += 1
+                flying.append(s)
+                full[s].arrive(1)
+            yield
+        for t in range(max(0, loads - places), loads) if careful else ():
+            while not full[t % places].done((t // places) & 1):
+                yield
+
+    def reader():
+        dead = False
+        for t in range(tiles):
+            s = t % places
+            if not (yield from wait(full[s], (t // places) & 1)):
+                dead = True
+            for _ in range(r.randint(0, 6)):
+                yield
+            if not (careful and dead):
+                empty[s].arrive()
+            yield
+
+    roles = [loader()] + [reader() for _ in range(readers)]
+    for _ in range(200000):
+        if flying and r.random() < 0.15:
+            s = flying.pop(r.randrange(len(flying)))
+            due[s] -= 1
+            full[s].land()
+        g = r.choice(roles)
+        try:
+            next(g)
+        except StopIteration:
+            roles.remove(g)
+        if not roles:
+            break
+    else:
+        wrong.append("a role does not end")
+    if flying:
+        wrong.append("a load outlives the CTA")
+    return wrong[0] if wrong else None
+
+
+def test_no_load_meets_another_or_outlives_the_cta():
+    assert {rings(seed, True) for seed in range(1500)} == {None}
+    # the model sees both faults where the rules are left out
+    assert {rings(seed, False) for seed in range(1500)} >= {"a load into a place whose load is due", "a load outlives the CTA"}
