@@ -17,7 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cu", "stats.cu", "sampler.cu", "verify.cu", "misc.cu", "topk.cu", "ngram.cu", "tree.cu", "kv.cu",
            "kv_api.cu", "attend.cu", "attend_bf16.cu", "attend_bf16_wide.cu", "attend_e4m3.cu", "attend_e4m3_wide.cu"]
-HEADERS = ["attend.cuh", "common.cuh", "internal.h", "kv.cuh", "kv.h", "precise.cuh", "stream.cuh", "tile.cuh"]
+HEADERS = ["attend.cuh", "common.cuh", "internal.h", "kv.cuh", "kv.h", "precise.cuh", "settle.h",
+           "stream.cuh", "tile.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

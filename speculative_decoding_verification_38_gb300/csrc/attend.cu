@@ -95,6 +95,8 @@ cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
     char* ws = (char*)workspace;
     p.arrive = (uint32_t*)ws;
     p.err = (uint32_t*)(ws + kErrWordOffset);
+    p.left = (uint32_t*)(ws + kLeftOffset);
+    p.late = (int32_t*)(ws + kLateOffset);
     p.part_o = (float*)(ws + kHeaderBytes);
     p.part_ml = (float2*)(ws + kHeaderBytes + (size_t)grid * 2 * n * 128 * 4);
     if (a.c.esz == 1) return n < 48 ? attend_e4m3(n, p, s) : attend_e4m3_wide(n, p, s);

@@ -44,6 +44,7 @@
 
 #include "internal.h"
 #include "kv.cuh"
+#include "settle.h"
 
 namespace specv {
 
@@ -55,6 +56,8 @@ struct AttParams {
     float2* part_ml;   // [grid * 2][N] their maxima (log2) and weights' sums
     uint32_t* arrive;  // [grid] parts arrived, zero between calls
     uint32_t* err;
+    uint32_t* left;    // CTAs that are done, and whether one of them gave up: zero between calls
+    int32_t* late;     // [grid][2] sequences of the CTAs that gave up: zero between calls
     int32_t grid, device;
 };
 
@@ -366,6 +369,20 @@ struct Walk {
 // one CTA alone, the 26 parts of 128 rows took it 50 us, as an SM has few bytes under way. Fewer rows, larger groups.
 template <int N>
 constexpr int kJoinLog = N <= 16 ? 5 : N <= 32 ? 4 : N <= 48 ? 3 : 2;
+
+// The words of settle.h.
+struct Settled {
+    const AttParams& p;
+    __device__ __forceinline__ void put(int32_t i, int32_t v) const { p.late[i] = v; }
+    __device__ __forceinline__ int32_t get(int32_t i) const { return __ldcg(p.late + i); }
+    __device__ __forceinline__ void raise() const { atomicOr(p.left + 1, 1u); }
+    __device__ __forceinline__ bool raised() const { return __ldcg(p.left + 1) != 0; }
+    __device__ __forceinline__ void lower() const { p.left[1] = 0; }
+    __device__ __forceinline__ void fence() const { __threadfence(); }
+    __device__ __forceinline__ int32_t count() const { return (int32_t)atomicAdd(p.left, 1u); }
+    __device__ __forceinline__ void clear_count() const { p.left[0] = 0; }
+    __device__ __forceinline__ void mark(int32_t b) const { p.a.seq_status[b] = kKvTimeout; }
+};
 
 // Joins `n` parts of an entry, CTAs c0 + i, c0 + i + step, .., into the first or (all of them) into the output. By the
 // softmax warps, a row each at a time, four columns to a lane. Out of line: its registers are not taken from the loop
@@ -1001,7 +1018,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             Seg g;
             walk.next(g);
             // (a place that does not come free: no more segments, and those who wait for them give up in their turn)
-            if (s >= R && !__all_sync(0xFFFFFFFFu, wait_seg(seg_empty + s % R, (s / R - 1) & 1))) break;
+            if (s >= R && !__all_sync(0xFFFFFFFFu, wait_seg(seg_empty + s % R, (s / R - 1) & 1))) {
+                if (lane == 0) *last_seq = (uint32_t)(c.B - 1);  // the run's end is not known
+                break;
+            }
             if (lane == 0) {
                 segs[s % R] = g;
                 *last_seq = (uint32_t)min(walk.b, c.B - 1);
@@ -1670,10 +1690,13 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
-    if (*aborted && tid == 0) {
-        atomicOr(p.err, 1u);
-        if (a.seq_status && u0 < u1)
-            for (int32_t b = b0; b <= (int32_t)*last_seq; ++b) a.seq_status[b] = kKvTimeout;
+    if (tid == 0) {
+        const bool late = *aborted;
+        if (late) atomicOr(p.err, 1u);
+        if (a.seq_status) {
+            const Settled words{p};
+            settle(words, (int32_t)blockIdx.x, p.grid, late && u0 < u1 ? b0 : 0, late && u0 < u1 ? (int32_t)*last_seq + 1 : 0);
+        }
     }
 }
 

@@ -35,18 +35,23 @@ constexpr int kGridCap = 4096;        // most CTAs of one streaming pass
 constexpr int kMaxBatch = 65536;      // per-sequence words in the workspace header
 // Workspace header, zeroed once by spec_workspace_init; every word returns
 // to zero by the end of each call that uses it:
-//   [0, 4B)     per-sequence arrival counters (both streaming passes)
-//   [4B, 8B)    per-sequence tile items done (fused verify kernel)
+//   [0, 4B)     per-sequence arrival counters (both streaming passes); the
+//               cache attention's, one for each CTA
+//   [4B, 8B)    per-sequence tile items done (fused verify kernel); the cache
+//               attention's sequences of CTAs that gave up, two words for each CTA
 //   [8B, 12B)   fused verify kernel: sequences in the order they were
 //               finalized, as b + 1 (0: not yet)
 //   then 256 bytes of words: the device error flags, the fused kernel's
-//   ready-list length, its exit counter and its count of tile items handed out.
+//   ready-list length, its exit counter and its count of tile items handed
+//   out; the cache attention's CTAs that are done and whether one gave up.
 constexpr size_t kTilesDoneOffset = (size_t)kMaxBatch * 4;
 constexpr size_t kReadyOffset = (size_t)kMaxBatch * 8;
 constexpr size_t kErrWordOffset = (size_t)kMaxBatch * 12;       // device error flags (bit 0: a wait timed out)
 constexpr size_t kReadyTailOffset = kErrWordOffset + 4;
 constexpr size_t kExitCountOffset = kErrWordOffset + 8;
 constexpr size_t kClaimOffset = kErrWordOffset + 12;              // fused kernel: tile items handed out
+constexpr size_t kLateOffset = kTilesDoneOffset;                 // cache attention: see settle.h
+constexpr size_t kLeftOffset = kErrWordOffset + 16;
 constexpr size_t kHeaderBytes = kErrWordOffset + 256;
 
 constexpr int kSeqTimeout = 6;                                   // per-sequence status after a timed-out wait

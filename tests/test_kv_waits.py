@@ -1,5 +1,23 @@
-"""What the attention does when a bounded wait gives up: a model of the rings that loads go through, on the CPU."""
+"""What the attention does when a bounded wait gives up, on the CPU: the rule that settles the statuses (the kernel's own
+code, threads in place of CTAs), and a model of the rings that loads go through."""
+import os
 import random
+import shutil
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "speculative_decoding_verification_38_gb300", "csrc")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no C++ compiler")
+def test_timeouts_outlast_the_statuses_of_other_ctas(tmp_path):
+    exe = str(tmp_path / "settle")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-pthread", "-I", CSRC, os.path.join(HERE, "settle_threads.cpp"), "-o", exe],
+                   check=True)
+    r = subprocess.run([exe, "300", "5"], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
 
 
 class Bar:
