@@ -82,7 +82,7 @@ constexpr int kTurnWarp = kQueryWarp + 1; // e4m3: four warps for queries and sc
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 4;                  // tiles of the K ring, and of the V ring
 constexpr uint32_t kAttWaitNs = 2000000000;   // a wait that gives up marks the call, which then runs out unwaited
-constexpr float kNoMax = -1.0e30f;            // running maximum before any score
+constexpr float kNoMax = -3.402823466e38f;    // running maximum before any score: not above one, whatever it is
 constexpr size_t kSmemMax = 232448;
 
 // ------------------------------------------------------------ instructions
@@ -1304,20 +1304,29 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     wait(s_full + buf, (t / SB) & 1);
                     tc_after();
 
-                    // scores of piece m less the reference, in units of log2
+                    // scores of piece m less the reference, in units of log2; from zero, for the reference, rounded down, so
+                    // that the largest one's weight is no less than one however far from zero it lies (rounded to nearest,
+                    // a row's only weight was 2^-128 and less from scores of 2^31 on)
                     auto relative = [&](int m, float2 (&z)[4], bool from_zero) {
                         const int r = (sub + X::GT * m) * 8;
-                        const float4 m0 = *(const float4*)(mref + r), m1 = *(const float4*)(mref + r + 4);
-                        float2 x[4] = {{-m0.x, -m0.y}, {-m0.z, -m0.w}, {-m1.x, -m1.y}, {-m1.z, -m1.w}};
-                        if (from_zero) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
+                        float2 f[4];
                         if (Q8) {
                             const float4 a0 = *(const float4*)(arow + r), a1 = *(const float4*)(arow + r + 4);
-                            const float2 f[4] = {{a0.x, a0.y}, {a0.z, a0.w}, {a1.x, a1.y}, {a1.z, a1.w}};
+                            f[0] = {a0.x, a0.y}, f[1] = {a0.z, a0.w}, f[2] = {a1.x, a1.y}, f[3] = {a1.z, a1.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) z[k] = fma2(z[k], mul2(f[k], make_float2(ks, ks)), x[k]);
+                            for (int k = 0; k < 4; ++k) f[k] = mul2(f[k], make_float2(ks, ks));
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) z[k] = fma2(z[k], make_float2(k2, k2), x[k]);
+                            for (int k = 0; k < 4; ++k) f[k] = make_float2(k2, k2);
+                        }
+                        if (from_zero) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k] = make_float2(__fmul_rd(z[k].x, f[k].x), __fmul_rd(z[k].y, f[k].y));
+                        } else {
+                            const float4 m0 = *(const float4*)(mref + r), m1 = *(const float4*)(mref + r + 4);
+                            const float2 x[4] = {{-m0.x, -m0.y}, {-m0.z, -m0.w}, {-m1.x, -m1.y}, {-m1.z, -m1.w}};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k] = fma2(z[k], f[k], x[k]);
                         }
                         if (masked) {
 #pragma unroll

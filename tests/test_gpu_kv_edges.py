@@ -116,3 +116,43 @@ def test_attend_value_scales_of_a_wide_range(sv, G, t):
     c.attend(sv)
     assert c.status.tolist() == [0] * 5
     c.check()
+
+
+# ------------------------------------------------------------------ attention: scores far from zero
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [10, 33, 60, 110, 112])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("G,D,t", [(8, 64, 1), (8, 64, 3), (8, 128, 5), (8, 64, 12), (8, 256, 3)])
+def test_attend_scores_far_from_zero(sv, dtype, power, sign, G, D, t):
+    """Equal scores of up to 2^117 either side of zero, and others twice as far below: a row is the mean of the values
+    that share its largest score."""
+    lens = [t, t + 1, 127 + t, 300, 1100]
+    c = Case(lens=lens, tokens=[t] * len(lens), H=1, G=G, D=D, dtype=dtype)
+    r = np.random.default_rng(3)
+    half = 2.0 ** (power // 2 if dtype == "bf16" else 0)  # k's magnitude; the rest lies with q (e4m3: K's scales too)
+    rest = 2.0**power / half / (1 if dtype == "bf16" else 2.0 ** (power // 2))
+    far = torch.from_numpy(r.random(c.held.shape) < 0.3)  # positions whose score lies further down (page, slot)
+    for b in range(c.B):
+        far[int(c.table[b, 0]), 0] = False  # every token sees position 0
+    k = torch.where(far, -2.0 if sign > 0 else 2.0, 1.0)[None, :, :, None, None].expand(c.k.shape) * half
+    c.k.copy_(k.to(torch.bfloat16) if dtype == "bf16" else k.to(torch.float8_e4m3fn).view(torch.uint8))
+    if dtype == "e4m3":
+        c.ks[:] = 2.0 ** (power // 2)
+    q = sign * rest * torch.from_numpy(1 + r.random((c.rows, G, 1))).expand(c.rows, G, D)
+    c.q = q.to(torch.bfloat16)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * c.B
+    got, lse = c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    _, v, _, vs = c.host()
+    s = c.q.double().numpy().sum(-1) * c.scale * half * (1 if dtype == "bf16" else 2.0 ** (power // 2))
+    for b in range(c.B):
+        vv = okv.entries(v, vs, c.table[b], 0, 0, lens[b])
+        near = np.array([not far[int(c.table[b, j // c.bs]), j % c.bs] for j in range(lens[b])])
+        for i in range(t):
+            seen = near & (np.arange(lens[b]) <= lens[b] - t + i)
+            row = int(c.row_off[b]) + i
+            want, mean = vv[seen].mean(0), np.abs(vv[seen]).mean(0)
+            # an output's rounding, weights of 11 bits and more, float32 sums (tests/kv_cases.py)
+            bound = 2.0**-8 * np.abs(want) + (2.0**-10 + lens[b] * 2.0**-23) * mean + 1e-30
+            assert (np.abs(got[row] - want) <= bound).all(), (b, i, np.abs(got[row] - want).max())
+            assert (np.abs(lse[row] - s[row] - np.log(seen.sum())) <= 2.0**-23 * (D + 8) * (np.abs(s[row]) + 10)).all()
