@@ -492,7 +492,9 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int64
  * has no effect on it, a NaN or an infinity there included. A token whose
  * every s_j is -inf gets zeros and lse -inf. Statistics and sums are float32.
  * Up to head_dim 128 the products run on the tensor cores: SPEC_BF16 with
- * queries as they are and weights as two bf16 parts (16 bits); SPEC_E4M3 with
+ * queries as they are and weights, up to 2^16 before the sums are divided, as
+ * two bf16 parts (16 bits; values whose magnitudes sum to 2^111 or less over
+ * the positions cannot overflow); SPEC_E4M3 with
  * queries exact down to 2^-24 of their row's largest element (the rest to
  * 2^-31 of it) and weights times V's scales in fp16: 11 bits of what is 2^-19
  * of the largest V scale the token sees or more (the rest to 2^-30 of that).

@@ -1147,15 +1147,16 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         // Thread = one position of the tile; group gr is of team gr % TM and has
         // every GT-th 8-row piece of the query rows. A weight is 2^(score - m) with m a
         // reference that starts as the row's maximum in its first tile and moves
-        // only when a later score passes it by 2^grow: a weight in bf16 parts or
-        // float32 sums may be that large (2^60), one in f16 less (2^8). e4m3: a weight goes to f16 times V's scale and
-        // the row's unit u = 2^(6 - v), 2^v the smallest power of two that no scale the row has seen passes: at most
-        // 2^14 (f16's largest is 2^16), and f16's least is 2^-30 of a weight of one with that scale. The unit is a row's
-        // own, so that the scale of a new token that the row does not see leaves no trace in it.
+        // only when a later score passes it by 2^grow. bf16: 2^16, as what the weights have above one the sums lose of
+        // float32's range to values (with 2^60 values of 2^67 overflowed; moves are as rare, and no case took longer).
+        // e4m3: 2^8; a weight goes to f16 times V's scale and the row's unit u = 2^(6 - v), 2^v the smallest power of
+        // two that no scale the row has seen passes: at most 2^14 (f16's largest is 2^16), and f16's least is 2^-30 of
+        // a weight of one with that scale. The unit is a row's own, so that the scale of a new token that the row does
+        // not see leaves no trace in it.
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
-        constexpr float grow = Q8 ? 8.f : 60.f;
+        constexpr float grow = Q8 ? 8.f : 16.f;
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t team = gr % TM, sub = gr / TM;
         const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;

@@ -1,5 +1,7 @@
 """The paged cache's operators where they could go wrong and the other GPU tests do not reach, against the float64 oracle
 (oracle/kv.py); bounds from tests/kv_cases.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -156,3 +158,29 @@ def test_attend_scores_far_from_zero(sv, dtype, power, sign, G, D, t):
             bound = 2.0**-8 * np.abs(want) + (2.0**-10 + lens[b] * 2.0**-23) * mean + 1e-30
             assert (np.abs(got[row] - want) <= bound).all(), (b, i, np.abs(got[row] - want).max())
             assert (np.abs(lse[row] - s[row] - np.log(seen.sum())) <= 2.0**-23 * (D + 8) * (np.abs(s[row]) + 10)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,D,t", [(1, 64, 1), (2, 128, 9), (4, 128, 9), (8, 128, 9), (8, 64, 12), (2, 256, 3)])
+def test_attend_large_values_under_rising_scores(sv, dtype, G, D, t):
+    """Values of about 2^100 with scores that rise by up to 2^58 in the weights from one tile to a later one of the same
+    processor (and team of its warps): the sums stay finite. 160 (sequence, head) pairs, so that one has several tiles."""
+    c = Case(lens=[t, 300 + t] + [900, 1300] * 19, tokens=[t] * 40, H=4, G=G, D=D, dtype=dtype)
+    rise = np.array([0, 12, 3, 1, 40, 50, 58, 30, 96, 70, 100, 60])  # log2 of the weights, by tile
+    unit = math.log(2) / (c.scale * D) / (1.0 if dtype == "bf16" else 2.0**-3)
+    k = torch.zeros(c.held.shape)
+    for b in range(c.B):
+        for j in range(c.lens[b]):
+            k[int(c.table[b, j // c.bs]), j % c.bs] = float(rise[j // 128])
+    k = (k * unit)[None, :, :, None, None].expand(c.k.shape)
+    if dtype == "bf16":
+        c.k.copy_(k.to(torch.bfloat16))
+        c.v.mul_(2.0**100)
+    else:
+        c.k.copy_(k.to(torch.float8_e4m3fn).view(torch.uint8))
+        c.ks[:] = 2.0**-3
+        c.vs.mul_(2.0**98)
+    c.q = torch.ones_like(c.q)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * 40
+    c.check()
