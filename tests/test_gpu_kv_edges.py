@@ -184,3 +184,58 @@ def test_attend_large_values_under_rising_scores(sv, dtype, G, D, t):
     c.attend(sv)
     assert c.status.tolist() == [0] * 40
     c.check()
+
+
+# ------------------------------------------------------------------ large batches
+def _lens(B, most, seed):
+    """Lengths and new tokens of a batch, empty sequences among them."""
+    r = np.random.default_rng(seed)
+    tokens = r.integers(0, 6, B)
+    tokens[r.random(B) < 0.3] = 0
+    return (tokens + r.integers(0, most, B) * (r.random(B) < 0.8)).tolist(), tokens.tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [33, 300, 1100, 2100])
+def test_append_and_gather_of_many_sequences(sv, dtype, B):
+    """A row's sequence is found in steps of 32: one to three of them, sequences without rows between."""
+    lens, tokens = _lens(B, 20, B)
+    c = Case(lens=lens, tokens=tokens, H=2, D=32, bs=4, dtype=dtype)
+    status, want = _append(sv, c)
+    assert status.tolist() == [0] * B
+    _same_cache(c, want)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    got = [torch.full((int(off[-1]), 2, 32), 7.0, device="cuda") for _ in range(2)]
+    status.fill_(-7)
+    sv.check(sv.spec_kv_gather(c.cache, c.dlens, torch.from_numpy(off).cuda(), *got, seq_status=status), "gather")
+    assert status.tolist() == [0] * B
+    k, v, ks, vs = want
+    for pool, sc, x in ((k, ks, got[0]), (v, vs, got[1])):
+        x = x.cpu().numpy()
+        for b in range(B):
+            for h in range(2):
+                e = okv.entries(pool, sc, c.table[b], 0, h, lens[b]).astype(np.float32)
+                np.testing.assert_array_equal(x[off[b]:off[b + 1], h], e)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,G,D", [(641, 2, 64), (1300, 4, 128), (2700, 1, 64)])
+@pytest.mark.parametrize("as_tree", [False, True])
+def test_attend_many_sequences(sv, dtype, B, G, D, as_tree):
+    """More sequences than a CTA has threads: each counts several. A bad one and empty ones among them."""
+    lens, tokens = _lens(B, 200 if B < 1000 else 24, B + 1)
+    lens[B // 2], tokens[B // 2] = 9, 4
+    parent = sum((random_tree(t, b) for b, t in enumerate(tokens) if t), []) if as_tree else None
+    c = Case(lens=lens, tokens=tokens, H=1, G=G, D=D, bs=8, dtype=dtype, parent=parent)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * B
+    c.check()
+    c.dlens[B // 2] = 3  # shorter than its new tokens
+    c.attend(sv)
+    assert c.status.tolist() == [2 if b == B // 2 else 0 for b in range(B)]
+    lo, hi = int(c.row_off[B // 2]), int(c.row_off[B // 2 + 1])
+    assert (c.out[lo:hi] == 0).all() and torch.isneginf(c.lse[lo:hi]).all()
+    keep = np.r_[0:lo, hi:c.rows]
+    out, lse, av, mag, spread = c.expected()
+    far = np.abs(c.out.double().cpu().numpy() - out) - c.bound(out, av, mag, spread)
+    assert (far[keep] <= 0).all()
