@@ -275,13 +275,13 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _dtype_code(t) -> int:
+def _dtype_code(t, name="logits") -> int:
     T = _types()
     if t.dtype is T.bfloat16:
         return SPEC_BF16
     if t.dtype is T.float32:
         return SPEC_F32
-    raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def _check_dev(t, name):
@@ -657,8 +657,8 @@ def spec_kv_append(cache: KVCache, k_new, v_new, kv_lens, row_off=None, t_max=No
     _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
     _check_typed(row_off, "row_off", T.int64, c.batch + 1)
     _check_typed(seq_status, "seq_status", T.int32, c.batch)
-    return (_lib or lib()).spec_kv_append(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), rows[1],
-                                          rows[0], _ptr(row_off), t_max or 0, kv_lens.data_ptr(), _ptr(seq_status),
+    return (_lib or lib()).spec_kv_append(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new, "k_new"),
+                                          rows[1], rows[0], _ptr(row_off), t_max or 0, kv_lens.data_ptr(), _ptr(seq_status),
                                           _stream(stream))
 
 
@@ -673,7 +673,7 @@ def spec_kv_gather(cache: KVCache, kv_lens, out_off, k_out, v_out, layer=0, seq_
     _check_typed(out_off, "out_off", T.int64, c.batch + 1, optional=False)
     _check_typed(seq_status, "seq_status", T.int32, c.batch)
     return (_lib or lib()).spec_kv_gather(cache.ref, layer, kv_lens.data_ptr(), out_off.data_ptr(), rows, k_out.data_ptr(),
-                                          v_out.data_ptr(), _dtype_code(k_out), _ptr(seq_status), _stream(stream))
+                                          v_out.data_ptr(), _dtype_code(k_out, "k_out"), _ptr(seq_status), _stream(stream))
 
 
 def spec_kv_compact(cache: KVCache, node_off, path, accepted, kv_lens_in, kv_lens_out, out_num_blocks=None,

@@ -113,7 +113,7 @@ cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s);
 bool attend_takes(int32_t head_dim);
 size_t attend_workspace(int64_t rows);
 cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s);
-// One warp for each query row, for the rest.
+// A CTA for each query row, for the rest.
 cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s);
 
 }  // namespace specv

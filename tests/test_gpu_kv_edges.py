@@ -239,3 +239,15 @@ def test_attend_many_sequences(sv, dtype, B, G, D, as_tree):
     out, lse, av, mag, spread = c.expected()
     far = np.abs(c.out.double().cpu().numpy() - out) - c.bound(out, av, mag, spread)
     assert (far[keep] <= 0).all()
+
+
+# ------------------------------------------------------------------ refusals
+def test_types_are_refused_by_their_own_names(sv):
+    c = Case(lens=[9], tokens=[3], H=2, D=32)
+    c.to_device(sv)
+    x = torch.zeros((3, 2, 32), dtype=torch.float16, device="cuda")
+    with pytest.raises(TypeError, match="^k_new must be float32 or bfloat16"):
+        sv.spec_kv_append(c.cache, x, x, c.dlens, row_off=c.doff)
+    with pytest.raises(TypeError, match="^k_out must be float32 or bfloat16"):
+        y = torch.zeros((9, 2, 32), dtype=torch.float16, device="cuda")
+        sv.spec_kv_gather(c.cache, c.dlens, torch.tensor([0, 9], device="cuda"), y, y)
