@@ -370,6 +370,24 @@ struct Walk {
 template <int N>
 constexpr int kJoinLog = N <= 16 ? 5 : N <= 32 ? 4 : N <= 48 ? 3 : 2;
 
+// For lane r, the largest value (zero: none) among the lanes whose `seen_by` has row r, of `rows`, by a warp: the lanes with
+// the largest give it to their rows, then those with the next for the rows still without. Out of line: it is for the
+// few tiles whose positions some rows do not see.
+__device__ __noinline__ uint32_t seen_max(uint32_t value, uint32_t seen_by, uint32_t rows) {
+    uint32_t mine = 0;
+    if (!seen_by) value = 0;
+#pragma unroll 1
+    while (rows) {
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, value);
+        if (!top) break;
+        const uint32_t to = rows & __reduce_or_sync(0xFFFFFFFFu, value == top ? seen_by : 0u);
+        if (to >> (threadIdx.x & 31) & 1) mine = top;
+        rows &= ~to;
+        if (value == top) value = 0;
+    }
+    return mine;
+}
+
 // The words of settle.h.
 struct Settled {
     const AttParams& p;
@@ -1341,10 +1359,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     // (Q8: and the units to the scales seen)
                     auto refer = [&]() {
                         unsigned char* const seen_e = (unsigned char*)(red + 5 * MC * 8);  // Q8: [4][MC * 8] 127 + exponents
+                        static_assert(!Q8 || MC <= 4, "a lane for each row of the group");
                         const uint32_t vw = __float_as_uint(fabsf(vs));
                         // of the smallest power of two not below this position's scale, 0 to 253 (no scale, 2^126 or more)
                         const uint32_t e = min(253u, (vw >> 23) + ((vw & 0x7FFFFFu) ? 1u : 0u));
-                        const uint32_t tile_e = Q8 ? __reduce_max_sync(0xFFFFFFFFu, e) : 0u;
 #pragma unroll 1
                         for (int m = 0; m < live; ++m) {
                             float2 z[4];
@@ -1359,16 +1377,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                                 x = lane == k ? top : x;
                             }
                             if (lane < 8) red[wq * MC * 8 + m * 8 + lane] = x;
-                            if (Q8) {
-                                uint32_t row_e = tile_e;
-                                if (masked)
-#pragma unroll 1
-                                    for (int k = 0; k < 8; ++k) {
-                                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, (vis >> (m * 8 + k) & 1) ? e : 0u);
-                                        row_e = lane == k ? top : row_e;
-                                    }
-                                if (lane < 8) seen_e[wq * MC * 8 + m * 8 + lane] = (unsigned char)row_e;
-                            }
+                        }
+                        if (Q8) {
+                            const uint32_t row_e = masked ? seen_max(e, (uint32_t)vis, ~0u >> (32 - live * 8))
+                                                          : __reduce_max_sync(0xFFFFFFFFu, e);
+                            if (lane < MC * 8) seen_e[wq * MC * 8 + lane] = (unsigned char)row_e;
                         }
                         bar_sync(bar_gr, 128);
                         if (wt < live * 8) {
@@ -1432,7 +1445,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         due = false;
                         float top = none;
                         const float wv = Q8 ? vs * u_all : 1.f;
-                        bool over = Q8 && !masked && fabsf(wv) > 64.f && u_all > 0x1p-120f;  // (it goes no lower)
+                        float big = Q8 && !masked && fabsf(wv) > 64.f && u_all > 0x1p-120f ? 65536.f : 0.f;  // (it goes no lower)
                         // two pieces at a time, so that one's latencies hide the other's
 #pragma unroll
                         for (int m0 = 0; m0 < MC; m0 += 2) {
@@ -1468,13 +1481,15 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll
                                         for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], make_float2(wv, wv));
                                     } else {
+                                        const float4 u0 = *(const float4*)(unit + piece * 8), u1 = *(const float4*)(unit + piece * 8 + 4);
+                                        const float2 u[4] = {{u0.x, u0.y}, {u0.z, u0.w}, {u1.x, u1.y}, {u1.z, u1.w}};
 #pragma unroll
                                         for (int k = 0; k < 4; ++k) {
                                             const int at = (m < live ? m : m0) * 8 + 2 * k;
-                                            z[k] = mul2(z[k], mul2(make_float2(vs, vs), *(const float2*)(unit + piece * 8 + 2 * k)));
+                                            z[k] = mul2(z[k], mul2(make_float2(vs, vs), u[k]));
                                             z[k].x = (vis >> at & 1) ? z[k].x : 0.f;
                                             z[k].y = (vis >> (at + 1) & 1) ? z[k].y : 0.f;
-                                            over |= fmaxf(fabsf(z[k].x), fabsf(z[k].y)) > 16384.f;
+                                            big = max3(big, fabsf(z[k].x), fabsf(z[k].y));
                                         }
                                     }
                                     *(uint4*)(pw + piece * 2048) = make_uint4(f16x2(z[0].x, z[0].y), f16x2(z[1].x, z[1].y),
@@ -1501,7 +1516,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             continue;
                         }
                         // (after a move nothing passes the reference, so that a second one is never due)
-                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || over)) break;
+                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || big > 16384.f)) break;
                         sign = -1.f;
                     }
                     if (tail && sub == 0 && (pos >= L || (in && pos >= ctx && T > 1))) {
