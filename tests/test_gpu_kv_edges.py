@@ -241,6 +241,22 @@ def test_attend_many_sequences(sv, dtype, B, G, D, as_tree):
     assert (far[keep] <= 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 256])
+def test_batch_without_new_tokens(sv, dtype, D):
+    """No rows at all: statuses only, nothing else touched."""
+    c = Case(lens=[0, 5, 300], tokens=[0, 0, 0], H=2, G=2, D=D, dtype=dtype)
+    c.attend(sv)
+    assert c.status.tolist() == [0, 0, 0]
+    before = c.raw(c.dk), c.raw(c.dv)
+    new = torch.zeros((0, 2, D), dtype=torch.bfloat16, device="cuda")
+    c.status.fill_(-7)
+    sv.check(sv.spec_kv_append(c.cache, new, new, c.dlens, row_off=c.doff, seq_status=c.status), "append")
+    assert c.status.tolist() == [0, 0, 0]
+    np.testing.assert_array_equal(before[0], c.raw(c.dk))
+    np.testing.assert_array_equal(before[1], c.raw(c.dv))
+
+
 # ------------------------------------------------------------------ refusals
 def test_types_are_refused_by_their_own_names(sv):
     c = Case(lens=[9], tokens=[3], H=2, D=32)
