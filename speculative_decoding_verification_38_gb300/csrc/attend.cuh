@@ -24,17 +24,23 @@
 // weights, in units that go by the scales that a row sees.
 //
 // Bounds (8 heads of 128, pages of 16). Nine bf16 tokens of each of 64
-// sequences over 146,153 positions: 118 us for 608 MB, 0.76 of the copy
+// sequences over 146,153 positions: 119 us for 608 MB, 0.75 of the copy
 // bandwidth; of two over 262,142: 182 us, 0.87. The difference is the ends of
 // entries, where a CTA's groups wait for the last of its tiles (about 12,000
-// cycles, four or five times in a run). Trees of 29 (116 rows): 180 us, 0.52;
-// the softmax groups' instructions (about 65 for eight weights) and one place
-// for P, as two parts of 128 rows take 64 KB. e4m3, one token of each of the
-// 64: 105 us for 310 MB, 0.43, and ragged chains of up to 72 rows 939 us for
-// 2.2 GB, 0.35: the same instructions and ends, and half the bytes for each
-// weight. A single sequence of 4,111: 14 us, of which launch, start (the list,
-// TMEM) and the chain page number - tile - score - weight - product - join are
-// latency.
+// cycles, four or five times in a run). Where a tile takes one team longer
+// than its loads, the length of its chain of steps bounds it (scores, their
+// read from TMEM, weights, their stores, the vote on references, the product),
+// with issue slots to spare: trees of 29 (116 rows), 180 us, 0.52, issue
+// active in 47 % of cycles, one place for P as two parts of 128 rows take
+// 64 KB; ragged e4m3 chains of up to 72 rows, 957 us for 2.2 GB, 0.34, about
+// 4,200 cycles a tile, issue active in 55 %, a fifth of the tiles make their
+// weights twice. One e4m3 token of each of the 64: 108 us for 310 MB, 0.42,
+// issue active in 40 %: the ends of entries. A single sequence of 4,111:
+// 15 us, of which launch, start (the list, TMEM) and the chain page number -
+// tile - score - weight - product - join are latency. Far from the floor:
+// rows over short caches (65 tokens of 64 sequences of 100 to 400, 8 query
+// heads to a key-value head: 263 us bf16, 401 e4m3, for 201 and 170 MB), where
+// an entry's opening and end outweigh its few tiles.
 #pragma once
 
 #include <cuda.h>

@@ -148,9 +148,11 @@ __device__ __forceinline__ void write_codes(const uint32_t (&w)[4], bool live, u
 // offsets and steps on from there. A thread asks for its values first, so that
 // the offsets, lengths and page numbers, each needing the last, come in their
 // shadow. The grid's last CTAs write the statuses, one warp for each sequence.
-// bf16 to bf16 HBM bounds it; to e4m3 the instructions of the conversion do:
-// 130,238 tokens of 8 heads in 178 us, 4.5 TB/s (0.67 of the copy bandwidth).
-// A round's 576 tokens: 3.8 us of latency (offsets, length, page, store).
+// Issue bounds it to e4m3 (active in 83 % of cycles: conversion, and a look-up
+// for each entry): 130,238 tokens of 8 heads in 178 us, 4.5 TB/s (0.67 of the
+// copy bandwidth). bf16 to bf16 210 us, 5.1 TB/s (0.75); float32 to bf16
+// 228 us, 7.0 TB/s, HBM. A round's 576 tokens: 3.6 us of latency (offsets,
+// length, page, store).
 template <int DT, bool Q8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const KvNew n, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
 
 // The cache back as rows: value = code * scale. Threads and entries as above;
 // a thread's entries are all looked up, then all asked for, then written.
-// Bound by HBM: 146,153 tokens of 8 heads from e4m3 in 142 us, 6.4 TB/s (0.94).
+// Bound by HBM: 146,153 tokens of 8 heads from e4m3 in 143 us, 6.3 TB/s (0.93);
+// to float32 265 us, 5.7 TB/s.
 template <bool Q8, int ODT>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, const KvRead g, int lanes_log, int64_t ctas) {
     __shared__ int32_t b_first;
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvView c, con
 // later entry: taken in order, each thread's column moves in place. A thread
 // owns one 16-byte column (or one scale) of one layer and head, and takes the
 // path kMove entries at a time: loads together, then stores (of 64 trees in 32
-// layers 8.3 us; one at a time 12.3). Bound by latency: path, pages, entries.
+// layers 8.5 us; one at a time 12.3). Bound by latency: path, pages, entries.
 // Each CTA of a sequence reads its old length; the first writes the new one
 // (m.part says whether that is this launch's to do, see launch_kv_compact).
 constexpr int kMove = 4;
@@ -444,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 6) kv_compact_kernel(const KvView c,
 // position's product with the query in shared memory, the running maximum and
 // sum over the warp, then the weighted values with eight of the head's columns
 // to a lane; the warps' sums are joined at the end. Bound by its 16-byte loads'
-// latency and by every query row reading the cache for itself.
+// latency and by every query row reading the cache for itself: 64 x 9 tokens
+// over 2,048 positions, 2 x 4 heads of 256, 1.67 ms for bytes of 40 us (e4m3 the
+// same time); one token over 4,096 positions 204 us.
 constexpr int kPlainWarps = 8;
 
 // Eight elements of an entry from `d` on.
