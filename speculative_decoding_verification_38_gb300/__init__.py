@@ -679,7 +679,8 @@ def spec_kv_gather(cache: KVCache, kv_lens, out_off, k_out, v_out, layer=0, seq_
 def spec_kv_compact(cache: KVCache, node_off, path, accepted, kv_lens_in, kv_lens_out, out_num_blocks=None,
                     seq_status=None, stream=None) -> int:
     """Keep the accepted path's entries of each sequence's tree, in every
-    layer (path and accepted: spec_tree_verify's out_path and out_accepted)."""
+    layer (path and accepted: spec_tree_verify's out_path and out_accepted).
+    kv_lens_out may be kv_lens_in."""
     T, c = _types(), cache.struct
     B = c.batch
     _check_typed(node_off, "node_off", T.int64, B + 1, optional=False)

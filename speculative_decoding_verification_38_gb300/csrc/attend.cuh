@@ -202,6 +202,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float larger3(float a, float b, float c) {  // of the magnitudes; a NaN stays one
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float max_warp(float x) {  // a NaN wins
     float r;
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
@@ -1451,6 +1456,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         due = false;
                         float top = none;
                         const float wv = Q8 ? vs * u_all : 1.f;
+                        // units have to move where a scale passes the common one, or a weight in its row's unit passes 2^14
+                        // or is not a number (zero times a unit times a scale past float32's range)
                         float big = Q8 && !masked && fabsf(wv) > 64.f && u_all > 0x1p-120f ? 65536.f : 0.f;  // (it goes no lower)
                         // two pieces at a time, so that one's latencies hide the other's
 #pragma unroll
@@ -1495,7 +1502,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                                             z[k] = mul2(z[k], mul2(make_float2(vs, vs), u[k]));
                                             z[k].x = (vis >> at & 1) ? z[k].x : 0.f;
                                             z[k].y = (vis >> (at + 1) & 1) ? z[k].y : 0.f;
-                                            big = max3(big, fabsf(z[k].x), fabsf(z[k].y));
+                                            big = larger3(big, z[k].x, z[k].y);
                                         }
                                     }
                                     *(uint4*)(pw + piece * 2048) = make_uint4(f16x2(z[0].x, z[0].y), f16x2(z[1].x, z[1].y),
@@ -1522,7 +1529,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             continue;
                         }
                         // (after a move nothing passes the reference, so that a second one is never due)
-                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || big > 16384.f)) break;
+                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || !(big <= 16384.f))) break;
                         sign = -1.f;
                     }
                     if (tail && sub == 0 && (pos >= L || (in && pos >= ctx && T > 1))) {

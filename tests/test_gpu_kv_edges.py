@@ -120,6 +120,27 @@ def test_attend_value_scales_of_a_wide_range(sv, G, t):
     c.check()
 
 
+@pytest.mark.parametrize("G,D,t", [(1, 64, 1), (4, 128, 9), (8, 128, 9), (4, 64, 29)])
+def test_attend_weightless_token_with_a_large_scale(sv, G, D, t):
+    """V scales of 2^-100 and, on new tokens whose weight is zero in float32, of 2^30: the product of a row's unit with
+    the latter is not finite before the unit moves, and zero times it must stay zero. 160 (sequence, head) pairs, so
+    that a processor comes to the new tokens' tile after others."""
+    c = Case(lens=[t + 1, t + 40] + [900, 1025] * 19, tokens=[t] * 40, H=4, G=G, D=D, dtype="e4m3")
+    c.vs[:] = 2.0**-100
+    c.ks[:] = 1.0
+    c.q = torch.ones_like(c.q)
+    k = torch.zeros(c.held.shape)
+    for b in range(c.B):
+        for j in range(c.lens[b] - t, c.lens[b]):
+            g, i = int(c.table[b, j // c.bs]), j % c.bs
+            k[g, i] = -448.0  # a score of -448 sqrt(D)
+            c.vs[0, g, :, i] = 2.0**30
+    c.k.copy_(k[None, :, :, None, None].expand(c.k.shape).to(torch.float8_e4m3fn).view(torch.uint8))
+    c.attend(sv)
+    assert c.status.tolist() == [0] * 40
+    c.check()
+
+
 # ------------------------------------------------------------------ attention: scores far from zero
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("power", [10, 33, 60, 110, 112])
