@@ -530,6 +530,94 @@ SPEC_API size_t spec_kv_attend_workspace_size(const spec_kv_cache_t* cache, cons
 SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* cache, const spec_kv_attend_args_t* args,
                                       spec_stream_t stream);
 
+/* Attention with a sliding window and sinks: spec_kv_attend in which a token
+ * sees, of the positions above, those less than `window` before its own and
+ * the cache's first `sinks` (0 <= sinks; window >= 1). A token's own position
+ * is kv_lens[b] - T_b plus its place in the chain, or its depth in the tree,
+ * and a new token's that it looks at likewise; the first `sinks` are counted
+ * by cache index. Arguments, outputs, statuses and workspace (its size too)
+ * are spec_kv_attend's. Pages in which no token of the sequence sees a
+ * position (none of kv_lens[b] - T_b + 1 - window and later, or of the sinks)
+ * are not read and their table entries may be anything, so that an engine can
+ * give them to other sequences; what a token does not see has no effect on it.
+ * A window of kv_lens[b] or more hides nothing. */
+SPEC_API spec_status_t spec_kv_attend_window(const spec_kv_cache_t* cache, const spec_kv_attend_args_t* args,
+                                             int32_t window, int32_t sinks, spec_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions. Pair i of a head's first rotary_dim elements, (a, b) =
+ * (i, i + rotary_dim / 2) or, adjacent, (2i, 2i + 1), turns by the angle
+ * t = position * inv_freq[i]:
+ *   x'_a = f (x_a cos t - x_b sin t),  x'_b = f (x_b cos t + x_a sin t),
+ * f = factor; the elements past rotary_dim stay as they are. Angles are exact
+ * to 2^-31 of a turn for any int32 position and inv_freq up to 2 (they are
+ * taken in 64-bit fractions of a turn; |inv_freq| up to 2^20 loses a bit for
+ * each power of two past that, and one that is larger or not finite gives
+ * NaN); sines and cosines are good to 2^-23, products and sums are float32,
+ * and the result is rounded once.
+ * ------------------------------------------------------------------------- */
+#define SPEC_ROPE_MAX_AXES 4
+typedef struct {
+    uint32_t struct_size; /* sizeof(spec_rope_t), for ABI checks */
+    int32_t rotary_dim;   /* even, 2 .. head_dim */
+    int32_t adjacent;     /* which elements make a pair: 0 halves, 1 neighbours */
+    int32_t axes;         /* 1 .. SPEC_ROPE_MAX_AXES positions of a token: for images and video, time, height, width */
+    /* Pairs of each axis, rotary_dim / 2 in all (unused with one axis). In
+     * blocks (alternating = 0): the first sections[0] pairs turn by axis 0, the
+     * next by axis 1, and so on. Alternating: pair i turns by axis i % axes
+     * while i < axes * sections[i % axes], else by axis 0; axes * sections[a]
+     * may not pass rotary_dim / 2 for a > 0. */
+    int32_t sections[SPEC_ROPE_MAX_AXES];
+    int32_t alternating;
+    float factor;          /* of cosines and sines; finite */
+    const float* inv_freq; /* device [rotary_dim / 2], radians for one position */
+} spec_rope_t;
+
+/* Rotate rows: x [rows, heads, head_dim], row r head h at
+ * x + r*x_token_stride + h*head_dim (elements of x_dtype), to out likewise;
+ * SPEC_BF16 or SPEC_F32 each. positions: device int32 [axes, rows]. out may be
+ * x with its type and stride (in place), but must not overlap it otherwise.
+ * x, out, their row strides and head_dim are multiples of 16 bytes, head_dim
+ * up to 256 (larger: SPEC_ERR_UNSUPPORTED). */
+SPEC_API spec_status_t spec_rope(const spec_rope_t* rope, const void* x, int32_t x_dtype, int64_t x_token_stride,
+                                 void* out, int32_t out_dtype, int64_t out_token_stride, int64_t rows, int32_t heads,
+                                 int32_t head_dim, const int32_t* positions, spec_stream_t stream);
+
+/* spec_kv_append with the rotation on the way: the new keys are rotated and
+ * written (an e4m3 entry's scale is its rotated values'), the values written
+ * as they are, and the pass's queries, where there are any, rotated by the
+ * same angles into q_out. A token's position is its index in the cache (chain:
+ * parent and positions NULL); kv_lens[b] - T_b plus its depth (tree: parent,
+ * local node indices as spec_tree_verify's); or given (positions, int32
+ * [axes, rows]; parent must then be NULL). Without positions every axis has
+ * the same one. Statuses are spec_kv_append's, and LAYOUT for a bad parent
+ * (nothing is written for the tokens whose way to the root leads over it). A
+ * sequence with an error of its offsets or length has no rows of q_out
+ * written; a token on a page outside the pool has its queries rotated all the
+ * same. */
+typedef struct {
+    uint32_t struct_size; /* sizeof(spec_kv_append_rope_args_t), for ABI checks */
+    int32_t layer;
+    int32_t new_dtype;    /* of k_new, v_new and q: SPEC_BF16 or SPEC_F32 */
+    int32_t t_max;        /* new tokens of each sequence without row_off */
+    int64_t rows;
+    const int64_t* row_off;   /* device [B+1] or NULL: rows = batch * t_max */
+    const int32_t* kv_lens;   /* device [B], the new tokens included */
+    const int32_t* parent;    /* device [rows] or NULL */
+    const int32_t* positions; /* device [axes, rows] or NULL */
+    const void* k_new;        /* device, as spec_kv_append's */
+    const void* v_new;
+    int64_t new_token_stride; /* elements */
+    const void* q;            /* device, row r head h at q + r*q_token_stride + h*head_dim, or NULL (q_heads = 0) */
+    void* q_out;              /* device bf16, row r head h at q_out + r*q_out_token_stride + h*head_dim; q itself only
+                                 where new_dtype is SPEC_BF16 and the strides are equal */
+    int64_t q_token_stride, q_out_token_stride; /* elements, multiples of 16 bytes */
+    int32_t q_heads;          /* 0: no queries */
+    int32_t* seq_status;      /* device [B] or NULL */
+} spec_kv_append_rope_args_t;
+SPEC_API spec_status_t spec_kv_append_rope(const spec_kv_cache_t* cache, const spec_rope_t* rope,
+                                           const spec_kv_append_rope_args_t* args, spec_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Test hooks. Same conventions; they expose intermediate values of the last
  * spec_verify_sample / spec_verify_greedy call made with the same arguments

@@ -69,11 +69,11 @@ def append(k, v, ks, vs, table, layer, k_new, v_new, row_off, kv_lens):
                         pool[layer, g, i, h], sc[layer, g, h, i] = quantise(x)
 
 
-def entries(pool, sc, table_row, layer, h, n: int) -> np.ndarray:
-    """Positions 0..n-1 of one head as float64 values [n, D]."""
+def entries(pool, sc, table_row, layer, h, n: int, wanted=None) -> np.ndarray:
+    """Positions 0..n-1 of one head as float64 values [n, D]; zeros for those that are not wanted (a bool each)."""
     bs = pool.shape[2]
-    out = np.empty((n, pool.shape[4]))
-    for j in range(n):
+    out = np.zeros((n, pool.shape[4]))
+    for j in range(n) if wanted is None else np.flatnonzero(wanted):
         g, i = slot_of(table_row, j, bs)
         out[j] = pool[layer, g, i, h] if sc is None else E4M3[pool[layer, g, i, h]] * float(sc[layer, g, h, i])
     return out
@@ -91,7 +91,19 @@ def ancestors(parent) -> np.ndarray:
     return see
 
 
-def attend(q, k, v, ks, vs, table, layer, row_off, kv_lens, scale, parent=None):
+def sight(T: int, L: int, parent=None, window: int = 0, sinks: int = 0) -> np.ndarray:
+    """[T, L]: what each of the last T of L positions sees. window > 0: of that, what lies less than `window` before its
+    own position (L - T and its place in the chain, or its depth in the tree), and the first `sinks`."""
+    see = np.ones((T, L), dtype=bool)
+    see[:, L - T:] = np.tril(np.ones((T, T), dtype=bool)) if parent is None else ancestors(parent)
+    if window > 0:
+        depth = np.arange(T) if parent is None else ancestors(parent).sum(1) - 1
+        place = np.concatenate([np.arange(L - T), L - T + depth])
+        see &= (place[None, L - T:].T - place[None, :] < window) | (np.arange(L) < sinks)
+    return see
+
+
+def attend(q, k, v, ks, vs, table, layer, row_off, kv_lens, scale, parent=None, window=0, sinks=0):
     """out [rows, Hq, D], lse [rows, Hq] and, for error bounds: the weighted mean of |v| (same shape as out), the
     largest |s| with its sum of |q k| terms [rows, Hq], and max |v| over the seen positions divided by the sum of the
     weights relative to the largest [rows, Hq]."""
@@ -107,10 +119,9 @@ def attend(q, k, v, ks, vs, table, layer, row_off, kv_lens, scale, parent=None):
         lo, T, L = int(row_off[b]), int(row_off[b + 1] - row_off[b]), int(kv_lens[b])
         if T == 0:
             continue
-        see = np.ones((T, L), dtype=bool)
-        see[:, L - T:] = np.tril(np.ones((T, T), dtype=bool)) if parent is None else ancestors(parent[lo:lo + T])
+        see = sight(T, L, None if parent is None else parent[lo:lo + T], window, sinks)
         for h in range(H):
-            kk, vv = entries(k, ks, table[b], layer, h, L), entries(v, vs, table[b], layer, h, L)
+            kk, vv = (entries(p, sc, table[b], layer, h, L, see.any(0)) for p, sc in ((k, ks), (v, vs)))
             for g in range(G):
                 for t in range(T):
                     ok = see[t]
@@ -145,3 +156,41 @@ def compact(pools, scales, table, node_off, path, accepted, kv_lens):
                     s[:, gd, :, sd] = s[:, gs, :, ss]
         new[b] = kv_lens[b] - (N - 1 - int(accepted[b]))
     return new
+
+
+def depths(parent) -> np.ndarray:
+    return ancestors(parent).sum(1) - 1
+
+
+def axis_of_pair(half: int, sections=None, alternating=False) -> np.ndarray:
+    """The axis each pair turns by: sections in blocks, or in turn as long as each lasts, the rest by axis 0."""
+    if sections is None:
+        return np.zeros(half, dtype=int)
+    if not alternating:
+        return np.repeat(np.arange(len(sections)), sections)
+    n = len(sections)
+    return np.array([i % n if i // n < sections[i % n] else 0 for i in range(half)])
+
+
+def rope(x, positions, inv_freq, *, adjacent=False, sections=None, alternating=False, factor=1.0):
+    """x [rows, heads, D] float64, positions [axes, rows], inv_freq [half] as float32 values: the pairs as complex
+    numbers, each times factor e^(i angle). The angle's turns are taken in 128-bit whole numbers, so that they are good
+    for any position."""
+    half = len(inv_freq)
+    axis = axis_of_pair(half, sections, alternating)
+    num, den = 2 * 2646693125139304345, 842468587426513207  # 2 pi, to 36 digits
+    turn = np.empty((x.shape[0], half))
+    for i in range(half):
+        m, e = np.frexp(np.float64(inv_freq[i]))
+        whole, shift = int(m * 2**24), int(24 - e)  # inv_freq = whole / 2^shift, exactly
+        for r in range(x.shape[0]):
+            up = int(positions[axis[i]][r]) * whole * den
+            down = num << shift if shift >= 0 else num
+            up = up if shift >= 0 else up << -shift
+            turn[r, i] = (up % down) / down
+    z = np.exp(2j * np.pi * turn)[:, None, :] * factor
+    y = np.array(x, dtype=np.float64)
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if adjacent else (slice(0, half), slice(half, 2 * half))
+    w = (y[..., a] + 1j * y[..., b]) * z
+    y[..., a], y[..., b] = w.real, w.imag
+    return y

@@ -11,8 +11,10 @@ Low-level entry points (same names as the C ABI):
     spec_debug_philox, spec_debug_row_stats, spec_debug_probs
     spec_kv_append, spec_kv_gather, spec_kv_compact, spec_kv_attend,
     spec_kv_attend_workspace_size (the paged key-value cache)
-Convenience: VerifyArgs, AttendArgs, KVCache (build the argument structs from
-tensors), Workspace.
+    spec_kv_append_rope, spec_rope, spec_kv_attend_window (rotary positions, a
+    sliding window with sinks)
+Convenience: VerifyArgs, AttendArgs, KVCache, Rope (build the argument structs
+from tensors), Workspace.
 """
 from __future__ import annotations
 
@@ -36,6 +38,7 @@ SEQ_OK, SEQ_BAD_TOKEN, SEQ_BAD_KV, SEQ_BAD_ROW, SEQ_BAD_LAYOUT, SEQ_BAD_TEMP = 0
 SEQ_TIMEOUT, SEQ_UNSUPPORTED = 6, 7
 SPEC_TREE_MAX_CANDIDATES = 64
 SPEC_KV_MAX_QUERIES = 128
+SPEC_ROPE_MAX_AXES = 4
 
 
 class SpecError(RuntimeError):
@@ -162,6 +165,46 @@ class SpecKvAttendArgs(ctypes.Structure):
     ]
 
 
+class SpecRope(ctypes.Structure):
+    """Mirror of spec_rope_t."""
+
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("rotary_dim", ctypes.c_int32),
+        ("adjacent", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * SPEC_ROPE_MAX_AXES),
+        ("alternating", ctypes.c_int32),
+        ("factor", ctypes.c_float),
+        ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class SpecKvAppendRopeArgs(ctypes.Structure):
+    """Mirror of spec_kv_append_rope_args_t."""
+
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("layer", ctypes.c_int32),
+        ("new_dtype", ctypes.c_int32),
+        ("t_max", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("row_off", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("parent", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p),
+        ("new_token_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_out_token_stride", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32),
+        ("seq_status", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -232,6 +275,13 @@ def lib():
             L.spec_kv_attend_workspace_size.argtypes = [C, T]
             L.spec_kv_attend.restype = ctypes.c_int
             L.spec_kv_attend.argtypes = [C, T, vp]
+            L.spec_kv_attend_window.restype = ctypes.c_int
+            L.spec_kv_attend_window.argtypes = [C, T, i32, i32, vp]
+            R = ctypes.POINTER(SpecRope)
+            L.spec_rope.restype = ctypes.c_int
+            L.spec_rope.argtypes = [R, vp, i32, i64, vp, i32, i64, i64, i32, i32, vp, vp]
+            L.spec_kv_append_rope.restype = ctypes.c_int
+            L.spec_kv_append_rope.argtypes = [C, R, ctypes.POINTER(SpecKvAppendRopeArgs), vp]
             if L.spec_abi_version() != SPEC_ABI_VERSION:
                 raise ImportError("libspecverify.so ABI version mismatch")
             _lib = L
@@ -528,6 +578,33 @@ class AttendArgs:
         self.struct.layer = int(layer)
 
 
+class Rope:
+    """spec_rope_t over a CUDA tensor, which it keeps alive.
+
+    inv_freq: float32 [rotary_dim / 2], radians for one position; the first
+    rotary_dim elements of a head turn. adjacent: pairs are neighbours, not
+    halves. sections: pairs of each axis (2 to 4 axes), in blocks or
+    alternating; None: one axis. factor: of cosines and sines.
+    """
+
+    def __init__(self, inv_freq, *, adjacent=False, sections=None, alternating=False, factor=1.0):
+        _check_typed(inv_freq, "inv_freq", _types().float32, optional=False)
+        sections = [] if sections is None else [int(x) for x in sections]
+        if sections and not 2 <= len(sections) <= SPEC_ROPE_MAX_AXES:
+            raise ValueError(f"sections must name 2 to {SPEC_ROPE_MAX_AXES} axes, got {len(sections)}")
+        self.inv_freq = inv_freq
+        r = SpecRope()
+        r.struct_size = ctypes.sizeof(SpecRope)
+        r.rotary_dim = 2 * inv_freq.numel()
+        r.adjacent, r.alternating = int(bool(adjacent)), int(bool(alternating and sections))
+        r.axes = max(1, len(sections))
+        for i, n in enumerate(sections):
+            r.sections[i] = n
+        r.factor, r.inv_freq = float(factor), inv_freq.data_ptr()
+        self.struct = r
+        self.ref = ctypes.byref(r)
+
+
 def check(status: int, what: str = "spec call"):
     if status != SPEC_OK:
         raise SpecError(status, what)
@@ -702,6 +779,73 @@ def spec_kv_attend_workspace_size(args: AttendArgs) -> int:
 def spec_kv_attend(args: AttendArgs, stream=None) -> int:
     """Attention of every sequence's new tokens over its cache (see AttendArgs)."""
     return (_lib or lib()).spec_kv_attend(args.cache.ref, args.ref, _stream(stream))
+
+
+def spec_kv_attend_window(args: AttendArgs, window: int, sinks: int = 0, stream=None) -> int:
+    """spec_kv_attend in which a token sees the `window` positions up to its own
+    and the cache's first `sinks`."""
+    return (_lib or lib()).spec_kv_attend_window(args.cache.ref, args.ref, window, sinks, _stream(stream))
+
+
+def _head_rows(t, name, dim=None) -> tuple:
+    """(rows, heads, row stride) of a CUDA tensor [rows, heads, head_dim] with a row's heads packed."""
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, heads, head_dim]")
+    rows, heads, d = t.shape
+    a, b, e = t.stride()
+    if (dim is not None and d != dim) or e != 1 or (heads > 1 and b != d):
+        raise ValueError(f"{name} must have packed heads" + ("" if dim is None else f" of {dim}"))
+    return rows, heads, (a if rows > 1 else 0)
+
+
+def _check_positions(t, rope, rows):
+    T = _types()
+    _check_typed(t, "positions", T.int32, rope.struct.axes * rows)
+
+
+def spec_rope(rope: Rope, x, out, positions, stream=None) -> int:
+    """Rotate rows x [rows, heads, head_dim] (bfloat16 or float32, a row's
+    heads packed) into out (of that shape; x itself: in place). positions:
+    int32 [rows], or [axes, rows]."""
+    rows, heads, stride = _head_rows(x, "x")
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    out_stride = _head_rows(out, "out")[2]
+    if positions is None:
+        raise ValueError("positions is required")
+    _check_positions(positions, rope, rows)
+    return (_lib or lib()).spec_rope(rope.ref, x.data_ptr(), _dtype_code(x, "x"), stride, out.data_ptr(),
+                                     _dtype_code(out, "out"), out_stride, rows, heads, x.shape[2], positions.data_ptr(),
+                                     _stream(stream))
+
+
+def spec_kv_append_rope(cache: KVCache, rope: Rope, k_new, v_new, kv_lens, row_off=None, t_max=None, parent=None,
+                        positions=None, q=None, q_out=None, layer=0, seq_status=None, stream=None) -> int:
+    """spec_kv_append with the keys rotated on the way, and the queries q
+    [rows, q_heads, head_dim] (k_new's type) into q_out (bfloat16; q itself: in
+    place). Positions are the cache's own (parent int32 [rows]: by depth in a
+    token tree), or given: int32 [rows], or [axes, rows]."""
+    T, c = _types(), cache.struct
+    rows, stride = _entry_rows(k_new, "k_new", c)
+    if v_new.dtype is not k_new.dtype or _entry_rows(v_new, "v_new", c) != (rows, stride):
+        raise ValueError("k_new and v_new must have one type, shape and row stride")
+    _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
+    _check_typed(row_off, "row_off", T.int64, c.batch + 1)
+    _check_typed(parent, "parent", T.int32, rows)
+    _check_positions(positions, rope, rows)
+    _check_typed(seq_status, "seq_status", T.int32, c.batch)
+    qp = outp = None
+    q_heads = q_stride = out_stride = 0
+    if q is not None:
+        n, q_heads, q_stride = _head_rows(q, "q", c.head_dim)
+        if n != rows or q.dtype is not k_new.dtype or q_out is None or q_out.shape != q.shape or q_out.dtype is not T.bfloat16:
+            raise ValueError("q must have k_new's rows and type, and q_out its shape in bfloat16")
+        out_stride = _head_rows(q_out, "q_out", c.head_dim)[2]
+        qp, outp = q.data_ptr(), q_out.data_ptr()
+    a = SpecKvAppendRopeArgs(ctypes.sizeof(SpecKvAppendRopeArgs), layer, _dtype_code(k_new, "k_new"), t_max or 0, rows,
+                             _ptr(row_off), kv_lens.data_ptr(), _ptr(parent), _ptr(positions), k_new.data_ptr(),
+                             v_new.data_ptr(), stride, qp, outp, q_stride, out_stride, q_heads, _ptr(seq_status))
+    return (_lib or lib()).spec_kv_append_rope(cache.ref, rope.ref, ctypes.byref(a), _stream(stream))
 
 
 def spec_debug_philox(seed, rnd, seq_offset, batch, npos, out, stream=None) -> int:

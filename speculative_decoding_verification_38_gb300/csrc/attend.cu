@@ -22,7 +22,11 @@ int tile_rows(int64_t rows) {
     return 128;
 }
 
+// Slots of a box with a window: what is loaded for a few sinks, and past the window's ends.
+constexpr int kWindowBox = 16;
+
 constexpr size_t kPartAlign = 256;
+constexpr size_t kDepthBytes = (size_t)kAttMaxGrid * kKvMaxQueries;  // behind the parts
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 
@@ -70,7 +74,7 @@ bool attend_takes(int32_t head_dim) { return head_dim <= 128; }
 
 size_t attend_workspace(int64_t rows) {
     const size_t n = (size_t)kAttMaxGrid * 2 * tile_rows(rows);
-    return kHeaderBytes + (n * 128 * 4 + n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign;
+    return kHeaderBytes + (n * 128 * 4 + n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign + kDepthBytes;
 }
 
 cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
@@ -90,7 +94,8 @@ cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
     p.device = dev;
     p.box = 1;
     p.box_log = 0;
-    while (p.box < kTileTok && a.c.bs % (2 * p.box) == 0) p.box *= 2, ++p.box_log;
+    const int widest = a.window ? kWindowBox : kTileTok;
+    while (p.box < widest && a.c.bs % (2 * p.box) == 0) p.box *= 2, ++p.box_log;
     if ((e = box_map(p.k_map, a.c, a.c.k, p.box)) != cudaSuccess) return e;
     if ((e = box_map(p.v_map, a.c, a.c.v, p.box)) != cudaSuccess) return e;
     const int n = tile_rows((int64_t)a.t_max * a.G);
@@ -101,6 +106,11 @@ cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {
     p.late = (int32_t*)(ws + kLateOffset);
     p.part_o = (float*)(ws + kHeaderBytes);
     p.part_ml = (float2*)(ws + kHeaderBytes + (size_t)grid * 2 * n * 128 * 4);
+    p.depth = (unsigned char*)(p.part_ml + (size_t)grid * 2 * n);
+    if (a.window) {
+        if (a.c.esz == 1) return n < 48 ? attend_window_e4m3(n, p, s) : attend_window_e4m3_wide(n, p, s);
+        return n < 48 ? attend_window_bf16(n, p, s) : attend_window_bf16_wide(n, p, s);
+    }
     if (a.c.esz == 1) return n < 48 ? attend_e4m3(n, p, s) : attend_e4m3_wide(n, p, s);
     return n < 48 ? attend_bf16(n, p, s) : attend_bf16_wide(n, p, s);
 }

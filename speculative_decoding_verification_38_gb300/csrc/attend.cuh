@@ -64,6 +64,7 @@ struct AttParams {
     uint32_t* err;
     uint32_t* left;    // CTAs that are done, and whether one of them gave up: zero between calls
     int32_t* late;     // [grid][2] sequences of the CTAs that gave up: zero between calls
+    unsigned char* depth;  // [grid][kKvMaxQueries] a window's trees, where shared memory is full
     int32_t grid, device;
 };
 
@@ -72,6 +73,11 @@ cudaError_t attend_bf16(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_bf16_wide(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_e4m3(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_e4m3_wide(int n, const AttParams& p, cudaStream_t s);
+// The same with a sliding window (p.a.window > 0).
+cudaError_t attend_window_bf16(int n, const AttParams& p, cudaStream_t s);
+cudaError_t attend_window_bf16_wide(int n, const AttParams& p, cudaStream_t s);
+cudaError_t attend_window_e4m3(int n, const AttParams& p, cudaStream_t s);
+cudaError_t attend_window_e4m3_wide(int n, const AttParams& p, cudaStream_t s);
 
 constexpr int kAttMaxGrid = 160;  // CTAs (the workspace holds two parts for each)
 
@@ -253,8 +259,39 @@ struct __align__(16) Seg {
     int32_t c0, c1;              // the CTAs that share the entry
 };
 
+// What the tokens of a sequence see through a window: the tiles hold, box by box, the sinks, then the positions from
+// where every token sees them to the end, then those before that only some of them still see. A tile of positions that
+// all rows see thus never comes after one that parts them, as the e4m3 units need it, and no box is loaded that no row
+// sees a position of. Places [0, s1) are positions as they are, [s1, i1) are di further on, [i1, end) are de further on.
+struct Sight {
+    int32_t s1, i1, di, de, end;
+    int32_t lo;    // the first position that the first token's window holds
+    int32_t tail;  // the first place from which rows may part: new tokens, or the window's end
+    __device__ __forceinline__ Sight() {}
+    __device__ __forceinline__ Sight(int32_t T, int32_t L, int32_t window, int32_t sinks, int32_t box_log) {
+        const int32_t ctx = L - T, more = (1 << box_log) - 1;
+        lo = max(0, ctx + 1 - window);
+        const int32_t first = min(sinks, L), up = (first + more) & ~more;
+        s1 = lo < up ? first & ~more : up;  // (a box that the sinks end in, within the window, is the window's)
+        const int32_t last = (L + more) & ~more, e0 = max(s1, lo & ~more);
+        const int32_t i0 = min(max((max(0, ctx + T - window) + more) & ~more, e0), last);
+        di = i0 - s1;
+        i1 = last - di;
+        de = e0 - i1;
+        end = i1 + i0 - e0;
+        tail = ctx < s1 ? ctx : ctx < i0 ? s1 : ctx - di;
+    }
+    __device__ __forceinline__ int32_t at(int32_t place) const {  // a position past any length where there is none
+        return place < s1 ? place : place < i1 ? place + di : place < end ? place + de : INT32_MAX;
+    }
+    // at once for places of one box; whether some token sees it
+    __device__ __forceinline__ bool seen(int32_t pos, int32_t L, int32_t sinks) const {
+        return pos < L && (pos < sinks || pos >= lo);
+    }
+};
+
 // ------------------------------------------------------------------ layout
-template <int NN, int DP, bool Q8>
+template <int NN, int DP, bool Q8, bool Win>
 struct Shape {
     static constexpr int N = NN;                           // query rows of a row tile
     static constexpr bool tight = !Q8 && N == 128 && DP == 128;  // shared memory and TMEM are full
@@ -281,13 +318,14 @@ struct Shape {
     static constexpr uint32_t q_bytes = Q8 ? 3 * N * 128 : N * DP * 2;  // e4m3: three parts
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
-    static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 6 : 8;  // tiles of them: more than the K ring and scores can hold
+    static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 6 : tight && Win ? 7 : 8;  // tiles of them: more than the K ring and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + (Q8 ? 4 * MC * 8 : 0);  // a group's scratch
     // after the tiles, Q and P: aux ring, per team and row the reference, weight sum, factor and (e4m3) unit, row factors
-    // of Q, scratch, ancestors, segments, poison, barriers
+    // of Q, scratch, ancestors, (window) depths and poison before the new tokens, segments, poison, barriers
     static constexpr uint32_t state = tight ? N * 4 : (Q8 ? 4 : 3) * TM * N * 4;
     static constexpr uint32_t misc = aux_ring * aux_bytes + state + (Q8 ? segs * N * 4 : 0) +
-                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + segs * sizeof(Seg) + (tight ? 40 : 48) +
+                                     (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + (Win ? 16 + (tight ? 0 : kKvMaxQueries) : 0) + segs * sizeof(Seg) +
+                                     (tight ? 40 : 48) +
                                      (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * RV : 0)) * 8 +
                                      (2 * SB + 2 * PS + 5 + aux_ring + 2 * segs) * 8;
     static constexpr int room = (int)(kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc), fit = room / slot_bytes;
@@ -310,28 +348,31 @@ constexpr int kOver = 5;
 // Kept out of line: the few places that divide 64-bit numbers do so once in a while, and their code is large.
 __device__ __noinline__ int64_t divide(int64_t a, int64_t b) { return a / b; }
 
-template <int N>
+template <int N, bool Win>
 struct Walk {
     const KvAttend& a;
+    const int32_t box_log;
     int64_t u, u1, per, first;  // place, end; where the entry at hand begins
     int32_t b, h, rt;           // the entry
     KvSeq s;
     int32_t tiles, nrt;
 
-    __device__ __forceinline__ static int64_t count(const KvAttend& a, int32_t b, KvSeq& s, int32_t& tiles,
+    __device__ __forceinline__ static int64_t count(const KvAttend& a, int32_t box_log, int32_t b, KvSeq& s, int32_t& tiles,
                                                     int32_t& nrt) {
         s = kv_seq(b, a.row_off, a.t_max, a.rows, a.kv_lens, a.c.bs, a.c.max_blocks, true);
         tiles = nrt = 0;
         if (s.st != kKvOk || s.T == 0) return 0;
-        tiles = (s.L + kTileTok - 1) / kTileTok;
+        const int32_t places = Win ? Sight(s.T, s.L, a.window, a.sinks, box_log).end : s.L;
+        tiles = (places + kTileTok - 1) / kTileTok;
         nrt = (s.T * a.G + N - 1) / N;
         return (int64_t)(tiles + kOver) * nrt * a.c.H;
     }
     // base0: where sequence b0 begins, which has u0 in it
-    __device__ __forceinline__ Walk(const KvAttend& a_, int64_t u0, int64_t u1_, int64_t per_, int32_t b0, int64_t base0)
-        : a(a_), u(u0), u1(u1_), per(per_), b(b0), h(0), rt(0) {
+    __device__ __forceinline__ Walk(const KvAttend& a_, int32_t box_log_, int64_t u0, int64_t u1_, int64_t per_, int32_t b0,
+                                    int64_t base0)
+        : a(a_), box_log(box_log_), u(u0), u1(u1_), per(per_), b(b0), h(0), rt(0) {
         if (u >= u1) return;
-        count(a, b, s, tiles, nrt);
+        count(a, box_log, b, s, tiles, nrt);
         const int64_t e = divide(u - base0, tiles + kOver);
         h = (int32_t)divide(e, nrt);
         rt = (int32_t)(e - (int64_t)h * nrt);
@@ -368,7 +409,7 @@ struct Walk {
                             u = u1;
                             break;
                         }
-                    } while (count(a, b, s, tiles, nrt) == 0);
+                    } while (count(a, box_log, b, s, tiles, nrt) == 0);
                 }
             }
             if (g.n) return;
@@ -537,9 +578,9 @@ __device__ __noinline__ void join_many(Join w, float* f_sm) {
     }
 }
 
-template <int NN, int DP, bool Q8>
-__global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
-    using X = Shape<NN, DP, Q8>;
+template <int NN, int DP, bool Q8, bool Win>
+__global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_kernel(const __grid_constant__ AttParams p) {
+    using X = Shape<NN, DP, Q8, Win>;
     constexpr int N = X::N, MC = X::MC, R = X::segs, QB = X::QB, TM = X::TM, SB = X::SB, PS = X::PS, kAuxRing = X::aux_ring;
     constexpr uint32_t SK = X::SK, SV = X::SV, RV = X::RV;
     constexpr int kAttThreads = X::threads;
@@ -557,7 +598,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     float* const arow_all = mref_all + X::state / 4;  // Q8: [R][N] a query row's power of two times scale * log2(e)
     unsigned char* const red_sm = (unsigned char*)(arow_all + (Q8 ? R * N : 0));
     uint32_t* const seen_by = (uint32_t*)(red_sm + (X::tight ? 0 : kGroups * X::red_bytes));  // [T][4] the tokens that see a tree's token
-    Seg* const segs = (Seg*)(seen_by + kKvMaxQueries * 4);
+    uint32_t* const early = seen_by + kKvMaxQueries * 4;  // Win: [4] poison, positions from the window's end
+    // Win: depths of a tree's tokens (tight: in the workspace, this CTA's own)
+    unsigned char* const depth = X::tight ? p.depth + blockIdx.x * kKvMaxQueries : (unsigned char*)(early + (Win ? 4 : 0));
+    Seg* const segs = (Seg*)(early + (Win ? 4 + (X::tight ? 0 : kKvMaxQueries / 4) : 0));
     uint32_t* const poison = (uint32_t*)(segs + R);  // [4] new tokens with non-finite values, then:
     volatile uint32_t* const aborted = poison + 4;   // a wait gave up
     uint32_t* const tmem_at = poison + 5;
@@ -676,7 +720,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     for (int32_t b = bt0; b < bt1; ++b) {
         KvSeq s;
         int32_t tiles, nrt;
-        mine += Walk<N>::count(a, b, s, tiles, nrt);
+        mine += Walk<N, Win>::count(a, p.box_log, b, s, tiles, nrt);
     }
     int64_t incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
@@ -703,7 +747,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         for (; b + 1 < bt1; ++b) {
             KvSeq s;
             int32_t tiles, nrt;
-            const int64_t k = Walk<N>::count(a, b, s, tiles, nrt);
+            const int64_t k = Walk<N, Win>::count(a, p.box_log, b, s, tiles, nrt);
             if (u0 < at + k) break;
             at += k;
         }
@@ -728,22 +772,36 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         if (pos < L) pg = table[c.by_bs.of(pos)];
         return pg >= 0 && pg < c.num_blocks ? pg : c.num_blocks;
     };
+    // (Win: `at` counts places, g's positions go by its sight)
+    auto sight_of = [&](const Seg* g) { return Win ? Sight(g->T, g->L, a.window, a.sinks, p.box_log) : Sight(); };
+    auto position = [&](const Sight& sight, int32_t place) { return Win ? sight.at(place) : place; };
     auto bring = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar, const int32_t* table, int32_t at, int32_t L,
-                     int32_t head, int32_t pages) {  // pages: of boxes 0 .. 31, a lane each
+                     int32_t head, int32_t pages, const Sight& sight) {  // pages: of boxes 0 .. 31, a lane each
         if (elect()) mbar_arrive_expect_tx(bar, kTileTok * (Q8 || DP == 64 ? 128 : 256));
         __syncwarp();
-        int32_t sl = at - c.by_bs.of(at) * c.bs;
+        int32_t sl = at - c.by_bs.of(at) * c.bs, slots = 0;
+        auto slot_at = [&](int j) {  // Win: a box's slot, by its own position
+            const int32_t pos = sight.at(at + (j + lane) * p.box);
+            slots = pos < L ? pos - c.by_bs.of(pos) * c.bs : 0;
+        };
+        if (Win) slot_at(0);
 #pragma unroll 1
         for (int j = 0; j < boxes; ++j) {
-            if (j && (j & 31) == 0) pages = page_of(table, at + (j + lane) * p.box, L);
+            if (j && (j & 31) == 0) {
+                pages = page_of(table, position(sight, at + (j + lane) * p.box), L);
+                if (Win) slot_at(j);
+            }
             const int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, j & 31);
+            if (Win) sl = __shfl_sync(0xFFFFFFFFu, slots, j & 31);
             if (elect()) {
                 tma_box(dst, map, 0, sl, head, pg, bar);
                 if (!Q8 && DP == 128) tma_box(dst + kTileTok * 128, map, 64, sl, head, pg, bar);
             }
             dst += p.box * 128;
-            sl += p.box;
-            if (sl >= c.bs) sl = 0;
+            if (!Win) {
+                sl += p.box;
+                if (sl >= c.bs) sl = 0;
+            }
         }
         __syncwarp();
     };
@@ -770,7 +828,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 if (!n) break;
                 const Seg* const g = segs + si % R;
                 const int32_t L = g->L, h = g->h, row0 = g->rt * N, rows = min(N, g->T * a.G - row0);
-                int32_t pos = g->tile0 * kTileTok + fw * 32 + lane;
+                const Sight sight = sight_of(g);
+                int32_t place = g->tile0 * kTileTok + fw * 32 + lane, pos = position(sight, place);
                 const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
                 const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)h * a.G * c.D * 2 + piece * 16;
                 done_seg(si);
@@ -779,14 +838,15 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                 bool in = false;
                 // scales of the row at pos, its page known; on to the next tile's page
                 auto scales = [&]() {
-                    in = pg >= 0 && pg < c.num_blocks;
+                    in = pg >= 0 && pg < c.num_blocks && (!Win || sight.seen(pos, L, a.sinks));
                     sk = sv = 0.f;
                     if (in) {
                         const int64_t i = ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs);
                         sk = c.ks[i];
                         sv = c.vs[i];
                     }
-                    pos += kTileTok;
+                    place += kTileTok;
+                    pos = position(sight, place);
                     pg = pos < L ? table[c.by_bs.of(pos)] : -1;
                 };
                 scales();
@@ -1040,7 +1100,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
         }
     } else if (warp == kSegWarp) {
         // ============================================================ segments, K
-        Walk<N> walk(a, u0, u1, per, b0, base0);
+        Walk<N, Win> walk(a, p.box_log, u0, u1, per, b0, base0);
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.k_map) : "memory");
         uint32_t kt = 0, loads = 0;  // (loads: fewer than tiles after a wait that gave up)
         for (uint32_t s = 0;; ++s) {
@@ -1060,15 +1120,16 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             const int n = __shfl_sync(0xFFFFFFFFu, g.n, 0);
             const int32_t* const table = c.table + (int64_t)g.b * c.max_blocks;
             int32_t at = g.tile0 * kTileTok;
-            int32_t next = page_of(table, at + lane * p.box, g.L);
+            const Sight sight = sight_of(&g);
+            int32_t next = page_of(table, position(sight, at + lane * p.box), g.L);
 #pragma unroll 1
             for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
                 const int32_t pages = next;
-                if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, g.L);
+                if (t + 1 < n) next = page_of(table, position(sight, at + kTileTok + lane * p.box), g.L);
                 const uint32_t slot = kt % SK;
                 const bool free = kt < SK || wait(k_empty + slot, (kt / SK - 1) & 1);
                 if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                    bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages);
+                    bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages, sight);
                     ++loads;
                 }
                 if constexpr (!Q8) {
@@ -1078,8 +1139,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     for (int w = 0; w < 4; ++w) {
                         const int32_t r = w * 32 + lane;
                         int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, (r >> p.box_log) & 31);
-                        if (boxes > 32) pg = page_of(table, at + r, g.L);
-                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, pg < c.num_blocks && at + r < g.L);
+                        const int32_t pos = position(sight, at + r);
+                        if (boxes > 32) pg = page_of(table, pos, g.L);
+                        const uint32_t bits =
+                            __ballot_sync(0xFFFFFFFFu, pg < c.num_blocks && (Win ? sight.seen(pos, g.L, a.sinks) : pos < g.L));
                         if (lane == 0) aux[w] = bits;
                     }
                     if (lane == 0) mbar_arrive(aux_full + kt % kAuxRing);
@@ -1118,12 +1181,16 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             if (a.seq_status) {
                 if (st == kKvOk) {
                     bad = false;
-                    if (s.T > 0)
+                    if (s.T > 0) {
+                        // Win: the sinks' pages, then the window's
+                        const int32_t gap = Win ? c.by_bs.of(max(0, s.L - s.T + 1 - a.window)) : 0;
+                        const int32_t first = Win ? min(gap, (int32_t)(((int64_t)min(a.sinks, s.L) + c.bs - 1) / c.bs)) : 0;
 #pragma unroll 1
-                        for (int32_t j = lane; j <= c.by_bs.of(s.L - 1); j += 32) {
-                            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+                        for (int32_t j = lane; j <= c.by_bs.of(s.L - 1) - (gap - first); j += 32) {
+                            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j + (j >= first ? gap - first : 0)];
                             bad |= pg < 0 || pg >= c.num_blocks;
                         }
+                    }
                     if (__any_sync(0xFFFFFFFFu, bad)) st = kKvBadLayout;
                 }
                 if (lane == 0) a.seq_status[b] = st;
@@ -1139,24 +1206,25 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     const int32_t L = g->L, h = g->h;
                     int32_t at = g->tile0 * kTileTok;
                     const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
+                    const Sight sight = sight_of(g);
                     done_seg(si++);
-                    int32_t next = page_of(table, at + lane * p.box, L);
+                    int32_t next = page_of(table, position(sight, at + lane * p.box), L);
 #pragma unroll 1
                     for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
                         const int32_t pages = next;
-                        if (t + 1 < n) next = page_of(table, at + kTileTok + lane * p.box, L);
+                        if (t + 1 < n) next = page_of(table, position(sight, at + kTileTok + lane * p.box), L);
                         if constexpr (Q8) {
                             const uint32_t slot = kt % RV;
                             const bool free = kt < RV || wait(raw_empty + slot, (kt / RV - 1) & 1);
                             if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                                bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages);
+                                bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages, sight);
                                 ++loads;
                             }
                         } else {
                             const uint32_t slot = kt % SV;
                             const bool free = kt < SV || wait(v_empty + slot, (kt / SV - 1) & 1);
                             if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                                bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages);
+                                bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages, sight);
                                 ++loads;
                             }
                         }
@@ -1218,6 +1286,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             if (!X::tight && tid < TM * N) lsum[tid] = 0.f;  // of a team without a tile here
             if (Q8 && tid < TM * N) unit_all[tid] = first_unit;
             if (tid < 4) poison[tid] = 0;
+            if (Win && tid < 4) early[tid] = 0;
             // (all of them go on or none does: they meet at barriers)
             if (!here) *lost = 1;
             bar_sync(bar_all, kSoftThreads);
@@ -1229,6 +1298,12 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             const int pieces = (rows + 7) / 8;
             const int live = (int)sub < pieces ? (pieces - (int)sub + X::GT - 1) / X::GT : 0;  // this group's pieces
             const float* const arow = arow_all + (si % R) * N;
+            const Sight sight = sight_of(g);
+            // Win: the largest depth of a token that sees position `pos` (as far as it is on its way)
+            auto reach = [&](int32_t pos) {
+                const int32_t u = pos - ctx;
+                return pos < a.sinks ? kKvMaxQueries : (u >= 0 && a.parent ? (int32_t)depth[u] : u) + a.window - 1;
+            };
             if (a.parent && g->b != tree_of) {
                 tree_of = g->b;
                 // ancestors by doubling: after k rounds a token knows those up to 2^k - 1 above it
@@ -1265,6 +1340,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     jump = far;
                     bar_sync(bar_all, kSoftThreads);
                 }
+                if (Win && tid < kKvMaxQueries)
+                    depth[tid] = (unsigned char)(__popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]) - (tid < T));
                 // and turned round: those that a token's entry is seen by, which is what a position's thread asks for
                 if (tid < kKvMaxQueries) {
 #pragma unroll
@@ -1301,15 +1378,16 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     const bool in = ((const uint32_t*)aux)[wq] >> lane & 1;
                     const float ks = Q8 ? ((const float*)(aux + 16))[wt] : 1.f;
                     const float vs = Q8 ? ((const float*)(aux + 16))[kTileTok + wt] : 1.f;
-                    const int32_t pos0 = (g->tile0 + i) * kTileTok, pos = pos0 + wt;
+                    const int32_t pos0 = (g->tile0 + i) * kTileTok, pos = position(sight, pos0 + wt);  // (Win: pos0 is a place)
                     const uint32_t s_at = tmem + buf * N + lanes + sub * 8;
-                    const bool tail = pos0 + kTileTok > ctx;
+                    const bool tail = pos0 + kTileTok > (Win ? sight.tail : ctx);
                     // rows that see this position (a bit for each of the group's rows), where not every row sees
                     // every one; a page outside the pool hides positions anywhere
                     using Rows = typename std::conditional<(MC > 4), uint64_t, uint32_t>::type;  // a bit for each
                     static_assert(MC * 8 <= 8 * (int)sizeof(Rows), "a bit for each row of the group");
                     Rows vis = in ? ~(Rows)0 : (Rows)0;
-                    if (tail && in && pos >= ctx) {
+                    const int32_t far = Win && tail && in ? reach(pos) : kKvMaxQueries;
+                    if (tail && in && (pos >= ctx || (Win && far < T - 1))) {
                         const int32_t u = pos - ctx;
                         vis = 0;
 #pragma unroll 1
@@ -1317,10 +1395,20 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             const int32_t r = row0 + (sub + X::GT * m) * 8, tk = a.by_G.of(r), w = tk >> 5;
                             int32_t left = (tk + 1) * a.G - r;  // rows of token tk from here
                             uint32_t see;                       // tokens tk, tk + 1, ..
-                            if (a.parent)
+                            if (Win && u < 0)
+                                see = ~0u;
+                            else if (a.parent)
                                 see = __funnelshift_r(w < 4 ? seen_by[u * 4 + w] : 0, w < 3 ? seen_by[u * 4 + w + 1] : 0, tk & 31);
                             else
                                 see = tk >= u ? ~0u : u - tk >= 8 ? 0u : ~0u << (u - tk);
+                            if (Win && far < T - 1) {  // not past the window
+                                if (!a.parent)
+                                    see &= far < tk ? 0u : far - tk >= 8 ? ~0u : (2u << (far - tk)) - 1;
+                                else
+#pragma unroll 1
+                                    for (int k = 0; k < 8; ++k)
+                                        if (depth[min(tk + k, kKvMaxQueries - 1)] > far) see &= ~(1u << k);
+                            }
                             uint32_t bits = 0;
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
@@ -1532,7 +1620,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                         if (i == first || moved || !bar_or(bar_gr, 128, top > grow || !(big <= 16384.f))) break;
                         sign = -1.f;
                     }
-                    if (tail && sub == 0 && (pos >= L || (in && pos >= ctx && T > 1))) {
+                    // (Win: a box's slots that no token sees are cleared too)
+                    const bool clear = Win ? !in && pos != INT32_MAX : pos >= L;
+                    const bool parts = Win ? in && T > 1 && (pos >= ctx || far < T - 1) : in && pos >= ctx && T > 1;
+                    if ((Win ? masked : tail) && sub == 0 && (clear || parts)) {
                         // The values of a page's slots past the length are cleared. A new token's values that are not
                         // finite would reach rows that do not see it (0 * inf): they leave the tile here and join the
                         // rows that do see it at the end.
@@ -1546,7 +1637,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll 1
                         for (int k = 0; k < DP / 8; ++k) {
                             uint4* const at = (uint4*)(v_row + (k >> 3) * (kTileTok * 128) + (k & 7) * 16);
-                            if (pos >= L) {
+                            if (clear) {
                                 *at = make_uint4(0, 0, 0, 0);
                                 continue;
                             }
@@ -1561,7 +1652,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                             if (here) *at = v;
                             found |= here;
                         }
-                        if (found) atomicOr(poison + ((pos - ctx) >> 5), 1u << ((pos - ctx) & 31));
+                        if (found) {
+                            // (Win: one before the new tokens is its distance from the first token's window's end)
+                            const int32_t u = Win && pos < ctx ? pos - (ctx + 1 - a.window) : pos - ctx;
+                            atomicOr((Win && pos < ctx ? early : poison) + (u >> 5), 1u << (u & 31));
+                        }
                     }
                     tc_before();
                     fence_async();
@@ -1633,7 +1728,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
             for (int tm = 0; tm < TM; ++tm) has[tm] = finished(tm);
             tc_after();
             bar_sync(bar_all, kSoftThreads);
-            const bool any_poison = poison[0] | poison[1] | poison[2] | poison[3];
+            const bool any_poison = (poison[0] | poison[1] | poison[2] | poison[3]) ||
+                                    (Win && (early[0] | early[1] | early[2] | early[3]));
 #pragma unroll 1
             for (int piece = gr; piece < pieces; piece += kGroups) {
                 const int r0 = piece * 8;
@@ -1656,9 +1752,11 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
                     }
                 if (any_poison && wt < c.D) {
 #pragma unroll 1
-                    for (int32_t u = 0; u < T; ++u) {
-                        if (!(poison[u >> 5] >> (u & 31) & 1)) continue;
-                        const int32_t pos = ctx + u;
+                    for (int32_t i = 0; i < (Win ? 2 * T : T); ++i) {
+                        const int32_t e = i < T ? i : i - T;
+                        if (!((i < T ? poison : early)[e >> 5] >> (e & 31) & 1)) continue;
+                        const int32_t pos = i < T ? ctx + e : ctx + 1 - a.window + e, u = pos - ctx;
+                        const int32_t far = Win ? reach(pos) : kKvMaxQueries;
                         const int32_t pg = c.table[(int64_t)g->b * c.max_blocks + c.by_bs.of(pos)], sl = (pos - c.by_bs.of(pos) * c.bs);
                         if (pg < 0 || pg >= c.num_blocks) continue;  // (only after a wait has given up)
                         const unsigned char* v = c.v + pg * c.block_bytes + sl * c.token_bytes + g->h * c.head_bytes;
@@ -1667,7 +1765,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int32_t tk = a.by_G.of(row0 + r0 + k);
-                            if (a.parent ? tk < T && (seen_by[u * 4 + (tk >> 5)] >> (tk & 31) & 1) : tk >= u) o[k] += x;
+                            const bool after = a.parent ? tk < T && (u < 0 || (seen_by[u * 4 + (tk >> 5)] >> (tk & 31) & 1)) : tk >= u;
+                            if (after && (!Win || (a.parent ? (int32_t)depth[tk] : tk) <= far)) o[k] += x;
                         }
                     }
                 }
@@ -1738,10 +1837,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8>::threads, 1) attend_kernel(c
     }
 }
 
-template <int N, int DP, bool Q8>
+template <int N, int DP, bool Q8, bool Win>
 cudaError_t launch(const AttParams& p, cudaStream_t s) {
-    using X = Shape<N, DP, Q8>;
-    auto* f = attend_kernel<N, DP, Q8>;
+    using X = Shape<N, DP, Q8, Win>;
+    auto* f = attend_kernel<N, DP, Q8, Win>;
     // more than half of an SM's shared memory, whatever the ring took: one CTA on an SM owns its TMEM
     constexpr int bytes = (int)(X::total > kSmemMax / 2 + 1024 ? X::total : kSmemMax / 2 + 1024);
     static std::atomic<uint64_t> known{0};  // devices on which the kernel may use that much
@@ -1755,9 +1854,9 @@ cudaError_t launch(const AttParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int N, bool Q8>
+template <int N, bool Q8, bool Win = false>
 cudaError_t launch_dim(const AttParams& p, cudaStream_t s) {
-    return p.a.c.D <= 64 ? launch<N, 64, Q8>(p, s) : launch<N, 128, Q8>(p, s);
+    return p.a.c.D <= 64 ? launch<N, 64, Q8, Win>(p, s) : launch<N, 128, Q8, Win>(p, s);
 }
 
 }  // namespace

@@ -11,58 +11,6 @@ namespace {
 
 constexpr int kThreads = kKvThreads;
 
-// Status of each sequence, one warp each: the offsets and length by `st`,
-// then every page of positions [p0, L).
-__device__ __forceinline__ int32_t check_pages(const KvView& c, int32_t b, int64_t p0, int64_t L) {
-    const int lane = threadIdx.x & 31;
-    bool bad = false;
-    if (L > p0)
-        for (int64_t j = p0 / c.bs + lane; j <= (L - 1) / c.bs; j += 32) {
-            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
-            bad |= pg < 0 || pg >= c.num_blocks;
-        }
-    return __any_sync(0xFFFFFFFFu, bad) ? kKvBadLayout : kKvOk;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// The smallest power of two s >= 2^-126 with a / s <= 448 = 1.75 * 2^8, as
-// exponents: s = 2^e (a finite and >= 0; a = 0 gives 2^0).
-__device__ __forceinline__ int32_t scale_exponent(float a) {
-    const uint32_t w = __float_as_uint(a);
-    if (w == 0) return 0;
-    const int32_t e = (int32_t)(w >> 23) - 127 - 8 + ((w & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return max(e, -126);
-}
-__device__ __forceinline__ float pow2(int32_t e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
-
-// The eight values of lane `i` of an entry, as floats.
-template <int DT>
-__device__ __forceinline__ void load8(const unsigned char* row, int i, float (&x)[8]) {
-    if (DT == kKvBf16) {
-        const uint4 w = *(const uint4*)(row + 16 * i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = bf16_lo(u[j]);
-            x[2 * j + 1] = bf16_hi(u[j]);
-        }
-    } else {
-        const float4 a = *(const float4*)(row + 32 * i), b = *(const float4*)(row + 32 * i + 16);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-}
-
 // One entry (token, head) of K or V, `lanes` (a power of two, 8 values each)
 // threads together: scale from the largest finite value, codes, stores.
 template <int DT, bool Q8>
@@ -468,10 +416,13 @@ __device__ __forceinline__ void entry_at(const KvView& c, const unsigned char* r
     }
 }
 
+// Win: with a sliding window. A row's positions are then the sinks and, `skip` further on, those of its own window.
+template <bool Win>
 __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const KvAttend p) {
     __shared__ __align__(16) float q_sh[kKvMaxDim];
     __shared__ float o_sh[kPlainWarps][kKvMaxDim], m_sh[kPlainWarps], l_sh[kPlainWarps];
     __shared__ uint32_t anc[kKvMaxQueries / 32];
+    __shared__ int32_t depth_sh;
     static_assert(kKvMaxDim == 256 && kPlainWarps * 32 == kKvMaxDim, "eight columns to a lane, one to a thread");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const KvView& c = p.c;
@@ -487,7 +438,9 @@ __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const
         if (__any_sync(0xFFFFFFFFu, bad)) st = kKvBadLayout;
     }
     if (blockIdx.y == 0 && warp == 0 && p.seq_status) {
-        const int32_t st2 = st == kKvOk ? check_pages(c, b, 0, s.T ? s.L : 0) : st;
+        const int32_t lo = Win ? max(0, s.L - s.T + 1 - p.window) : 0;
+        int32_t st2 = st == kKvOk ? check_pages(c, b, lo, s.T ? s.L : 0) : st;
+        if (Win && st2 == kKvOk) st2 = check_pages(c, b, 0, s.T ? min(p.sinks, s.L) : 0);
         if (lane == 0) p.seq_status[b] = st2;
     }
     if (s.lo < 0) return;
@@ -509,13 +462,23 @@ __global__ void __launch_bounds__(kPlainWarps * 32) kv_attend_plain_kernel(const
         if (tid < c.D) q_sh[tid] = bf16_lo(*(const uint16_t*)(q + 2 * tid));
         if (tid < kKvMaxQueries / 32) anc[tid] = 0;
         __syncthreads();
-        if (p.parent && tid == 0)
-            for (int32_t v = t; v >= 0; v = p.parent[s.lo + v]) anc[v >> 5] |= 1u << (v & 31);
+        if (p.parent && tid == 0) {
+            int32_t up = 0;
+            for (int32_t v = t; v >= 0; v = p.parent[s.lo + v], ++up)
+                if (!Win || up < p.window || ctx + v < p.sinks) anc[v >> 5] |= 1u << (v & 31);
+            depth_sh = up - 1;
+        }
         __syncthreads();
         float m = none, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const int32_t last = p.parent ? s.L : ctx + t + 1;  // positions past it are not seen
-        for (int32_t j0 = warp * 32; j0 < last; j0 += kPlainWarps * 32) {
-            const int32_t j = j0 + lane;
+        int32_t near = 0, skip = 0;                         // Win: positions up to `near`, then `skip` further on
+        if (Win) {
+            const int32_t from = max(0, ctx + (p.parent ? depth_sh : t) + 1 - p.window);
+            near = min(p.sinks, p.parent ? min(ctx, from) : from);
+            skip = (p.parent ? min(ctx, from) : from) - near;
+        }
+        for (int32_t j0 = warp * 32; j0 < last - skip; j0 += kPlainWarps * 32) {
+            const int32_t j = j0 + lane + (Win && j0 + lane >= near ? skip : 0);
             float x = none, vscale = 1.f;
             int64_t at = -1;
             if (j < last && (!p.parent || j < ctx || (anc[(j - ctx) >> 5] >> ((j - ctx) & 31) & 1))) {
@@ -638,7 +601,8 @@ cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s) 
 
 cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s) {
     const int64_t y = std::min<int64_t>((int64_t)p.t_max * p.Hq, 65535);
-    kv_attend_plain_kernel<<<dim3((unsigned)p.c.B, (unsigned)y), kPlainWarps * 32, 0, s>>>(p);
+    auto* f = p.window ? kv_attend_plain_kernel<true> : kv_attend_plain_kernel<false>;
+    f<<<dim3((unsigned)p.c.B, (unsigned)y), kPlainWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 

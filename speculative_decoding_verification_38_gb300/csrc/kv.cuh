@@ -64,4 +64,56 @@ __device__ __forceinline__ float kv_e4m3(uint8_t code) {
     return (float)x;
 }
 
+// Status of each sequence, one warp each: the offsets and length by `st`,
+// then every page of positions [p0, L).
+__device__ __forceinline__ int32_t check_pages(const KvView& c, int32_t b, int64_t p0, int64_t L) {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    if (L > p0)
+        for (int64_t j = p0 / c.bs + lane; j <= (L - 1) / c.bs; j += 32) {
+            const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+            bad |= pg < 0 || pg >= c.num_blocks;
+        }
+    return __any_sync(0xFFFFFFFFu, bad) ? kKvBadLayout : kKvOk;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// The smallest power of two s >= 2^-126 with a / s <= 448 = 1.75 * 2^8, as
+// exponents: s = 2^e (a finite and >= 0; a = 0 gives 2^0).
+__device__ __forceinline__ int32_t scale_exponent(float a) {
+    const uint32_t w = __float_as_uint(a);
+    if (w == 0) return 0;
+    const int32_t e = (int32_t)(w >> 23) - 127 - 8 + ((w & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return max(e, -126);
+}
+__device__ __forceinline__ float pow2(int32_t e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
+
+// The eight values of lane `i` of an entry, as floats.
+template <int DT>
+__device__ __forceinline__ void load8(const unsigned char* row, int i, float (&x)[8]) {
+    if (DT == kKvBf16) {
+        const uint4 w = *(const uint4*)(row + 16 * i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16_lo(u[j]);
+            x[2 * j + 1] = bf16_hi(u[j]);
+        }
+    } else {
+        const float4 a = *(const float4*)(row + 32 * i), b = *(const float4*)(row + 32 * i + 16);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+
 }  // namespace specv

@@ -97,6 +97,30 @@ struct KvAttend {
     unsigned char* out;
     float* lse;
     int32_t* seq_status;
+    int32_t window, sinks;  // of a sliding window; window 0: every position before a token's own
+};
+
+// Rotary positions (rope.cu).
+constexpr int kRopeMaxAxes = 4;
+struct Rope {
+    const float* inv_freq;     // [half]
+    const int32_t* positions;  // [axes, rows], or null: the cache's own
+    int64_t rows;
+    int32_t rd, half;          // elements that turn, pairs of them
+    int32_t adjacent, one_axis;
+    float factor;
+    KvDiv by_heads;            // of the queries
+    uint32_t axis[kKvMaxDim / 2 / 16];  // two bits for each pair
+    __host__ __device__ int32_t axis_of(int32_t pair) const { return axis[pair >> 4] >> 2 * (pair & 15) & 3; }
+};
+
+// Rows of queries beside the cache's, or alone.
+struct RopeRows {
+    const unsigned char* x;
+    unsigned char* out;
+    int64_t x_row_bytes, out_row_bytes;
+    int32_t heads, D;
+    int32_t dtype, out_dtype;
 };
 
 // CTAs that a compaction gives each sequence: a thread for each 16-byte column, and each scale, of a token in all layers.
@@ -108,6 +132,10 @@ constexpr int64_t kKvCompactMaxCtas = 65535;  // a grid's second axis
 cudaError_t launch_kv_append(const KvView& c, const KvNew& n, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvView& c, const KvRead& r, cudaStream_t s);
 cudaError_t launch_kv_compact(const KvView& c, const KvMove& m, cudaStream_t s);
+// New tokens into the cache with their keys rotated, and q's rows (heads 0: none). parent: trees, or null.
+cudaError_t launch_kv_append_rope(const KvView& c, const KvNew& n, const Rope& r, const RopeRows& q, const int32_t* parent,
+                                  cudaStream_t s);
+cudaError_t launch_rope(const Rope& r, const RopeRows& q, int64_t rows, cudaStream_t s);
 // The attention on the tensor cores (attend.cu), for head_dim up to 128;
 // rows = t_max * query heads of a key-value head sets the workspace.
 bool attend_takes(int32_t head_dim);
