@@ -60,6 +60,8 @@ __device__ __forceinline__ int place_of(int pair, bool adjacent) {
     return adjacent ? pair : (pair & 4 ? kPairs / 2 : 0) + (pair >> 3) * 4 + (pair & 3);
 }
 
+constexpr int kResident = 4;             // CTAs on an SM: 64 registers a thread (3, 4, 5 and 6 of them: prompts 542, 490, 486
+                                         // and 606 us; a round 5.1, 5.1, 5.6 and 6.8)
 struct Token {
     int64_t at, scale;  // its entry in the cache: bytes, scales
     bool known, cached; // it has a position; its page is there
@@ -71,16 +73,45 @@ struct Chunks {
     bool has0, has1, turns;
 };
 
-// Both chunks of a row's head at `row`, turned. VEC: the rotary part is a multiple of 16 elements, so that pairs of halves
-// lie in the two chunks of one thread; otherwise an element's other half is fetched by itself.
-template <int DT, bool VEC>
-__device__ __forceinline__ void turned(const unsigned char* row, const Chunks& k, const Rope& r, const float* cs, const float* sn,
-                                       float (&x)[2][8]) {
+// A thread's chunks as they lie in memory.
+template <int DT>
+struct Raw {
+    uint4 w[DT == kKvBf16 ? 2 : 4];
+    __device__ __forceinline__ void load(const unsigned char* row, const Chunks& k, bool live) {
+        constexpr int per = DT == kKvBf16 ? 1 : 2;  // 16-byte words of a chunk
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[0][j] = x[1][j] = 0.f;
-    if (k.has0) load8<DT>(row, k.c0, x[0]);
-    if (k.has1) load8<DT>(row, k.c1, x[1]);
-    if (!k.turns) return;
+        for (int i = 0; i < 2 * per; ++i) {
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (live && (i < per ? k.has0 : k.has1)) w[i] = *((const uint4*)row + (i < per ? k.c0 : k.c1) * per + i % per);
+        }
+    }
+    __device__ __forceinline__ void floats(float (&x)[2][8]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (DT == kKvBf16) {
+                const uint32_t u[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[h][2 * j] = bf16_lo(u[j]);
+                    x[h][2 * j + 1] = bf16_hi(u[j]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 u = w[(2 * h + i) % (DT == kKvBf16 ? 2 : 4)];
+                    x[h][4 * i] = __uint_as_float(u.x), x[h][4 * i + 1] = __uint_as_float(u.y);
+                    x[h][4 * i + 2] = __uint_as_float(u.z), x[h][4 * i + 3] = __uint_as_float(u.w);
+                }
+            }
+        }
+    }
+};
+
+// Both chunks of a row's head (at `row`), turned. VEC: the rotary part is a multiple of 16 elements, so that pairs of
+// halves lie in the two chunks of one thread; otherwise an element's other half is fetched by itself.
+template <int DT, bool VEC>
+__device__ __forceinline__ void turn(const unsigned char* row, const Chunks& k, const Rope& r, const float* cs, const float* sn,
+                                     float (&x)[2][8]) {
     if (VEC && !r.adjacent) {
         const int l = k.c0 * 4;
 #pragma unroll
@@ -171,12 +202,14 @@ __device__ __forceinline__ void store_entry(const float (&x)[2][8], const Chunks
 }
 
 // `tb` tokens to a CTA. Their sequences, entries and positions are looked up by a lane each; sines and cosines are made
-// once for a token by all threads; then 2^lanes_log threads at a time take a head of a token, its keys and values or its
-// queries. n.k null: rows without a cache, at q.x.
+// once for a token by all threads; then the warps take keys, values and queries, 2^lanes_log threads to a head. What a
+// warp takes first is asked for before the look-ups, and the next before the last is done with. n.k null: rows without a
+// cache, at q.x.
 template <int DT, bool Q8, int ODT, bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ KvView c, const __grid_constant__ KvNew n,
-                                                        const __grid_constant__ Rope r, const __grid_constant__ RopeRows q,
-                                                        const int32_t* parent, int lanes_log, int tb, int64_t ctas) {
+__global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_constant__ KvView c, const __grid_constant__ KvNew n,
+                                                                   const __grid_constant__ Rope r,
+                                                                   const __grid_constant__ RopeRows q, const int32_t* parent,
+                                                                   int lanes_log, int tb, int64_t ctas) {
     __shared__ __align__(16) float cs[kTokens][kPairs], sn[kTokens][kPairs];
     __shared__ Token tok[kTokens];
     __shared__ int32_t pos[kTokens];
@@ -201,70 +234,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     const int64_t first = (int64_t)blockIdx.x * tb;
     const int nt = (int)min((int64_t)tb, n.rows - first);
-    // a thread's pair, and of how many tokens at a time
-    int wide = 5;  // log2 of the threads to a token
-    while ((1 << wide) < r.half) ++wide;
-    const int pair = threadIdx.x & ((1 << wide) - 1);
-    const float freq = pair < r.half ? r.inv_freq[pair] : 0.f;
-    if (warp == 0) {
-        int32_t b = 0;
-        if (cache) b = n.row_off ? kv_find(n.row_off, c.B, first) : (int32_t)(first / n.t_max);
-        if (lane < nt) {
-            const int64_t row = first + lane;
-            Token k;
-            k.at = k.scale = 0;
-            k.known = !cache;
-            k.cached = false;
-            int32_t p = 0;
-            if (cache) {
-                if (n.row_off)
-                    while (b < c.B && n.row_off[b + 1] <= row) ++b;
-                else
-                    b = (int32_t)(row / n.t_max);
-                if (b < c.B) {
-                    const KvSeq s = kv_seq(b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
-                    if (s.st == kKvOk && row >= s.lo) {
-                        const int32_t t = (int32_t)(row - s.lo), at = s.L - s.T + t;
-                        p = at;
-                        k.known = true;
-                        if (parent) {  // its depth
-                            p = s.L - s.T;
-                            int32_t v = t;
-                            while (v > 0) {
-                                const int32_t u = parent[s.lo + v];
-                                if (u < 0 || u >= v) break;
-                                v = u;
-                                ++p;
-                            }
-                            k.known = v == 0 && parent[s.lo] == -1;
-                        }
-                        const int32_t j = c.by_bs.of(at), sl = at - j * c.bs;
-                        const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
-                        k.cached = k.known && pg >= 0 && pg < c.num_blocks;
-                        k.at = pg * c.block_bytes + sl * c.token_bytes;
-                        k.scale = (int64_t)pg * c.H * c.bs + sl;
-                    }
-                }
-            }
-            tok[lane] = k;
-            pos[lane] = p;
-        }
-    }
-    const uint64_t turn = turns_of(freq);
-    const bool sound = fabsf(freq) <= 0x1p20f;
-    __syncthreads();
-    if (pair < r.half) {
-        const int axis = r.one_axis ? 0 : r.axis_of(pair), to = place_of(pair, r.adjacent);
-        for (int t = threadIdx.x >> wide; t < nt; t += kThreads >> wide) {
-            const int32_t p = r.positions ? r.positions[axis * r.rows + first + t] : pos[t];
-            const float2 y = cos_sin((uint64_t)(int64_t)p * turn);
-            cs[t][to] = sound ? y.x * r.factor : __uint_as_float(0x7FC00000u);
-            sn[t][to] = sound ? y.y * r.factor : __uint_as_float(0x7FC00000u);
-        }
-    }
-    __syncthreads();
 
-    const int lanes = 1 << lanes_log, l = lane & (lanes - 1), groups = 32 >> lanes_log, sub = lane >> lanes_log;
+    // this thread's part of a head
+    const int lanes = 1 << lanes_log, l = lane & (lanes - 1), groups_log = 5 - lanes_log, sub = lane >> lanes_log;
     Chunks k;
     const int D = cache ? c.D : q.D;
     if (VEC) {
@@ -279,40 +251,104 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     k.has0 = k.c0 * 8 < D;
     k.has1 = k.c1 * 8 < D;
-    Chunks still = k;
-    still.turns = false;
-    constexpr int isz = DT == kKvBf16 ? 2 : 4;
-    const int entries = cache ? nt * c.H : 0;
-    for (int e0 = warp * groups; e0 < entries; e0 += kWarps * groups) {
-        const int e = e0 + sub, t = min(c.by_H.of(e), nt - 1), h = e - t * c.H;
-        const bool live = e < entries && tok[t].cached;
-        Chunks a = k, b = still;
-        a.has0 = b.has0 = a.has0 && live;
-        a.has1 = b.has1 = a.has1 && live;
-        a.turns = a.turns && live;
-        const int64_t src = (first + t) * n.row_bytes + (int64_t)h * D * isz;
-        const int64_t at = tok[t].at + h * c.head_bytes, sc = tok[t].scale + (int64_t)h * c.bs;
-        float x[2][8], y[2][8];
-        turned<DT, VEC>(n.k + src, a, r, cs[t], sn[t], x);
-        turned<DT, VEC>(n.v + src, b, r, cs[t], sn[t], y);
-        store_entry<Q8>(x, a, live, c.k + at, Q8 ? c.ks + sc : nullptr, l == 0, lanes);
-        store_entry<Q8>(y, b, live, c.v + at, Q8 ? c.vs + sc : nullptr, l == 0, lanes);
+    // the CTA's heads, 2^groups_log to a warp at a time: [0, u_v) keys, [u_v, u_q) values, [u_q, u_end) queries
+    constexpr int isz = DT == kKvBf16 ? 2 : 4, osz = ODT == kKvBf16 ? 2 : 4;
+    const int entries = cache ? nt * c.H : 0, heads = nt * q.heads, more = (1 << groups_log) - 1;
+    const int u_v = (entries + more) >> groups_log, u_q = 2 * u_v, u_end = u_q + ((heads + more) >> groups_log);
+    int t = 0, h = 0;
+    bool live = false;
+    Raw<DT> raw;
+    const unsigned char* row = nullptr;
+    auto ask = [&](int u) {
+        const bool query = u >= u_q;
+        const int e = ((u - (query ? u_q : u >= u_v ? u_v : 0)) << groups_log) + sub;
+        live = e < (query ? heads : entries);
+        t = live ? (query ? r.by_heads.of(e) : c.by_H.of(e)) : 0;
+        h = e - t * (query ? q.heads : c.H);
+        row = (query ? q.x : u >= u_v ? n.v : n.k) + (first + t) * (query ? q.x_row_bytes : n.row_bytes) + (int64_t)h * D * isz;
+        raw.load(row, k, live);
+    };
+    if (warp < u_end) ask(warp);
+
+    // a thread's pair, and of how many tokens at a time
+    int wide = 5;  // log2 of the threads to a token
+    while ((1 << wide) < r.half) ++wide;
+    const int pair = threadIdx.x & ((1 << wide) - 1);
+    const float freq = pair < r.half ? r.inv_freq[pair] : 0.f;
+    if (cache) {
+        if (warp == 0) {
+            int32_t b = n.row_off ? kv_find(n.row_off, c.B, first) : (int32_t)(first / n.t_max);
+            if (lane < nt) {
+                const int64_t at_row = first + lane;
+                Token k;
+                k.at = k.scale = 0;
+                k.known = k.cached = false;
+                int32_t p = 0;
+                if (n.row_off)
+                    while (b < c.B && n.row_off[b + 1] <= at_row) ++b;
+                else
+                    b = (int32_t)(at_row / n.t_max);
+                if (b < c.B) {
+                    const KvSeq s = kv_seq(b, n.row_off, n.t_max, n.rows, n.kv_lens, c.bs, c.max_blocks, false);
+                    if (s.st == kKvOk && at_row >= s.lo) {
+                        const int32_t t = (int32_t)(at_row - s.lo), at = s.L - s.T + t;
+                        const int32_t j = c.by_bs.of(at), sl = at - j * c.bs;
+                        const int32_t pg = c.table[(int64_t)b * c.max_blocks + j];
+                        p = at;
+                        k.known = true;
+                        if (parent) {  // its depth
+                            p = s.L - s.T;
+                            int32_t v = t;
+                            while (v > 0) {
+                                const int32_t u = parent[s.lo + v];
+                                if (u < 0 || u >= v) break;
+                                v = u;
+                                ++p;
+                            }
+                            k.known = v == 0 && parent[s.lo] == -1;
+                        }
+                        k.cached = k.known && pg >= 0 && pg < c.num_blocks;
+                        k.at = pg * c.block_bytes + sl * c.token_bytes;
+                        k.scale = (int64_t)pg * c.H * c.bs + sl;
+                    }
+                }
+                tok[lane] = k;
+                pos[lane] = p;
+            }
+        }
+        __syncthreads();
     }
-    const int heads = nt * q.heads;
-    const int turn_of_warp = (warp + kWarps - (entries + groups - 1) / groups % kWarps) % kWarps;  // warps without entries first
-    for (int e0 = turn_of_warp * groups; e0 < heads; e0 += kWarps * groups) {
-        const int e = e0 + sub, t = min(r.by_heads.of(e), nt - 1), h = e - t * q.heads;
-        const bool live = e < heads && tok[t].known;
-        Chunks a = k;
-        a.has0 = a.has0 && live;
-        a.has1 = a.has1 && live;
-        a.turns = a.turns && live;
+    if (pair < r.half) {
+        const uint64_t turn_of = turns_of(freq);
+        const bool sound = fabsf(freq) <= 0x1p20f;
+        const int axis = r.one_axis ? 0 : r.axis_of(pair), to = place_of(pair, r.adjacent);
+        for (int i = threadIdx.x >> wide; i < nt; i += kThreads >> wide) {
+            const int32_t p = r.positions ? r.positions[axis * r.rows + first + i] : pos[i];
+            const float2 y = cos_sin((uint64_t)(int64_t)p * turn_of);
+            cs[i][to] = sound ? y.x * r.factor : __uint_as_float(0x7FC00000u);
+            sn[i][to] = sound ? y.y * r.factor : __uint_as_float(0x7FC00000u);
+        }
+    }
+    __syncthreads();
+
+    for (int u = warp; u < u_end; u += kWarps) {
+        const int now_t = t, now_h = h;
+        const unsigned char* const now_row = row;
+        const bool query = u >= u_q, key = u < u_v;
+        const bool now_live = live && (!cache || (query ? tok[t].known : tok[t].cached));
         float x[2][8];
-        turned<DT, VEC>(q.x + (first + t) * q.x_row_bytes + (int64_t)h * D * isz, a, r, cs[t], sn[t], x);
-        if (!VEC) __syncwarp();  // in place: a head's elements are all read before one is written
-        unsigned char* const out = q.out + (first + t) * q.out_row_bytes + (int64_t)h * D * (ODT == kKvBf16 ? 2 : 4);
-        if (a.has0) store8<ODT>(out, k.c0, x[0]);
-        if (a.has1) store8<ODT>(out, k.c1, x[1]);
+        raw.floats(x);
+        if (u + kWarps < u_end) ask(u + kWarps);
+        if ((key || query) && k.turns && now_live) turn<DT, VEC>(now_row, k, r, cs[now_t], sn[now_t], x);
+        if (query) {
+            if (!VEC) __syncwarp();  // in place: a head's elements are all read before one is written
+            unsigned char* const out = q.out + (first + now_t) * q.out_row_bytes + (int64_t)now_h * D * osz;
+            if (now_live && k.has0) store8<ODT>(out, k.c0, x[0]);
+            if (now_live && k.has1) store8<ODT>(out, k.c1, x[1]);
+        } else {
+            const int64_t at = tok[now_t].at + now_h * c.head_bytes, sc = tok[now_t].scale + (int64_t)now_h * c.bs;
+            store_entry<Q8>(x, k, now_live, (key ? c.k : c.v) + at, Q8 ? (key ? c.ks : c.vs) + sc : nullptr, l == 0, lanes);
+        }
     }
 }
 
@@ -321,8 +357,9 @@ cudaError_t launch(const KvView& c, const KvNew& n, const Rope& r, const RopeRow
     const int D = n.k ? c.D : q.D;
     int lanes_log = 0;
     while ((16 << lanes_log) < D) ++lanes_log;  // D <= 256: at most 16 lanes
-    const int tb = (int)std::min<int64_t>(kTokens, std::max<int64_t>(1, n.rows / 2048));
-    const int64_t ctas = (n.rows + tb - 1) / tb;
+    const int64_t slots = 152 * kResident;  // few tokens, one to a CTA; then as many as make one wave (trees of 64: 16 to 11 us)
+    const int tb = (int)std::min<int64_t>(kTokens, (n.rows + slots - 1) / slots);
+    const int64_t ctas = tb ? (n.rows + tb - 1) / tb : 0;
     const int64_t grid = ctas + (n.seq_status ? (c.B + kWarps - 1) / kWarps : 0);
     if (grid == 0) return cudaSuccess;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
