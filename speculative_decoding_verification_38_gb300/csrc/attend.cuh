@@ -1387,35 +1387,35 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                     static_assert(MC * 8 <= 8 * (int)sizeof(Rows), "a bit for each row of the group");
                     Rows vis = in ? ~(Rows)0 : (Rows)0;
                     const int32_t far = Win && tail && in ? reach(pos) : kKvMaxQueries;
-                    if (tail && in && (pos >= ctx || (Win && far < T - 1))) {
+                    if (T > 1 && tail && in && (pos >= ctx || (Win && far < T - 1))) {
                         const int32_t u = pos - ctx;
                         vis = 0;
-#pragma unroll 1
-                        for (int m = 0; m < live; ++m) {
-                            const int32_t r = row0 + (sub + X::GT * m) * 8, tk = a.by_G.of(r), w = tk >> 5;
-                            int32_t left = (tk + 1) * a.G - r;  // rows of token tk from here
-                            uint32_t see;                       // tokens tk, tk + 1, ..
-                            if (Win && u < 0)
-                                see = ~0u;
-                            else if (a.parent)
-                                see = __funnelshift_r(w < 4 ? seen_by[u * 4 + w] : 0, w < 3 ? seen_by[u * 4 + w + 1] : 0, tk & 31);
-                            else
-                                see = tk >= u ? ~0u : u - tk >= 8 ? 0u : ~0u << (u - tk);
-                            if (Win && far < T - 1) {  // not past the window
-                                if (!a.parent)
-                                    see &= far < tk ? 0u : far - tk >= 8 ? ~0u : (2u << (far - tk)) - 1;
-                                else
-#pragma unroll 1
-                                    for (int k = 0; k < 8; ++k)
-                                        if (depth[min(tk + k, kKvMaxQueries - 1)] > far) see &= ~(1u << k);
-                            }
-                            uint32_t bits = 0;
+                        if (!a.parent) {
+                            // tokens u to `far`: rows that lie together
+                            const int32_t from = max(u, 0) * a.G - row0, to = Win ? (min(far, T) + 1) * a.G - row0 : INT32_MAX;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                bits |= (see & 1) << k;
-                                if (--left == 0) left = a.G, see >>= 1;
+                            for (int m = 0; m < MC; ++m) {
+                                const int32_t r = (sub + X::GT * m) * 8;
+                                vis |= (Rows)(0xFFu << min(max(from - r, 0), 8) & 0xFFu >> (8 - min(max(to - r, 0), 8))) << (m * 8);
                             }
-                            vis |= (Rows)bits << (m * 8);
+                        } else {
+#pragma unroll 1
+                            for (int m = 0; m < live; ++m) {
+                                const int32_t r = row0 + (sub + X::GT * m) * 8, w = a.by_G.of(r) >> 5;
+                                int32_t tk = a.by_G.of(r), left = (tk + 1) * a.G - r;  // rows of token tk from here
+                                uint32_t see = ~0u;                                    // tokens tk, tk + 1, ..
+                                if (!Win || u >= 0)
+                                    see = __funnelshift_r(w < 4 ? seen_by[u * 4 + w] : 0, w < 3 ? seen_by[u * 4 + w + 1] : 0, tk & 31);
+                                uint32_t bits = 0;
+#pragma unroll 1
+                                for (int k = 0; k < 8; ++tk, see >>= 1) {
+                                    if ((see & 1) && (!Win || depth[min(tk, kKvMaxQueries - 1)] <= far))
+                                        bits |= 0xFFu >> max(0, 8 - left) << k;
+                                    k += left;
+                                    left = a.G;
+                                }
+                                vis |= (Rows)(bits & 0xFFu) << (m * 8);
+                            }
                         }
                     }
                     const bool masked = tail || __any_sync(0xFFFFFFFFu, !in);
@@ -1636,7 +1636,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                         bool found = false;
 #pragma unroll 1
                         for (int k = 0; k < DP / 8; ++k) {
-                            uint4* const at = (uint4*)(v_row + (k >> 3) * (kTileTok * 128) + (k & 7) * 16);
+                            // (a thread's units in an order of its own, so that neighbours' rows meet no bank twice)
+                            uint4* const at = (uint4*)(v_row + (k >> 3) * (kTileTok * 128) + ((k ^ wt) & 7) * 16);
                             if (clear) {
                                 *at = make_uint4(0, 0, 0, 0);
                                 continue;
