@@ -185,6 +185,13 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool x) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {  // bytes 0: a zero
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// An arrival once this thread's copies so far have landed (one of the barrier's count).
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // A box of the cache (elements, slots, head, page) into shared memory; past the pool or head_dim: zeros.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t e, int32_t slot, int32_t head,
@@ -327,18 +334,22 @@ struct Shape {
                                      (tight ? 0 : kGroups * red_bytes) + kKvMaxQueries * 16 + (Win ? 16 + (tight ? 0 : kKvMaxQueries) : 0) + segs * sizeof(Seg) +
                                      (tight ? 40 : 48) +
                                      (tight ? 8 : 4 * kMaxSlots + (Q8 ? 2 * RV : 0)) * 8 +
-                                     (2 * SB + 2 * PS + 5 + aux_ring + 2 * segs) * 8;
+                                     (2 * SB + 2 * PS + 5 + (Q8 ? 2 : 1) * aux_ring + 2 * segs) * 8;
     static constexpr int room = (int)(kSmemMax - raw_bytes - QB * q_bytes - PS * p_bytes - misc), fit = room / slot_bytes;
     // tiles of the K ring and of the V ring; a V tile is held longer
-    static constexpr int SK = Q8 ? (room - 3 * (int)k_bytes) / (int)slot_bytes >= 2 ? 3 : 2 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
+    static constexpr int SK = Q8 ? (room - 4 * (int)k_bytes) / (int)slot_bytes >= 2   ? 4
+                                   : (room - 3 * (int)k_bytes) / (int)slot_bytes >= 2 ? 3
+                                                                                      : 2
+                                 : fit / 2 > kMaxSlots ? kMaxSlots : fit / 2;
     static constexpr int rest = Q8 ? (room - SK * (int)k_bytes) / (int)slot_bytes : fit - SK;
     static constexpr int SV = rest > kMaxSlots ? kMaxSlots : rest;
     static constexpr uint32_t ring_bytes = SK * k_bytes + SV * slot_bytes;
     static constexpr uint32_t total = ring_bytes + raw_bytes + QB * q_bytes + PS * p_bytes + misc;
     static_assert(SK >= 2 && SV >= 2, "a ring needs two tiles");
     static_assert(2 * (SK + SV) <= (tight ? 8 : 4 * kMaxSlots) && total <= kSmemMax && columns <= 512, "memory");
-    // a tile's masks and scales are written while those of the last SK + SB tiles may be in use
-    static_assert(aux_ring > SK + SB, "aux ring");
+    // bf16: a tile's masks are written while those of the last SK + SB tiles may be in use. e4m3: a place of the ring is given
+    // back; that its arrivals keep to its turns takes the teams in order
+    static_assert(Q8 ? aux_ring > SB && aux_ring % TM == 0 && SB % TM == 0 : aux_ring > SK + SB, "aux ring");
 };
 
 // The flat list of tiles. An entry counts kOver more than its tiles, at its front, for what opening and closing it
@@ -621,7 +632,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
     uint64_t* const q_full = drain + 1;
     uint64_t* const q_empty = q_full + 2;
     uint64_t* const aux_full = q_empty + 2;
-    uint64_t* const seg_full = aux_full + kAuxRing;
+    uint64_t* const aux_empty = aux_full + kAuxRing;  // Q8
+    uint64_t* const seg_full = aux_empty + (Q8 ? kAuxRing : 0);
     uint64_t* const seg_empty = seg_full + R;
     uint64_t* const raw_full = seg_empty + R;       // Q8: [RV]
     uint64_t* const raw_empty = raw_full + RV;
@@ -675,7 +687,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
     if (tid == 0) {
         for (uint32_t i = 0; i < SK; ++i) {
             mbar_init(k_full + i, 1);
-            mbar_init(k_empty + i, Q8 ? 5 : 1);
+            mbar_init(k_empty + i, 1);
         }
         for (uint32_t i = 0; i < SV; ++i) {
             mbar_init(v_full + i, Q8 ? 4 : 1);
@@ -699,7 +711,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
             mbar_init(q_empty + i, 1);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < kAuxRing; ++i) mbar_init(aux_full + i, Q8 ? 4 : 1);
+        for (int i = 0; i < kAuxRing; ++i) {
+            mbar_init(aux_full + i, Q8 ? 4 * 32 + 4 : 1);  // e4m3: each thread's copies, and each warp's bits
+            if (Q8) mbar_init(aux_empty + i, 4 * X::GT);
+        }
         for (int i = 0; i < R; ++i) {
             mbar_init(seg_full + i, 1);
             mbar_init(seg_empty + i, kSoftWarps + (Q8 ? 2 + 8 : 3));
@@ -833,23 +848,9 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                 const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
                 const unsigned char* const q0 = a.q + g->lo * a.q_row_bytes + (int64_t)h * a.G * c.D * 2 + piece * 16;
                 done_seg(si);
-                int32_t pg = pos < L ? table[c.by_bs.of(pos)] : -1;
-                float sk = 0.f, sv = 0.f;
-                bool in = false;
-                // scales of the row at pos, its page known; on to the next tile's page
-                auto scales = [&]() {
-                    in = pg >= 0 && pg < c.num_blocks && (!Win || sight.seen(pos, L, a.sinks));
-                    sk = sv = 0.f;
-                    if (in) {
-                        const int64_t i = ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs);
-                        sk = c.ks[i];
-                        sv = c.vs[i];
-                    }
-                    place += kTileTok;
-                    pos = position(sight, place);
-                    pg = pos < L ? table[c.by_bs.of(pos)] : -1;
-                };
-                scales();
+                // pages of this lane's position in this tile and in the next two
+                auto page_at = [&](int32_t pos) { return pos < L ? table[c.by_bs.of(pos)] : -1; };
+                int32_t pos1 = position(sight, place + kTileTok), pg = page_at(pos), pg1 = page_at(pos1);
                 const uint32_t q_at = smem_addr(q_sm) + (si % QB) * X::q_bytes + (piece & 1) * 8;
                 float* const arow = arow_all + (si % R) * N;
                 auto load_q = [&](int r) {
@@ -907,24 +908,35 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                 fence_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full + si % QB);
+                // A tile's scales go to its place by copies of their own, as far ahead as the ring has places. (Through
+                // registers, a tile at a time behind its K tile, they took the loads' latency for each tile: one token of 64
+                // sequences through a window of 1,024, 77 to 73 us.)
 #pragma unroll 1
                 for (int t = 0; t < n; ++t, ++kt) {
-                    const uint32_t slot = kt % SK;
-                    // in step with the K ring, so that the scales' is not overrun
-                    if (!wait(k_full + slot, (kt / SK) & 1)) dead = true;
+                    const uint32_t at = kt % kAuxRing;
+                    const int32_t pos2 = position(sight, place + 2 * kTileTok), pg2 = page_at(pos2);
+                    if (kt >= kAuxRing && !wait(aux_empty + at, (kt / kAuxRing - 1) & 1)) dead = true;
                     unsigned char* const aux = aux_of(kt);
+                    const bool in = pg >= 0 && pg < c.num_blocks && (!Win || sight.seen(pos, L, a.sinks));
                     const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
                     if (lane == 0) ((uint32_t*)aux)[fw] = bits;
-                    ((float*)(aux + 16))[fw * 32 + lane] = sk;
-                    ((float*)(aux + 16))[kTileTok + fw * 32 + lane] = sv;
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (!dead) mbar_arrive(k_empty + slot);
-                        mbar_arrive(aux_full + kt % kAuxRing);
+                    if (!__any_sync(0xFFFFFFFFu, dead)) {
+                        const int64_t i = in ? ((int64_t)pg * c.H + h) * c.bs + (pos - c.by_bs.of(pos) * c.bs) : 0;
+                        const uint32_t to = smem_addr(aux + 16) + (fw * 32 + lane) * 4;
+                        cp4(to, c.ks + i, in ? 4u : 0u);
+                        cp4(to + kTileTok * 4, c.vs + i, in ? 4u : 0u);
+                        cp_arrive(aux_full + at);
+                    } else {
+                        mbar_arrive(aux_full + at);
                     }
-                    if (t + 1 < n) scales();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(aux_full + at);
+                    place += kTileTok;
+                    pos = pos1, pos1 = pos2;
+                    pg = pg1, pg1 = pg2;
                 }
             }
+            cp_wait_all();  // (a copy under way must not outlive the CTA)
         } else {
             // ======================================================== e4m3: V to f16
             // Exactly, 32 rows to a warp, from a tile as it is to the V ring.
@@ -1253,7 +1265,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
-        constexpr float grow = Q8 ? 8.f : 16.f;
+        constexpr float grow = Q8 ? (Win ? 9.75f : 8.f) : 16.f;
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t team = gr % TM, sub = gr / TM;
         const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;
@@ -1617,7 +1629,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                             continue;
                         }
                         // (after a move nothing passes the reference, so that a second one is never due)
-                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || !(big <= 16384.f))) break;
+                        if (i == first || moved || !bar_or(bar_gr, 128, top > grow || !(big <= (Win ? 61440.f : 16384.f)))) break;
                         sign = -1.f;
                     }
                     // (Win: a box's slots that no token sees are cleared too)
@@ -1669,6 +1681,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                         if (turn) wait(pv_done + ps, (turn - 1) & 1);
                     }
                     mbar_arrive(s_empty + buf);
+                    if (Q8) mbar_arrive(aux_empty + t % kAuxRing);
                     mbar_arrive(p_full + ps);
                 }
             }
