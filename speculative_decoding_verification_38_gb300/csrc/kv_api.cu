@@ -220,6 +220,10 @@ spec_status_t attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, i
     p.seq_status = a->seq_status;
     p.window = (int32_t)std::min<int64_t>(window, kMaxPositions);  // (so that sums with positions stay in range)
     p.sinks = (int32_t)std::min<int64_t>(sinks, kMaxPositions);
+    if (window && attend_few_takes(c->head_dim, (int64_t)a->t_max * p.G)) {
+        if ((int64_t)c->batch * c->kv_heads > kMaxEntries) return SPEC_ERR_UNSUPPORTED;  // a CTA for each
+        return launched(launch_attend_few(p, a->workspace, (cudaStream_t)stream));
+    }
     return launched(attend_takes(c->head_dim) ? launch_attend(p, a->workspace, (cudaStream_t)stream)
                                               : launch_kv_attend_plain(p, (cudaStream_t)stream));
 }
@@ -292,7 +296,10 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* c, const int64_t* 
 
 SPEC_API size_t spec_kv_attend_workspace_size(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a) {
     if (check_attend_shape(c, a) != SPEC_OK) return 0;
-    return attend_takes(c->head_dim) ? attend_workspace((int64_t)a->t_max * (a->q_heads / c->kv_heads)) : kHeaderBytes;
+    const int64_t rows = (int64_t)a->t_max * (a->q_heads / c->kv_heads);
+    if (!attend_takes(c->head_dim)) return kHeaderBytes;
+    // (one size, whether the call has a window or not)
+    return attend_few_takes(c->head_dim, rows) ? std::max(attend_workspace(rows), attend_few_workspace(rows)) : attend_workspace(rows);
 }
 
 SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, spec_stream_t stream) {
