@@ -36,11 +36,9 @@ struct FewParams {
     uint32_t* arrive;   // [entry] pieces done, zero between calls
 };
 
-constexpr int kWarps = 4;
-constexpr int kRun = 16;          // positions of a run
+constexpr int kMaxWarps = 8;
 constexpr int kBoxLog = 4;        // log2 of the most positions that the list keeps together
-constexpr int64_t kWaves = 4;     // of CTAs, where entries are split for them
-constexpr int64_t kLeast = 4;     // runs of a warp, at least
+constexpr int64_t kLeast = 32;    // positions of a warp, at least
 constexpr int64_t kParts = 2048;  // most pieces where entries are split
 constexpr float kNone = -INFINITY;
 
@@ -84,15 +82,23 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // a in the lo
     return r;
 }
 
+// Two codes each, the low and the high half of a word, exact as f16.
+__device__ __forceinline__ void codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 template <int NR, int DP, bool Q8>
 struct Few {
+    static constexpr int run = Q8 || DP <= 64 ? 32 : 16;            // positions of a run
     static constexpr int sets = NR / 8;                             // rows 8 at a time
     static constexpr uint32_t row = Q8 ? (DP <= 64 ? 64 : 128) : DP * 2;  // bytes of a position in shared memory
-    static constexpr uint32_t half = kRun * row;                    // K, or V, of a run
-    static constexpr uint32_t stage = 2 * half + (Q8 ? 256 : 128);  // and (e4m3) their scales [2][kRun], which positions are there
-    static constexpr int stages = Q8 ? 4 : DP <= 64 ? 4 : 2;
+    static constexpr uint32_t half = run * row;                     // K, or V, of a run
+    static constexpr uint32_t stage = 2 * half + (Q8 ? 384 : 128);  // and (e4m3) their scales [2][run], which positions are there
+    static constexpr int stages = 3;
     static constexpr uint32_t warp_bytes = stages * stage > NR * DP * 4 ? stages * stage : NR * DP * 4;  // and its outputs at the end
-    static constexpr uint32_t total = kWarps * (warp_bytes + NR * 16);
+    static constexpr uint32_t per_warp = warp_bytes + NR * 16;
     // where a 16-byte unit of a position lies: eight positions' same unit in different banks
     static __device__ __forceinline__ uint32_t at(uint32_t pos, uint32_t unit) {
         return pos * row + (unit ^ (row == 64 ? pos >> 1 & 3 : pos & 7)) * 16;
@@ -100,16 +106,16 @@ struct Few {
 };
 
 template <int NR, int DP, bool Q8>
-__global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) attend_few_kernel(const __grid_constant__ FewParams p) {
     using X = Few<NR, DP, Q8>;
-    constexpr int sets = X::sets;
+    constexpr int sets = X::sets, kRun = X::run, NT = kRun / 8;
     extern __shared__ __align__(128) unsigned char smem[];
     const KvAttend& a = p.a;
     const KvView& c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     if ((int64_t)blockIdx.x >= p.ctas) {
         // ------------------------------------------------------ statuses, a warp for each sequence
-        const int64_t b = ((int64_t)blockIdx.x - p.ctas) * kWarps + warp;
+        const int64_t b = ((int64_t)blockIdx.x - p.ctas) * warps + warp;
         if (b >= c.B) return;
         const KvSeq s = kv_seq((int32_t)b, a.row_off, a.t_max, a.rows, a.kv_lens, c.bs, c.max_blocks, true);
         int32_t st = s.st;
@@ -210,8 +216,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     constexpr int chunks = X::row / 16, per = 32 / chunks;  // 16-byte units of a position; positions of one copy instruction
     const int chunk = lane % chunks, sub = lane / chunks;
     const bool inside = chunk * 16 < c.D * c.esz;
-    // lane i (and i + 16): position i of a run, its page
-    auto pos_of = [&](int32_t run) { return sight.at(run * kRun + (lane & 15)); };
+    // lane i (and, of 16, i + 16): position i of a run, its page
+    auto pos_of = [&](int32_t run) { return sight.at(run * kRun + (lane & (kRun - 1))); };
     auto page_of = [&](int32_t run, int32_t pos) {
         return run < run1 && sight.seen(pos, L, a.sinks) ? table[c.by_bs.of(pos)] : -1;
     };
@@ -230,11 +236,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
             cp16(dst, c.k + off, on);
             cp16(dst + X::half, c.v + off, on);
         }
-        if (Q8) {  // lanes 0 .. 15: K's scales, 16 .. 31: V's
+        if (Q8) {
             const int64_t i = there ? ((int64_t)pg * c.H + h) * c.bs + sl : 0;
-            cp4(to + 2 * X::half + lane * 4, (lane < 16 ? c.ks : c.vs) + i, there);
+            cp4(to + 2 * X::half + lane * 4, c.ks + i, there);
+            cp4(to + 2 * X::half + 128 + lane * 4, c.vs + i, there);
         }
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, there) & 0xFFFFu;
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, there);
         if (lane == 0) *(uint32_t*)(ring + st * X::stage + X::stage - 16) = bits;
     };
 
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     auto fetch = [&](int st) {
         const int32_t pos = next_pos, pg = next_pg;
         const bool any = next < run1;
-        next += kWarps;
+        next += warps;
         next_pos = pos_of(next);
         next_pg = page_of(next, next_pos);
         if (any) load(pos, pg, st);
@@ -269,39 +276,44 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
         const float* const scales = (const float*)(ring + st * X::stage + 2 * X::half);
         const uint32_t live = *(const uint32_t*)(ring + st * X::stage + X::stage - 16);
         const int32_t place0 = run * kRun;
-        const bool masked = live != 0xFFFFu || (T > 1 && place0 + kRun > sight.tail);
+        constexpr uint32_t every = kRun == 32 ? ~0u : (1u << (kRun & 31)) - 1;
+        const bool masked = (live & every) != every || (T > 1 && place0 + kRun > sight.tail);
         // ---- scores: rows lane / 4 (+ 8), positions 8n + 2j, + 1
-        float x[2][4] = {};
+        float x[NT][4] = {};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int k = 0; k < DP / 16; k += Q8 ? 4 : 2)
 #pragma unroll
-            for (int k = 0; k < DP / 16; k += Q8 ? 4 : 2) {
+            for (int n = 0; n < NT; ++n) {
                 uint32_t w[4];  // 8 positions by 4 units of 16 bytes
-                const int unit_of = Q8 ? k + (lane >> 3) : 2 * k + (lane >> 3);
-                ldsm(k_at + X::at(n * 8 + (lane & 7), unit_of), w);
+                ldsm(k_at + X::at(n * 8 + (lane & 7), (Q8 ? k : 2 * k) + (lane >> 3)), w);
 #pragma unroll
                 for (int i = 0; i < (Q8 ? 4 : 2); ++i) {
-                    const uint32_t b0 = Q8 ? e4m3_f16x2(w[i] & 0xFFFF) : w[2 * i], b1 = Q8 ? e4m3_f16x2(w[i] >> 16) : w[(2 * i + 1) & 3];
+                    uint32_t b0 = w[(2 * i) & 3], b1 = w[(2 * i + 1) & 3];
+                    if (Q8) codes(w[i], b0, b1);
                     mma<Q8>(x[n], q[k + i][0], sets > 1 ? q[k + i][sets > 1 ? 2 : 0] : 0u, q[k + i][1],
                             sets > 1 ? q[k + i][sets > 1 ? 3 : 1] : 0u, b0, b1);
                 }
             }
-        float vs[2][2];
+        float2 vs[NT];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float ks = Q8 ? scales[n * 8 + 2 * j + i] : 1.f;
-                vs[n][i] = Q8 ? scales[16 + n * 8 + 2 * j + i] : 1.f;
-#pragma unroll
-                for (int t = 0; t < sets; ++t) x[n][2 * t + i] *= Q8 ? arow[t] * ks : k2;
+        for (int n = 0; n < NT; ++n) {
+            float2 ks = make_float2(1.f, 1.f);
+            if (Q8) {
+                ks = *(const float2*)(scales + n * 8 + 2 * j);
+                vs[n] = *(const float2*)(scales + 32 + n * 8 + 2 * j);
             }
-        uint32_t vis[sets];  // of the row's 16 positions, this lane's four: bit 8n + 2j + i
+#pragma unroll
+            for (int t = 0; t < sets; ++t) {
+                x[n][2 * t] *= Q8 ? arow[t] * ks.x : k2;
+                x[n][2 * t + 1] *= Q8 ? arow[t] * ks.y : k2;
+            }
+        }
+        uint32_t vis[sets];  // of the row's positions, this lane's: bit 8n + 2j + i
         if (masked) {
 #pragma unroll
             for (int t = 0; t < sets; ++t) vis[t] = 0;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int at = n * 8 + 2 * j + i;
@@ -321,7 +333,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
         bool change = false;
 #pragma unroll
         for (int t = 0; t < sets; ++t) {
-            float top = fmaxf(fmaxf(x[0][2 * t], x[0][2 * t + 1]), fmaxf(x[1][2 * t], x[1][2 * t + 1]));
+            float top = kNone;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) top = max3(top, x[n][2 * t], x[n][2 * t + 1]);
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             const float mn = fmaxf(m[t], top);
@@ -330,18 +344,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
             m[t] = mn;
             fo[t] = f[t];
             if (Q8) {
-                // of the smallest power of two not below a scale, as it is held, 0 to 253 (no scale, 2^126 or more)
-                uint32_t e = 0;
+                // the largest scale's magnitude, as an integer; of the smallest power of two not below it the exponent as it
+                // is held, 0 to 253 (no scale, 2^126 or more)
+                uint32_t w = 0;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w = __float_as_uint(fabsf(vs[n][i]));
-                        const uint32_t y = min(253u, (w >> 23) + ((w & 0x7FFFFFu) ? 1u : 0u));
-                        e = max(e, !masked || (vis[t] >> (n * 8 + 2 * j + i) & 1) ? y : 0u);
-                    }
-                e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
-                e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t lo = __float_as_uint(vs[n].x) & 0x7FFFFFFFu, hi = __float_as_uint(vs[n].y) & 0x7FFFFFFFu;
+                    w = max(w, !masked || (vis[t] >> (n * 8 + 2 * j) & 1) ? lo : 0u);
+                    w = max(w, !masked || (vis[t] >> (n * 8 + 2 * j + 1) & 1) ? hi : 0u);
+                }
+                w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
+                w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+                const uint32_t e = min(253u, (w + 0x7FFFFFu) >> 23);
                 // the unit is 2^(15 - e), held as 127 + 15 - (e - 127)
                 const uint32_t was = 269 - (__float_as_uint(unit[t]) >> 23), now = max(was, max(e, 16u));
                 unit[t] = __uint_as_float((269 - now) << 23);
@@ -363,19 +377,19 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
             }
         }
         // ---- weights: the second product's operand as they lie
-        uint32_t w0[sets][2], w1[sets][2];  // bf16: two parts, 16 bits of a weight; e4m3: f16, times V's scale and the unit
+        uint32_t w0[sets][NT], w1[sets][NT];  // bf16: two parts, 16 bits of a weight; e4m3: f16, times V's scale and the unit
 #pragma unroll
         for (int t = 0; t < sets; ++t) {
             const float mr = m[t] == kNone ? 0.f : m[t];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < NT; ++n) {
                 float w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     w[i] = ex2(x[n][2 * t + i] - mr);
                     l[t] += w[i];
                     if (Q8) {
-                        w[i] *= vs[n][i] * unit[t];
+                        w[i] *= (i ? vs[n].y : vs[n].x) * unit[t];
                         if (masked) w[i] = vis[t] >> (n * 8 + 2 * j + i) & 1 ? w[i] : 0.f;
                     }
                 }
@@ -390,19 +404,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
         // ---- O^T += V^T P^T
         // V's operands of 16 elements of the head each, `step` at a time: lanes hold pairs of positions of an element
         constexpr int step = Q8 ? 2 : 1;
-        auto values = [&](int k, uint32_t (&v)[step][4]) {
+        auto values = [&](int part, int k, uint32_t (&v)[step][4]) {  // of positions 16 part ..
             uint32_t w[4];
             if constexpr (Q8) {
                 // pairs of codes, of positions 0 .. 7 and 8 .. 15, of this 16 elements and the next
-                ldsm_t(v_at + X::at(lane & 15, k + (lane >> 4)), w);
+                ldsm_t(v_at + X::at(16 * part + (lane & 15), k + (lane >> 4)), w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t y = __byte_perm(w[i], 0, 0x3120);  // an element's two positions side by side
-                    v[i >> 1][2 * (i & 1)] = e4m3_f16x2(y & 0xFFFF);
-                    v[i >> 1][2 * (i & 1) + 1] = e4m3_f16x2(y >> 16);
-                }
+                for (int i = 0; i < 4; ++i)  // an element's two positions side by side
+                    codes(__byte_perm(w[i], 0, 0x3120), v[i >> 1][2 * (i & 1)], v[i >> 1][2 * (i & 1) + 1]);
             } else {
-                ldsm_t(v_at + X::at((lane & 7) + (lane & 16 ? 8 : 0), 2 * k + (lane >> 3 & 1)), v[0]);
+                ldsm_t(v_at + X::at(16 * part + (lane & 7) + (lane & 16 ? 8 : 0), 2 * k + (lane >> 3 & 1)), v[0]);
             }
         };
         // A value that is not finite, at a position that some rows see and others do not, would reach those too (0 * inf).
@@ -426,17 +437,20 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
         }
         if (!poison) {
 #pragma unroll
-            for (int k = 0; k < DP / 16; k += step) {
-                uint32_t v[step][4];
-                values(k, v);
+            for (int part = 0; part < NT / 2; ++part)
 #pragma unroll
-                for (int i = 0; i < step; ++i)
+                for (int k = 0; k < DP / 16; k += step) {
+                    uint32_t v[step][4];
+                    values(part, k, v);
 #pragma unroll
-                    for (int t = 0; t < sets; ++t) {
-                        mma<Q8>(o[k + i][t], v[i][0], v[i][1], v[i][2], v[i][3], w0[t][0], w0[t][1]);
-                        if (!Q8) mma<Q8>(o[k + i][t], v[i][0], v[i][1], v[i][2], v[i][3], w1[t][0], w1[t][1]);
-                    }
-            }
+                    for (int i = 0; i < step; ++i)
+#pragma unroll
+                        for (int t = 0; t < sets; ++t) {
+                            mma<Q8>(o[k + i][t], v[i][0], v[i][1], v[i][2], v[i][3], w0[t][2 * part], w0[t][2 * part + 1]);
+                            if (!Q8)
+                                mma<Q8>(o[k + i][t], v[i][0], v[i][1], v[i][2], v[i][3], w1[t][2 * part], w1[t][2 * part + 1]);
+                        }
+                }
         } else {
             // a row at a time, from the values it sees
 #pragma unroll
@@ -447,20 +461,24 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
 #pragma unroll 1
                 for (int r = 0; r < 8; ++r) {
                     const uint32_t on = __shfl_sync(0xFFFFFFFFu, of_row, 4 * r);
-                    auto both = [&](int at) { return (on >> at & 1 ? 0xFFFFu : 0u) | (on >> (at + 1) & 1 ? 0xFFFF0000u : 0u); };
-                    const uint32_t lo = both(2 * j), hi = both(8 + 2 * j);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; k += step) {
-                        uint32_t v[step][4];
-                        values(k, v);
+                    for (int part = 0; part < NT / 2; ++part) {
+                        auto both = [&](int at) { return (on >> at & 1 ? 0xFFFFu : 0u) | (on >> (at + 1) & 1 ? 0xFFFF0000u : 0u); };
+                        const uint32_t lo = both(16 * part + 2 * j), hi = both(16 * part + 8 + 2 * j);
 #pragma unroll
-                        for (int i = 0; i < step; ++i) {
-                            float y[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma<Q8>(y, v[i][0] & lo, v[i][1] & lo, v[i][2] & hi, v[i][3] & hi, w0[t][0], w0[t][1]);
-                            if (!Q8) mma<Q8>(y, v[i][0] & lo, v[i][1] & lo, v[i][2] & hi, v[i][3] & hi, w1[t][0], w1[t][1]);
-                            const bool even = r == 2 * j, odd = r == 2 * j + 1;
-                            if (even) o[k + i][t][0] += y[0], o[k + i][t][2] += y[2];
-                            if (odd) o[k + i][t][1] += y[1], o[k + i][t][3] += y[3];
+                        for (int k = 0; k < DP / 16; k += step) {
+                            uint32_t v[step][4];
+                            values(part, k, v);
+#pragma unroll
+                            for (int i = 0; i < step; ++i) {
+                                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma<Q8>(y, v[i][0] & lo, v[i][1] & lo, v[i][2] & hi, v[i][3] & hi, w0[t][2 * part], w0[t][2 * part + 1]);
+                                if (!Q8)
+                                    mma<Q8>(y, v[i][0] & lo, v[i][1] & lo, v[i][2] & hi, v[i][3] & hi, w1[t][2 * part], w1[t][2 * part + 1]);
+                                const bool even = r == 2 * j, odd = r == 2 * j + 1;
+                                if (even) o[k + i][t][0] += y[0], o[k + i][t][2] += y[2];
+                                if (odd) o[k + i][t][1] += y[1], o[k + i][t][3] += y[3];
+                            }
                         }
                     }
                 }
@@ -470,14 +488,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     };
     int st = 0;
 #pragma unroll 1
-    for (int32_t run = run0 + warp; run < run1; run += kWarps) {
+    for (int32_t run = run0 + warp; run < run1; run += warps) {
         one(run, st);
         st = st + 1 == S ? 0 : st + 1;
     }
     cp_wait<0>();
     __syncwarp();
     // ---------------------------------------------------------- the warps' sums
-    float4* const sums = (float4*)(smem + kWarps * X::warp_bytes);  // [kWarps][NR] maximum (log2), weights' sum, unit
+    float4* const sums = (float4*)(smem + warps * X::warp_bytes);  // [warps][NR] maximum (log2), weights' sum, unit
     float* const mine = (float*)ring;                               // [NR][DP]
 #pragma unroll
     for (int t = 0; t < sets; ++t) {
@@ -497,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     __syncthreads();
     // Joins n parts (32 at most), a row to a warp, in their order: lane w has part w's statistics, then each lane DP / 32
     // elements of the outputs.
-    constexpr int E = DP / 32;
+    constexpr int E = DP / 32, kAtOnce = 16;
     auto join = [&](int n, int r, auto&& stats, auto&& values, bool all, float4* to_s, float* to_o) {
         const float4 y = lane < n ? stats(lane, r) : make_float4(kNone, 0.f, 0x1p115f, 0.f);
         float M = y.x, U = y.z;
@@ -513,12 +531,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
         const float g = f * (U / y.z);  // (units are powers of two)
         float x[E] = {};
 #pragma unroll 1
-        for (int w0 = 0; w0 < n; w0 += 4) {
-            float z[4][E];
+        for (int w0 = 0; w0 < n; w0 += kAtOnce) {
+            float z[kAtOnce][E];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) values(min(w0 + w, n - 1), r, z[w]);
+            for (int w = 0; w < kAtOnce; ++w) values(min(w0 + w, n - 1), r, z[w]);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < kAtOnce; ++w) {
                 const float gw = __shfl_sync(0xFFFFFFFFu, g, min(w0 + w, n - 1));
                 if (w0 + w >= n || gw == 0.f) continue;
 #pragma unroll
@@ -546,8 +564,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     float4* const to_s = p.part_s + (part0 + split) * p.rows_max;
     float* const to_o = p.part_o + (part0 + split) * p.rows_max * DP;
 #pragma unroll 1
-    for (int r = warp; r < rows; r += kWarps)
-        join(kWarps, r, [&](int w, int r) { return sums[w * NR + r]; },
+    for (int r = warp; r < rows; r += warps)
+        join(warps, r, [&](int w, int r) { return sums[w * NR + r]; },
              [&](int w, int r, float (&z)[E]) {
 #pragma unroll
                  for (int i = 0; i < E; ++i) z[i] = ((const float*)(smem + w * X::warp_bytes))[r * DP + lane * E + i];
@@ -566,7 +584,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
     __syncthreads();
     if (!last) return;
 #pragma unroll 1
-    for (int r = warp; r < rows; r += kWarps)
+    for (int r = warp; r < rows; r += warps)
         join(p.splits, r, [&](int w, int r) { return __ldcg(p.part_s + (part0 + w) * p.rows_max + r); },
              [&](int w, int r, float (&z)[E]) {
                  const float* const at = p.part_o + ((part0 + w) * p.rows_max + r) * DP + lane * E;
@@ -579,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_few_kernel(const __grid
 }
 
 template <int NR, int DP, bool Q8>
-cudaError_t launch(const FewParams& p, cudaStream_t s) {
+cudaError_t launch(const FewParams& p, int warps, cudaStream_t s) {
     using X = Few<NR, DP, Q8>;
     auto* f = attend_few_kernel<NR, DP, Q8>;
     static std::atomic<uint64_t> known{0};  // devices on which the kernel may use that much shared memory
@@ -588,18 +606,18 @@ cudaError_t launch(const FewParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(known.load() & bit) || dev >= 64) {
-        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X::total)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxWarps * X::per_warp))) != cudaSuccess) return e;
         known.fetch_or(bit);
     }
-    const int64_t grid = p.ctas + (p.a.c.B + kWarps - 1) / kWarps;
+    const int64_t grid = p.ctas + (p.a.c.B + warps - 1) / warps;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    f<<<(unsigned)grid, kWarps * 32, X::total, s>>>(p);
+    f<<<(unsigned)grid, warps * 32, warps * X::per_warp, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int NR, bool Q8>
-cudaError_t launch_dim(const FewParams& p, cudaStream_t s) {
-    return p.a.c.D <= 64 ? launch<NR, 64, Q8>(p, s) : launch<NR, 128, Q8>(p, s);
+cudaError_t launch_dim(const FewParams& p, int warps, cudaStream_t s) {
+    return p.a.c.D <= 64 ? launch<NR, 64, Q8>(p, warps, s) : launch<NR, 128, Q8>(p, warps, s);
 }
 
 }  // namespace
@@ -612,11 +630,10 @@ size_t attend_few_workspace(int64_t rows) {
 
 cudaError_t launch_attend_few(const KvAttend& a, void* workspace, cudaStream_t s) {
     const int64_t rows = (int64_t)a.t_max * a.G, entries = (int64_t)a.c.B * a.c.H;
-    // Pieces: so many that the CTAs make several waves (152 SMs, 3 CTAs each), but none shorter than four runs for each
-    // warp where the window is full.
-    const int64_t most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + kRun);
-    const int64_t runs = (most + kRun - 1) / kRun, wanted = kWaves * 3 * 152;
-    int64_t splits = std::min((wanted + entries - 1) / entries, runs / (kWarps * kLeast));
+    // @@RULE
+    const int64_t most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + 16);
+    const int warps = entries >= 304 ? 2 : 8;
+    int64_t splits = std::min(152 * 8 / warps / entries, most / (warps * kLeast));
     splits = std::max<int64_t>(1, std::min<int64_t>({splits, 32, kParts / entries}));
     FewParams p;
     p.a = a;
@@ -630,8 +647,8 @@ cudaError_t launch_attend_few(const KvAttend& a, void* workspace, cudaStream_t s
     p.part_s = (float4*)(ws + kHeaderBytes);
     p.part_o = (float*)(p.part_s + kParts * rows);
     const bool q8 = a.c.esz == 1;
-    if (rows <= 8) return q8 ? launch_dim<8, true>(p, s) : launch_dim<8, false>(p, s);
-    return q8 ? launch_dim<16, true>(p, s) : launch_dim<16, false>(p, s);
+    if (rows <= 8) return q8 ? launch_dim<8, true>(p, warps, s) : launch_dim<8, false>(p, warps, s);
+    return q8 ? launch_dim<16, true>(p, warps, s) : launch_dim<16, false>(p, warps, s);
 }
 
 }  // namespace specv
