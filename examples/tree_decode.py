@@ -5,9 +5,13 @@ per step: the drafter hangs a tree of candidates on each sequence's last
 token; spec_kv_append writes the tree's keys and values, spec_kv_attend lets
 each node see the cache and its ancestors, spec_tree_verify walks the tree on
 the logits, and spec_kv_compact keeps the accepted path's entries and lengths.
-What comes out is what one token at a time gives, in fewer steps.
+With --rotary the keys are rotated on their way into the cache, the queries
+beside them (spec_kv_append_rope), and with --window a token sees the latest
+positions and the first few only (spec_kv_attend_window). What comes out is
+what one token at a time gives, in fewer steps.
 
     python examples/tree_decode.py --cache e4m3 --batch 16 --tokens 128
+    python examples/tree_decode.py --rotary --window 64 --sinks 4
 """
 import argparse
 import os
@@ -23,7 +27,7 @@ import speculative_decoding_verification_38_gb300 as sv  # noqa: E402
 class Model:
     """Random weights; the attention is the caller's."""
 
-    def __init__(self, *, vocab=512, layers=2, q_heads=8, kv_heads=2, head_dim=64, seed=0, device="cuda"):
+    def __init__(self, *, vocab=512, layers=2, q_heads=8, kv_heads=2, head_dim=64, seed=0, device="cuda", rotary=False):
         self.vocab, self.layers, self.q_heads, self.kv_heads, self.head_dim = vocab, layers, q_heads, kv_heads, head_dim
         width = q_heads * head_dim
         gen = torch.Generator().manual_seed(seed)
@@ -32,11 +36,15 @@ class Model:
         self.qkv = [new(width, (q_heads + 2 * kv_heads) * head_dim) / width**0.5 for _ in range(layers)]
         self.out = [new(width, width) / width**0.5 for _ in range(layers)]
         self.freq = torch.exp(-torch.arange(0, width, 2, device=device) * (5.0 / width))
+        # rotary: positions turn keys and queries; else they are added to the tokens
+        self.rope = sv.Rope(10000.0 ** (-torch.arange(0, head_dim, 2, device=device) / head_dim)) if rotary else None
 
     def logits(self, tokens, positions, attend):
         """attend(layer, q [rows, q_heads, head_dim], k, v [rows, kv_heads, head_dim]) gives q's shape."""
-        angle = positions[:, None] * self.freq
-        x = self.embed[tokens] + torch.cat([angle.sin(), angle.cos()], 1)
+        x = self.embed[tokens]
+        if self.rope is None:
+            angle = positions[:, None] * self.freq
+            x = x + torch.cat([angle.sin(), angle.cos()], 1)
         D = self.head_dim
         for i in range(self.layers):
             y = (self._norm(x) @ self.qkv[i]).to(torch.bfloat16).view(len(x), -1, D)  # q, k and v stay one tensor
@@ -52,9 +60,9 @@ class Model:
 class Decoder:
     """A batch of sequences and their cache."""
 
-    def __init__(self, model, batch, max_len, *, quantised=False, block_size=16, seed=0):
+    def __init__(self, model, batch, max_len, *, quantised=False, block_size=16, seed=0, window=0, sinks=0):
         m, dev = model, model.embed.device
-        self.model, self.batch = model, batch
+        self.model, self.batch, self.window, self.sinks = model, batch, window, sinks
         per = -(-max_len // block_size)
         shape = (m.layers, batch * per, block_size, m.kv_heads, m.head_dim)
         pages = torch.randperm(batch * per, generator=torch.Generator().manual_seed(seed))  # in no order
@@ -74,13 +82,22 @@ class Decoder:
         out = torch.empty(len(tokens), m.q_heads, m.head_dim, dtype=torch.bfloat16, device=dev)
 
         def attend(layer, q, k, v):
-            sv.check(sv.spec_kv_append(self.cache, k, v, lens, row_off, t_max, layer), "append")
+            if m.rope is None:
+                sv.check(sv.spec_kv_append(self.cache, k, v, lens, row_off, t_max, layer), "append")
+            else:  # positions are the cache's own, a node's by its depth
+                turned = torch.empty_like(out)
+                sv.check(sv.spec_kv_append_rope(self.cache, m.rope, k, v, lens, row_off, t_max, parent=parent, q=q, q_out=turned,
+                                                layer=layer), "append")
+                q = turned
             args = sv.AttendArgs(cache=self.cache, q=q, out=out, kv_lens=lens, row_off=row_off, t_max=t_max,
                                  scale=m.head_dim**-0.5, parent=parent, layer=layer)
             if t_max not in self.workspace:  # one for each shape, kept
                 self.workspace[t_max] = sv.Workspace.for_attend(args)
             args.set_workspace(self.workspace[t_max])
-            sv.check(sv.spec_kv_attend(args), "attend")
+            if self.window:
+                sv.check(sv.spec_kv_attend_window(args, self.window, self.sinks), "attend")
+            else:
+                sv.check(sv.spec_kv_attend(args), "attend")
             return out
 
         return m.logits(tokens, start + depth, attend), lens
@@ -173,10 +190,13 @@ def main():
     ap.add_argument("--batch", type=int, default=16)
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--tokens", type=int, default=128)
+    ap.add_argument("--rotary", action="store_true")
+    ap.add_argument("--window", type=int, default=0, help="positions that a token sees (0: all)")
+    ap.add_argument("--sinks", type=int, default=4, help="first positions that stay visible with a window")
     o = ap.parse_args()
-    model = Model()
+    model = Model(rotary=o.rotary)
     prompt = torch.randint(model.vocab, (o.batch, o.prompt), generator=torch.Generator().manual_seed(1)).cuda()
-    how = dict(quantised=o.cache == "e4m3")
+    how = dict(quantised=o.cache == "e4m3", window=o.window, sinks=o.sinks)
     want, lead = one_at_a_time(model, prompt, o.tokens, **how)
     torch.cuda.synchronize()
     t = time.perf_counter()

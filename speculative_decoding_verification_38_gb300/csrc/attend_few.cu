@@ -13,7 +13,17 @@
 // O^T += V^T P^T with the rows as its 8 columns, as S's accumulators are that
 // operand as they lie.
 //
-// Bounds: @@BOUNDS
+// Bounds (8 heads of 128, pages of 16). bf16 tokens of 16 sequences through a
+// window of 4,096: 44 us for 268 MB, 0.90 of the copy bandwidth; of 64, 1.0.
+// e4m3 tokens of 64 sequences through 1,024: 31 us for 138 MB, 0.66: issue,
+// some 850 instructions for a warp's run of 32 positions (a third turn codes to
+// f16), at 0.4 a cycle with two warps to a scheduler. One sequence through
+// 4,096: 9.6 us, latency: launch, length, page, run, the warps' join, the
+// pieces'. On the tensor cores' asynchronous path (attend.cuh, rows in tiles of
+// 16) these took 62, 197, 73 and 14.6 us: there an entry's end waits for the
+// last of its tiles, and a window's entry has few. From 17 rows on it is the
+// faster one: rows of 16 to a warp, three warps to a run, 9 tokens x 4 query
+// heads of 64 sequences took 138 us, there 76.
 #include <algorithm>
 #include <atomic>
 
@@ -38,7 +48,7 @@ struct FewParams {
 
 constexpr int kMaxWarps = 8;
 constexpr int kBoxLog = 4;        // log2 of the most positions that the list keeps together
-constexpr int64_t kLeast = 32;    // positions of a warp, at least
+constexpr int64_t kLeast = 32;    // positions of a warp, at least, where an entry is in pieces
 constexpr int64_t kParts = 2048;  // most pieces where entries are split
 constexpr float kNone = -INFINITY;
 
@@ -524,8 +534,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend_few_kernel(const __g
             M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, i));
             U = fminf(U, __shfl_xor_sync(0xFFFFFFFFu, U, i));
         }
-        const float f = y.x == kNone ? 0.f : ex2(y.x - M);
-        float sum = y.x == kNone ? 0.f : f * y.y;
+        // (a part whose scores are all NaN has no maximum, and a sum that is NaN)
+        const float f = y.x != kNone ? ex2(y.x - M) : y.y == 0.f ? 0.f : 1.f;
+        float sum = f * y.y;
 #pragma unroll
         for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
         const float g = f * (U / y.z);  // (units are powers of two)
@@ -538,7 +549,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) attend_few_kernel(const __g
 #pragma unroll
             for (int w = 0; w < kAtOnce; ++w) {
                 const float gw = __shfl_sync(0xFFFFFFFFu, g, min(w0 + w, n - 1));
-                if (w0 + w >= n || gw == 0.f) continue;
+                if (w0 + w >= n) continue;
 #pragma unroll
                 for (int i = 0; i < E; ++i) x[i] = fmaf(gw, z[w][i], x[i]);
             }
@@ -630,9 +641,13 @@ size_t attend_few_workspace(int64_t rows) {
 
 cudaError_t launch_attend_few(const KvAttend& a, void* workspace, cudaStream_t s) {
     const int64_t rows = (int64_t)a.t_max * a.G, entries = (int64_t)a.c.B * a.c.H;
-    // @@RULE
+    // Warps to an entry: with fewer a CTA starts and ends for more positions, but the CTAs of a call should be on the 152 SMs
+    // at once (rings of 1 x 8, 2 x 4 or 4 x 2 warps fit). One e4m3 token through 1,024 positions, us with 8, 4 and 2 warps:
+    // of 16 sequences (128 entries) 11.8, 13.9, 16; of 32 22, 17, 22; of 64 46, 36, 31; of 96 66, 52, 57.
+    // Pieces only where an entry's warps leave SMs empty, and none shorter than kLeast positions for each warp where the
+    // window is full (one sequence through 4,096: 32 positions 8.8 us, 64 10.4).
     const int64_t most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + 16);
-    const int warps = entries >= 304 ? 2 : 8;
+    const int warps = entries <= 152 ? 8 : entries <= 304 ? 4 : entries <= 608 ? 2 : 4;
     int64_t splits = std::min(152 * 8 / warps / entries, most / (warps * kLeast));
     splits = std::max<int64_t>(1, std::min<int64_t>({splits, 32, kParts / entries}));
     FewParams p;

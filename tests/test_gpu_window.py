@@ -72,8 +72,8 @@ def test_tree(sv, dtype, window, sinks, H, G, D, bs, order, pad):
 @pytest.mark.parametrize("G,D,t", [(1, 64, 1), (4, 128, 1), (4, 128, 5), (4, 64, 9), (8, 128, 9), (4, 128, 29), (8, 128, 17)])
 def test_many_tiles_to_a_processor(sv, dtype, G, D, t):
     """More tiles than 152 processors take at once, every size of row tile; half the batch as trees."""
-    lens = [int(x) for x in np.random.default_rng(3).integers(t, 2500, 24)]
-    tokens = [max(1, t - b % 3) for b in range(24)]
+    lens = [int(x) for x in np.random.default_rng(3).integers(t, 1800, 14)]
+    tokens = [max(1, t - b % 3) for b in range(14)]
     for parent in (None, sum((random_tree(n, b) for b, n in enumerate(tokens)), [])):
         c = WindowCase(lens=lens, tokens=tokens, H=8, G=G, D=D, dtype=dtype, q_scale=2.0, window=900, sinks=5, parent=parent)
         c.attend(sv)
@@ -310,3 +310,181 @@ def test_batch_without_new_tokens(sv, dtype, D):
     c = WindowCase(lens=[30, 0, 7], tokens=[0, 0, 0], H=2, G=2, D=D, dtype=dtype, window=5, sinks=1)
     c.attend(sv)
     assert c.status.tolist() == [0, 0, 0]
+
+
+# ------------------------------------------------------------------ up to 16 rows to a key-value head
+FEW = [  # G, t, D, bs, order
+    (1, 16, 128, 16, "nhd"), (2, 8, 64, 16, "hnd"), (4, 4, 128, 5, "nhd"), (8, 2, 96, 16, "nhd"), (3, 5, 128, 24, "hnd"),
+    (16, 1, 64, 1, "nhd"), (1, 9, 32, 128, "hnd"), (2, 4, 128, 16, "hnd"), (1, 8, 16, 16, "nhd"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("as_tree", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (5, 7), (16, 16), (40, 3), (200, 0), (2**31 - 1, 5)])
+@pytest.mark.parametrize("G,t,D,bs,order", FEW)
+def test_few_rows(sv, dtype, as_tree, window, sinks, G, t, D, bs, order):
+    """Ragged chains and trees of few rows: windows shorter than the tree is deep, sinks among the new tokens."""
+    tokens = [t, max(1, t - 1), 1, t, 0, t]
+    lens = [t, 33, 17, 400, 9, 131]
+    parent = sum((random_tree(n, b) if n else [] for b, n in enumerate(tokens)), []) if as_tree else None
+    c = WindowCase(lens=lens, tokens=tokens, H=2, G=G, D=D, bs=bs, dtype=dtype, order=order, parent=parent, q_scale=2.0,
+                   window=window, sinks=sinks)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * c.B
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,H", [(1, 1), (3, 2), (19, 8), (25, 8), (40, 8), (101, 8)])
+@pytest.mark.parametrize("G,t,D", [(4, 1, 64), (4, 4, 64)])
+def test_few_rows_of_many_entries(sv, dtype, B, H, G, t, D):
+    """Entries in pieces, and by eight, four and two warps; more of them than fit at once. The same call twice: the same bits."""
+    r = np.random.default_rng(B)
+    tokens = [int(x) for x in r.integers(1, t + 1, B)]
+    lens = [n + int(x) for n, x in zip(tokens, r.integers(0, 700, B))]
+    c = WindowCase(lens=lens, tokens=tokens, H=H, G=G, D=D, dtype=dtype, window=500, sinks=9, q_scale=2.0)
+    c.attend(sv)
+    assert c.status.tolist() == [0] * B
+    c.check()
+    first = c.out.clone()
+    for _ in range(3):
+        c.attend(sv)
+        assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("dtype,value", [("bf16", float("nan")), ("bf16", float("inf")), ("bf16", -float("inf")),
+                                         ("e4m3", float("nan"))])
+@pytest.mark.parametrize("window,sinks", [(3, 0), (12, 4), (130, 0)])
+@pytest.mark.parametrize("G,t,D", [(1, 16, 128), (4, 4, 64), (2, 4, 96)])
+@pytest.mark.parametrize("as_tree", [False, True])
+def test_values_that_only_some_of_few_rows_see(sv, dtype, value, window, sinks, G, t, D, as_tree):
+    lens = [t, 130, 257, 500]
+    parent = sum((random_tree(t, 7 + b) for b in range(4)), []) if as_tree else None
+    make = lambda: WindowCase(lens=lens, tokens=[t] * 4, H=2, G=G, D=D, dtype=dtype, parent=parent, q_scale=2.0,  # noqa: E731
+                              window=window, sinks=sinks)
+    clean = make()
+    out, lse, av, mag, spread = clean.expected()
+    for what in ("kv", "v"):
+        c = make()
+        hit = np.zeros(c.rows, dtype=bool)
+        for b in range(c.B):
+            p = _parted(c, b)
+            for at in ((p[0], p[-1]) if len(p) else ()):
+                c.fill(b, at, value, what)
+                hit[c.row_off[b]:c.row_off[b + 1]] |= c.seen(b)[:, at]
+        c.attend(sv)
+        got = c.out.double().cpu().numpy()
+        assert hit.any() and (~hit).any()
+        assert (np.abs(got - out) <= clean.bound(out, av, mag, spread))[~hit].all()
+        if what == "v" or value != value:
+            assert not np.isfinite(got[hit]).any()
+
+
+@pytest.mark.parametrize("value", [2.0**20, 2.0**100, float("inf"), float("nan")])
+@pytest.mark.parametrize("as_tree", [False, True])
+@pytest.mark.parametrize("G,t,D", [(1, 16, 128), (4, 4, 64), (2, 4, 128)])
+def test_value_scales_that_only_some_of_few_rows_see(sv, value, as_tree, G, t, D):
+    parent = sum((random_tree(t, b) for b in range(3)), []) if as_tree else None
+    make = lambda: WindowCase(lens=[600, 1300, 250], tokens=[t] * 3, H=2, G=G, D=D, dtype="e4m3", parent=parent, q_scale=2.0,  # noqa: E731
+                              window=200, sinks=140)
+    clean, c = make(), make()
+    hit = np.zeros(c.rows, dtype=bool)
+    for b in range(c.B):
+        p = _parted(c, b)[0]
+        g, i = c.pages_of[b, p // c.bs], p % c.bs
+        c.vs[c.layer, g, :, i] = value
+        hit[c.row_off[b]:c.row_off[b + 1]] |= c.seen(b)[:, p]
+    c.attend(sv)
+    out, lse, av, mag, spread = clean.expected()
+    got = c.out.double().cpu().numpy()
+    assert hit.any() and (~hit).any()
+    assert (np.abs(got - out) <= clean.bound(out, av, mag, spread))[~hit].all()
+    if value == 2.0**20:
+        out, lse, av, mag, spread = c.expected()
+        assert (np.abs(got - out) <= c.bound(out, av, mag, spread)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [10, 33, 60, 110])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("G,t,D", [(8, 1, 64), (4, 4, 128), (8, 9, 64)])
+def test_scores_far_from_zero(sv, dtype, power, sign, G, t, D):
+    """All scores about sign * 2^power: equal keys, so that the weights are equal and a row's output is a mean of values."""
+    c = WindowCase(lens=[300, 40], tokens=[t, t], H=1, G=G, D=D, dtype=dtype, window=100, sinks=5)
+    half = power // 2
+    for b in range(2):
+        for j in range(c.lens[b]):
+            g, i = c.pages_of[b, j // c.bs], j % c.bs
+            if not c.seen(b)[:, j].any():
+                continue
+            if dtype == "bf16":
+                c.k[0, g, i, 0] = sign * 2.0**(power - half)
+            else:
+                c.k[0, g, i, 0] = 0x38 | (0x80 if sign < 0 else 0)
+                c.ks[0, g, 0, i] = 2.0**(power - half)
+    c.q.fill_(2.0**half)
+    c.attend(sv)
+    k, v, ks, vs = c.host()
+    got = c.out.double().cpu().numpy()
+    for b in range(2):
+        see = c.seen(b)
+        vv = okv.entries(v, vs, c.table[b], 0, 0, c.lens[b], see.any(0))
+        for u in range(t):
+            want, mean = vv[see[u]].mean(0), np.abs(vv[see[u]]).mean(0)
+            row = got[c.row_off[b] + u]
+            assert (np.abs(row - want) <= 2.0**-8 * np.abs(want) + 2.0**-10 * mean).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("G,t", [(4, 3), (4, 9)])
+def test_query_that_is_not_finite(sv, dtype, value, G, t):
+    """Its own row is NaN, and no other."""
+    make = lambda: WindowCase(lens=[150, 40], tokens=[t, 2], H=2, G=G, D=128, dtype=dtype, q_scale=2.0, window=60, sinks=2)  # noqa: E731
+    clean, c = make(), make()
+    c.q[1, 5, 77] = value
+    c.attend(sv)
+    out, lse, av, mag, spread = clean.expected()
+    got = c.out.double().cpu().numpy()
+    keep = np.ones(got.shape[:2], dtype=bool)
+    keep[1, 5] = False
+    assert np.isnan(got[1, 5]).all()
+    assert (np.abs(got - out) <= clean.bound(out, av, mag, spread))[keep].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,t", [(2, 1), (4, 4), (4, 9)])
+def test_growing_scores(sv, dtype, G, t):
+    """Scores that rise along the window (every run a new maximum), then fall."""
+    for sign in (1, -1):
+        c = WindowCase(lens=[1500], tokens=[t], H=1, G=G, D=64, dtype=dtype, window=1200, sinks=30)
+        ramp = torch.linspace(0.1, 4.0, 1500)
+        for j in range(1500):
+            if not c.seen(0)[:, j].any():
+                continue
+            g, i = c.pages_of[0, j // c.bs], j % c.bs
+            x = torch.full((64,), float(ramp[j] if sign > 0 else ramp[-1 - j]))
+            c.k[0, g, i, 0].copy_(x.to(torch.bfloat16) if dtype == "bf16" else (x * 64).to(torch.float8_e4m3fn).view(torch.uint8))
+            if dtype == "e4m3":
+                c.ks[0, g, 0, i] = 2.0**-6
+        c.q = torch.full_like(c.q, 2.0)
+        c.attend(sv)
+        c.check()
+
+
+def test_layers_of_a_cache_by_one_argument_struct(sv):
+    """set_layer between calls, strided queries, outputs without lse and statuses, on a stream of its own."""
+    c = WindowCase(lens=[70, 300], tokens=[2, 2], H=2, G=2, D=64, layers=3, layer=2, window=50, sinks=2, hide=False)
+    wide = torch.randn((c.rows, 8, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    c.q = wide[:, 2:6].cpu()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.attend(sv, lse=False, status=False, q=wide[:, 2:6], stream=s)
+        c.args.set_layer(0)
+        sv.check(sv.spec_kv_attend_window(c.args, 50, 2, stream=s), "window")
+        c.args.set_layer(2)
+        sv.check(sv.spec_kv_attend_window(c.args, 50, 2, stream=s), "window")
+    s.synchronize()
+    c.check()
