@@ -205,6 +205,8 @@ class SpecKvAppendRopeArgs(ctypes.Structure):
     ]
 
 
+_APPEND_ROPE_SIZE = ctypes.sizeof(SpecKvAppendRopeArgs)
+
 _lib = None
 _lock = threading.Lock()
 
@@ -521,6 +523,7 @@ class KVCache:
             k.stride(i) if k.shape[i] > 1 else 0 for i in range(4))
         c.k_scale, c.v_scale = _ptr(k_scale), _ptr(v_scale)
         c.block_table = block_table.data_ptr()
+        self.batch, self.kv_heads, self.head_dim = c.batch, heads, dim  # (a struct's fields are slow to read)
         self.struct = c
         self.ref = ctypes.byref(c)
 
@@ -601,6 +604,7 @@ class Rope:
         for i, n in enumerate(sections):
             r.sections[i] = n
         r.factor, r.inv_freq = float(factor), inv_freq.data_ptr()
+        self.axes = r.axes
         self.struct = r
         self.ref = ctypes.byref(r)
 
@@ -787,20 +791,14 @@ def spec_kv_attend_window(args: AttendArgs, window: int, sinks: int = 0, stream=
     return (_lib or lib()).spec_kv_attend_window(args.cache.ref, args.ref, window, sinks, _stream(stream))
 
 
-def _head_rows(t, name, dim=None) -> tuple:
+def _head_rows(t, name, heads=None, dim=None) -> tuple:
     """(rows, heads, row stride) of a CUDA tensor [rows, heads, head_dim] with a row's heads packed."""
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [rows, heads, head_dim]")
-    rows, heads, d = t.shape
-    a, b, e = t.stride()
-    if (dim is not None and d != dim) or e != 1 or (heads > 1 and b != d):
-        raise ValueError(f"{name} must have packed heads" + ("" if dim is None else f" of {dim}"))
-    return rows, heads, (a if rows > 1 else 0)
-
-
-def _check_positions(t, rope, rows):
-    T = _types()
-    _check_typed(t, "positions", T.int32, rope.struct.axes * rows)
+    shape = t.shape
+    if len(shape) == 3 and t.is_cuda and (heads is None or shape[1] == heads) and (dim is None or shape[2] == dim):
+        a, b, e = t.stride()
+        if e == 1 and (b == shape[2] or shape[1] == 1):
+            return shape[0], shape[1], (a if shape[0] > 1 else 0)
+    raise ValueError(f"{name} must be a CUDA tensor [rows, {heads or 'heads'}, {dim or 'head_dim'}] with a row's heads packed")
 
 
 def spec_rope(rope: Rope, x, out, positions, stream=None) -> int:
@@ -808,12 +806,12 @@ def spec_rope(rope: Rope, x, out, positions, stream=None) -> int:
     heads packed) into out (of that shape; x itself: in place). positions:
     int32 [rows], or [axes, rows]."""
     rows, heads, stride = _head_rows(x, "x")
-    if out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    out_stride = _head_rows(out, "out")[2]
-    if positions is None:
-        raise ValueError("positions is required")
-    _check_positions(positions, rope, rows)
+    out_stride = stride
+    if out is not x:
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        out_stride = _head_rows(out, "out")[2]
+    _check_typed(positions, "positions", _types().int32, rope.axes * rows, optional=False)
     return (_lib or lib()).spec_rope(rope.ref, x.data_ptr(), _dtype_code(x, "x"), stride, out.data_ptr(),
                                      _dtype_code(out, "out"), out_stride, rows, heads, x.shape[2], positions.data_ptr(),
                                      _stream(stream))
@@ -825,26 +823,30 @@ def spec_kv_append_rope(cache: KVCache, rope: Rope, k_new, v_new, kv_lens, row_o
     [rows, q_heads, head_dim] (k_new's type) into q_out (bfloat16; q itself: in
     place). Positions are the cache's own (parent int32 [rows]: by depth in a
     token tree), or given: int32 [rows], or [axes, rows]."""
-    T, c = _types(), cache.struct
-    rows, stride = _entry_rows(k_new, "k_new", c)
-    if v_new.dtype is not k_new.dtype or _entry_rows(v_new, "v_new", c) != (rows, stride):
+    T, batch, kind = _types(), cache.batch, k_new.dtype
+    rows, heads, stride = _head_rows(k_new, "k_new", cache.kv_heads, cache.head_dim)
+    if v_new.dtype is not kind or _head_rows(v_new, "v_new", heads, cache.head_dim) != (rows, heads, stride):
         raise ValueError("k_new and v_new must have one type, shape and row stride")
-    _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
-    _check_typed(row_off, "row_off", T.int64, c.batch + 1)
-    _check_typed(parent, "parent", T.int32, rows)
-    _check_positions(positions, rope, rows)
-    _check_typed(seq_status, "seq_status", T.int32, c.batch)
+    _check_typed(kv_lens, "kv_lens", T.int32, batch, optional=False)
+    if row_off is not None:
+        _check_typed(row_off, "row_off", T.int64, batch + 1)
+    if parent is not None:
+        _check_typed(parent, "parent", T.int32, rows)
+    if positions is not None:
+        _check_typed(positions, "positions", T.int32, rope.axes * rows)
+    if seq_status is not None:
+        _check_typed(seq_status, "seq_status", T.int32, batch)
     qp = outp = None
     q_heads = q_stride = out_stride = 0
     if q is not None:
-        n, q_heads, q_stride = _head_rows(q, "q", c.head_dim)
-        if n != rows or q.dtype is not k_new.dtype or q_out is None or q_out.shape != q.shape or q_out.dtype is not T.bfloat16:
+        n, q_heads, q_stride = _head_rows(q, "q", None, cache.head_dim)
+        if n != rows or q.dtype is not kind or q_out is None or q_out.shape != q.shape or q_out.dtype is not T.bfloat16:
             raise ValueError("q must have k_new's rows and type, and q_out its shape in bfloat16")
-        out_stride = _head_rows(q_out, "q_out", c.head_dim)[2]
+        out_stride = _head_rows(q_out, "q_out")[2]
         qp, outp = q.data_ptr(), q_out.data_ptr()
-    a = SpecKvAppendRopeArgs(ctypes.sizeof(SpecKvAppendRopeArgs), layer, _dtype_code(k_new, "k_new"), t_max or 0, rows,
-                             _ptr(row_off), kv_lens.data_ptr(), _ptr(parent), _ptr(positions), k_new.data_ptr(),
-                             v_new.data_ptr(), stride, qp, outp, q_stride, out_stride, q_heads, _ptr(seq_status))
+    a = SpecKvAppendRopeArgs(_APPEND_ROPE_SIZE, layer, _dtype_code(k_new, "k_new"), t_max or 0, rows, _ptr(row_off),
+                             kv_lens.data_ptr(), _ptr(parent), _ptr(positions), k_new.data_ptr(), v_new.data_ptr(), stride, qp,
+                             outp, q_stride, out_stride, q_heads, _ptr(seq_status))
     return (_lib or lib()).spec_kv_append_rope(cache.ref, rope.ref, ctypes.byref(a), _stream(stream))
 
 

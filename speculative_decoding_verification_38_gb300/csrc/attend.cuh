@@ -752,41 +752,50 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
     // is one past the pool: zeros. A page's slots past the length come as they are; softmax hides their scores and
     // clears their values.
     const int boxes = kTileTok >> p.box_log;
-    auto page_of = [&](const int32_t* table, int32_t pos, int32_t L) {
-        int32_t pg = -1;
-        if (pos < L) pg = table[c.by_bs.of(pos)];
-        return pg >= 0 && pg < c.num_blocks ? pg : c.num_blocks;
+    struct Box {
+        int32_t page, slot;
+    };
+    auto box_of = [&](const int32_t* table, int32_t pos, int32_t L) {
+        Box x = {-1, 0};
+        if (pos < L) {
+            const int32_t j = c.by_bs.of(pos);
+            x.page = table[j];
+            x.slot = pos - j * c.bs;
+        }
+        if (x.page < 0 || x.page >= c.num_blocks) x.page = c.num_blocks;
+        return x;
     };
     // (Win: `at` counts places, g's positions go by its sight)
     auto sight_of = [&](const Seg* g) { return Win ? Sight(g->T, g->L, a.window, a.sinks, p.box_log) : Sight(); };
     auto position = [&](const Sight& sight, int32_t place) { return Win ? sight.at(place) : place; };
+    // bf16: four boxes at a time, their pages to every lane, then their loads by one lane. (With a vote for that lane and a
+    // loop's turn for each box the warp that loads K took about 2,500 cycles a tile, as HBM does: 2 x 9 tokens through a
+    // window of 65,536 111 to 102 us, 64 x 9 over 146,153 positions 115 to 110. e4m3, a copy to a box, was slower by fours,
+    // 313 to 322 for ragged chains.)
     auto bring = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar, const int32_t* table, int32_t at, int32_t L,
-                     int32_t head, int32_t pages, const Sight& sight) {  // pages: of boxes 0 .. 31, a lane each
+                     int32_t head, Box mine, const Sight& sight) {  // mine: boxes 0 .. 31, a lane each
         if (elect()) mbar_arrive_expect_tx(bar, kTileTok * (Q8 || DP == 64 ? 128 : 256));
         __syncwarp();
-        int32_t sl = at - c.by_bs.of(at) * c.bs, slots = 0;
-        auto slot_at = [&](int j) {  // Win: a box's slot, by its own position
-            const int32_t pos = sight.at(at + (j + lane) * p.box);
-            slots = pos < L ? pos - c.by_bs.of(pos) * c.bs : 0;
-        };
-        if (Win) slot_at(0);
+        const uint32_t step = (uint32_t)p.box * 128;
+        constexpr int UN = Q8 ? 1 : 4;
 #pragma unroll 1
-        for (int j = 0; j < boxes; ++j) {
-            if (j && (j & 31) == 0) {
-                pages = page_of(table, position(sight, at + (j + lane) * p.box), L);
-                if (Win) slot_at(j);
+        for (int j0 = 0; j0 < boxes; j0 += UN) {
+            if (j0 && (j0 & 31) == 0) mine = box_of(table, position(sight, at + (j0 + lane) * p.box), L);
+            Box x[UN];
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                x[i].page = __shfl_sync(0xFFFFFFFFu, mine.page, (j0 + i) & 31);
+                x[i].slot = __shfl_sync(0xFFFFFFFFu, mine.slot, (j0 + i) & 31);
             }
-            const int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, j & 31);
-            if (Win) sl = __shfl_sync(0xFFFFFFFFu, slots, j & 31);
             if (elect()) {
-                tma_box(dst, map, 0, sl, head, pg, bar);
-                if (!Q8 && DP == 128) tma_box(dst + kTileTok * 128, map, 64, sl, head, pg, bar);
+#pragma unroll
+                for (int i = 0; i < UN; ++i)
+                    if (j0 + i < boxes) {
+                        tma_box(dst + i * step, map, 0, x[i].slot, head, x[i].page, bar);
+                        if (!Q8 && DP == 128) tma_box(dst + i * step + kTileTok * 128, map, 64, x[i].slot, head, x[i].page, bar);
+                    }
             }
-            dst += p.box * 128;
-            if (!Win) {
-                sl += p.box;
-                if (sl >= c.bs) sl = 0;
-            }
+            dst += UN * step;
         }
         __syncwarp();
     };
@@ -1103,29 +1112,36 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
             const int32_t* const table = c.table + (int64_t)g.b * c.max_blocks;
             int32_t at = g.tile0 * kTileTok;
             const Sight sight = sight_of(&g);
-            int32_t next = page_of(table, position(sight, at + lane * p.box), g.L);
+            Box next = box_of(table, position(sight, at + lane * p.box), g.L);
 #pragma unroll 1
             for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
-                const int32_t pages = next;
-                if (t + 1 < n) next = page_of(table, position(sight, at + kTileTok + lane * p.box), g.L);
+                const Box mine = next;
+                if (t + 1 < n) next = box_of(table, position(sight, at + kTileTok + lane * p.box), g.L);
                 const uint32_t slot = kt % SK;
                 const bool free = kt < SK || wait(k_empty + slot, (kt / SK - 1) & 1);
                 if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                    bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, pages, sight);
+                    bring(&p.k_map, smem_addr(smem) + slot * X::k_bytes, k_full + slot, table, at, g.L, g.h, mine, sight);
                     ++loads;
                 }
                 if constexpr (!Q8) {
                     // which positions are there
                     uint32_t* const aux = (uint32_t*)aux_of(kt);
+                    const bool there = lane >= boxes || mine.page < c.num_blocks;
+                    const bool inside = Win ? at >= sight.s1 && at + kTileTok <= sight.i1 && sight.at(at + kTileTok - 1) < g.L
+                                            : at + kTileTok <= g.L;
+                    if (inside && boxes <= 32 && __all_sync(0xFFFFFFFFu, there)) {
+                        if (lane < 4) aux[lane] = ~0u;
+                        __syncwarp();
+                    } else {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int32_t r = w * 32 + lane;
-                        int32_t pg = __shfl_sync(0xFFFFFFFFu, pages, (r >> p.box_log) & 31);
-                        const int32_t pos = position(sight, at + r);
-                        if (boxes > 32) pg = page_of(table, pos, g.L);
-                        const uint32_t bits =
-                            __ballot_sync(0xFFFFFFFFu, pg < c.num_blocks && (Win ? sight.seen(pos, g.L, a.sinks) : pos < g.L));
-                        if (lane == 0) aux[w] = bits;
+                        for (int w = 0; w < 4; ++w) {
+                            const int32_t r = w * 32 + lane, pos = position(sight, at + r);
+                            int32_t pg = __shfl_sync(0xFFFFFFFFu, mine.page, (r >> p.box_log) & 31);
+                            if (boxes > 32) pg = box_of(table, pos, g.L).page;
+                            const uint32_t bits =
+                                __ballot_sync(0xFFFFFFFFu, pg < c.num_blocks && (Win ? sight.seen(pos, g.L, a.sinks) : pos < g.L));
+                            if (lane == 0) aux[w] = bits;
+                        }
                     }
                     if (lane == 0) mbar_arrive(aux_full + kt % kAuxRing);
                 }
@@ -1190,23 +1206,23 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                     const int32_t* const table = c.table + (int64_t)g->b * c.max_blocks;
                     const Sight sight = sight_of(g);
                     done_seg(si++);
-                    int32_t next = page_of(table, position(sight, at + lane * p.box), L);
+                    Box next = box_of(table, position(sight, at + lane * p.box), L);
 #pragma unroll 1
                     for (int t = 0; t < n; ++t, ++kt, at += kTileTok) {
-                        const int32_t pages = next;
-                        if (t + 1 < n) next = page_of(table, position(sight, at + kTileTok + lane * p.box), L);
+                        const Box mine = next;
+                        if (t + 1 < n) next = box_of(table, position(sight, at + kTileTok + lane * p.box), L);
                         if constexpr (Q8) {
                             const uint32_t slot = kt % RV;
                             const bool free = kt < RV || wait(raw_empty + slot, (kt / RV - 1) & 1);
                             if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                                bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, pages, sight);
+                                bring(&p.v_map, smem_addr(raw_sm) + slot * X::raw_tile, raw_full + slot, table, at, L, h, mine, sight);
                                 ++loads;
                             }
                         } else {
                             const uint32_t slot = kt % SV;
                             const bool free = kt < SV || wait(v_empty + slot, (kt / SV - 1) & 1);
                             if (__all_sync(0xFFFFFFFFu, free && loads == kt)) {
-                                bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, pages, sight);
+                                bring(&p.v_map, smem_addr(v_sm) + slot * X::slot_bytes, v_full + slot, table, at, L, h, mine, sight);
                                 ++loads;
                             }
                         }
