@@ -540,7 +540,13 @@ SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* cache, const spec_k
  * position (none of kv_lens[b] - T_b + 1 - window and later, or of the sinks)
  * are not read and their table entries may be anything, so that an engine can
  * give them to other sequences; what a token does not see has no effect on it.
- * A window of kv_lens[b] or more hides nothing. */
+ * A window of kv_lens[b] or more hides nothing. Up to 16 rows (t_max times the
+ * query heads of a key-value head; head_dim up to 128) take a kernel of their
+ * own, with batch * kv_heads up to 2^31 - 65536 (more: SPEC_ERR_UNSUPPORTED):
+ * weights are at most one there, SPEC_BF16's in two bf16 parts, SPEC_E4M3's
+ * times V's scales in fp16: 11 bits of what is 2^-29 of the largest V scale the
+ * token sees or more (the rest to 2^-40 of that), queries exact down to 2^-31
+ * of their row's largest element. */
 SPEC_API spec_status_t spec_kv_attend_window(const spec_kv_cache_t* cache, const spec_kv_attend_args_t* args,
                                              int32_t window, int32_t sinks, spec_stream_t stream);
 
@@ -591,7 +597,8 @@ SPEC_API spec_status_t spec_rope(const spec_rope_t* rope, const void* x, int32_t
  * local node indices as spec_tree_verify's); or given (positions, int32
  * [axes, rows]; parent must then be NULL). Without positions every axis has
  * the same one. Statuses are spec_kv_append's, and LAYOUT for a bad parent
- * (nothing is written for the tokens whose way to the root leads over it). A
+ * (nothing is written for the tokens whose way to the root leads over it; a
+ * node's depth is found by walking that way). A
  * sequence with an error of its offsets or length has no rows of q_out
  * written; a token on a page outside the pool has its queries rotated all the
  * same. */

@@ -72,9 +72,10 @@ cudaError_t box_map(CUtensorMap& m, const KvView& c, void* base, int32_t box) {
 
 bool attend_takes(int32_t head_dim) { return head_dim <= 128; }
 
-size_t attend_workspace(int64_t rows) {
+size_t attend_workspace(int64_t rows, bool window) {
     const size_t n = (size_t)kAttMaxGrid * 2 * tile_rows(rows);
-    return kHeaderBytes + (n * 128 * 4 + n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign + kDepthBytes;
+    return kHeaderBytes + (n * 128 * 4 + n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign +
+           (window ? kDepthBytes : 0);
 }
 
 cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s) {

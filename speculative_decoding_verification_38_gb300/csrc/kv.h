@@ -139,7 +139,7 @@ cudaError_t launch_rope(const Rope& r, const RopeRows& q, int64_t rows, cudaStre
 // The attention on the tensor cores (attend.cu), for head_dim up to 128;
 // rows = t_max * query heads of a key-value head sets the workspace.
 bool attend_takes(int32_t head_dim);
-size_t attend_workspace(int64_t rows);
+size_t attend_workspace(int64_t rows, bool window);
 cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s);
 // Through a window, for rows = t_max * query heads of a key-value head up to 16 (attend_few.cu).
 bool attend_few_takes(int32_t head_dim, int64_t rows);

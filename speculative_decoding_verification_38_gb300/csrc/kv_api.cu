@@ -184,6 +184,13 @@ spec_status_t rope_rows(RopeRows& q, const void* x, int32_t x_dtype, int64_t x_s
     return SPEC_OK;
 }
 
+// Bytes that a call works on, with a window or without.
+size_t workspace_of(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, bool window) {
+    const int64_t rows = (int64_t)a->t_max * (a->q_heads / c->kv_heads);
+    if (!attend_takes(c->head_dim)) return kHeaderBytes;
+    return window && attend_few_takes(c->head_dim, rows) ? attend_few_workspace(rows) : attend_workspace(rows, window);
+}
+
 // window 0: none.
 spec_status_t attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, int32_t window, int32_t sinks,
                      spec_stream_t stream) {
@@ -200,8 +207,7 @@ spec_status_t attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, i
     if ((a->row_off && !aligned(a->row_off, 8)) || !aligned(a->kv_lens, 4) || !aligned(a->parent, 4) ||
         !aligned(a->lse, 4) || !aligned(a->seq_status, 4))
         return SPEC_ERR_ALIGNMENT;
-    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < spec_kv_attend_workspace_size(c, a))
-        return SPEC_ERR_WORKSPACE;
+    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < workspace_of(c, a, window > 0)) return SPEC_ERR_WORKSPACE;
     KvAttend p;
     p.c = view(c, a->layer);
     p.Hq = a->q_heads;
@@ -296,10 +302,7 @@ SPEC_API spec_status_t spec_kv_compact(const spec_kv_cache_t* c, const int64_t* 
 
 SPEC_API size_t spec_kv_attend_workspace_size(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a) {
     if (check_attend_shape(c, a) != SPEC_OK) return 0;
-    const int64_t rows = (int64_t)a->t_max * (a->q_heads / c->kv_heads);
-    if (!attend_takes(c->head_dim)) return kHeaderBytes;
-    // (one size, whether the call has a window or not)
-    return attend_few_takes(c->head_dim, rows) ? std::max(attend_workspace(rows), attend_few_workspace(rows)) : attend_workspace(rows);
+    return std::max(workspace_of(c, a, false), workspace_of(c, a, true));  // (one size, whether the call has a window or not)
 }
 
 SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, spec_stream_t stream) {

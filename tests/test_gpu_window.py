@@ -488,3 +488,44 @@ def test_layers_of_a_cache_by_one_argument_struct(sv):
         sv.check(sv.spec_kv_attend_window(c.args, 50, 2, stream=s), "window")
     s.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("G", [2, 8])
+def test_offsets_past_32_bits(sv, G):
+    """Pages two gigabytes apart: rotating append and windowed attention as in a cache whose pages lie together."""
+    H, D, bs, t = 2, 64, 16, 4
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([45], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    near = [torch.randn((1, 3, bs, H, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    far = []
+    for x in near:
+        room = torch.empty(2 * 2**30 + bs * H * D, dtype=torch.bfloat16, device="cuda")
+        view = room.as_strided((1, 3, bs, H, D), (0, 2**30, H * D, D, 1))
+        view.copy_(x)
+        far.append(view)
+    k, v = (torch.randn((t, H, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((t, H * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    rope = sv.Rope(torch.logspace(0, -4, 32, device="cuda"))
+    got = []
+    for pools in (near, far):
+        cache = sv.KVCache(*pools, table)
+        turned, out = torch.empty_like(q), torch.empty_like(q)
+        sv.check(sv.spec_kv_append_rope(cache, rope, k, v, lens, t_max=t, q=q, q_out=turned), "append")
+        args = sv.AttendArgs(cache=cache, q=turned, out=out, kv_lens=lens, t_max=t, scale=0.125)
+        args.set_workspace(sv.Workspace.for_attend(args))
+        sv.check(sv.spec_kv_attend_window(args, 30, 3), "window")
+        got.append((turned, out, pools[0].clone(), pools[1].clone()))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_a_workspace_without_a_window_may_be_smaller(sv):
+    """spec_kv_attend's own need has not grown: the size function names what serves both calls."""
+    c = WindowCase(lens=[300, 40], tokens=[2, 2], H=2, G=4, D=128, window=50, sinks=2, hide=False)
+    c.attend(sv)
+    need = sv.spec_kv_attend_workspace_size(c.args)
+    c.args.struct.workspace_bytes = need - 256
+    assert sv.spec_kv_attend_window(c.args, 50, 2) == sv.SPEC_ERR_WORKSPACE
+    sv.check(sv.spec_kv_attend(c.args), "attend")
+    torch.cuda.synchronize()

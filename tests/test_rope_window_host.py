@@ -107,6 +107,7 @@ def test_places_hold_what_is_seen_once(box):
         assert all(seen[b[b < L]].any() for b in boxes)  # and no box is loaded for nothing
         inside = pos < L
         assert np.array_equal(seen[pos[inside]], ((pos < sinks) | (pos >= lo))[inside])
+        assert all(seen[p] for p in pos[s1:i1] if p < L)  # (a whole tile of these is not looked at position by position)
         # before `tail`, a position is seen by every row or by none
         for p in pos[:tail]:
             assert p >= L or see[:, p].all() or not see[:, p].any()
