@@ -17,8 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cu", "stats.cu", "sampler.cu", "verify.cu", "misc.cu", "topk.cu", "ngram.cu", "tree.cu", "kv.cu",
            "kv_api.cu", "attend.cu", "attend_bf16.cu", "attend_bf16_wide.cu", "attend_e4m3.cu", "attend_e4m3_wide.cu",
-           "attend_window_bf16.cu", "attend_window_bf16_wide.cu", "attend_window_e4m3.cu", "attend_window_e4m3_wide.cu",
-           "attend_few.cu", "rope.cu"]
+           "attend_window_bf16.cu", "attend_window_e4m3.cu", "attend_few.cu", "rope.cu"]
 HEADERS = ["attend.cuh", "common.cuh", "internal.h", "kv.cuh", "kv.h", "precise.cuh", "settle.h", "sight.cuh",
            "stream.cuh", "tile.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

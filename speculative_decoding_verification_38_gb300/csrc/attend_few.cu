@@ -23,7 +23,7 @@
 // 16) these took 62, 197, 73 and 14.6 us: there an entry's end waits for the
 // last of its tiles, and a window's entry has few. From 17 rows on it is the
 // faster one: rows of 16 to a warp, three warps to a run, 9 tokens x 4 query
-// heads of 64 sequences took 138 us, there 76.
+// heads of 64 sequences took 115 us, there 74.
 #include <algorithm>
 #include <atomic>
 
