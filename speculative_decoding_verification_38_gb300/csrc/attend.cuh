@@ -24,23 +24,35 @@
 // weights, in units that go by the scales that a row sees.
 //
 // Bounds (8 heads of 128, pages of 16). Nine bf16 tokens of each of 64
-// sequences over 146,153 positions: 119 us for 608 MB, 0.75 of the copy
-// bandwidth; of two over 262,142: 182 us, 0.87. The difference is the ends of
+// sequences over 146,153 positions: 113 us for 608 MB, 0.79 of the copy
+// bandwidth; of two over 262,142: 180 us, 0.88. The difference is the ends of
 // entries, where a CTA's groups wait for the last of its tiles (about 12,000
 // cycles, four or five times in a run). Where a tile takes one team longer
 // than its loads, the length of its chain of steps bounds it (scores, their
 // read from TMEM, weights, their stores, the vote on references, the product),
-// with issue slots to spare: trees of 29 (116 rows), 180 us, 0.52, issue
+// with issue slots to spare: trees of 29 (116 rows), 176 us, 0.53, issue
 // active in 47 % of cycles, one place for P as two parts of 128 rows take
-// 64 KB; ragged e4m3 chains of up to 72 rows, 957 us for 2.2 GB, 0.34, about
+// 64 KB; ragged e4m3 chains of up to 72 rows, 967 us for 2.2 GB, 0.34, about
 // 4,200 cycles a tile, issue active in 55 %, a fifth of the tiles make their
-// weights twice. One e4m3 token of each of the 64: 108 us for 310 MB, 0.42,
+// weights twice. One e4m3 token of each of the 64: 99 us for 310 MB, 0.46,
 // issue active in 40 %: the ends of entries. A single sequence of 4,111:
 // 15 us, of which launch, start (the list, TMEM) and the chain page number -
 // tile - score - weight - product - join are latency. Far from the floor:
 // rows over short caches (65 tokens of 64 sequences of 100 to 400, 8 query
 // heads to a key-value head: 263 us bf16, 401 e4m3, for 201 and 170 MB), where
 // an entry's opening and end outweigh its few tiles.
+//
+// Through a sliding window (Win) the tiles are those of a list of what the
+// tokens see (sight.cuh). Nine bf16 tokens of 64 sequences, window 1,024:
+// 74 us for 270 MB, 0.54 (entries of nine tiles: their ends are a third of a
+// run); trees of 29, window 2,000: 169 us for 547 MB, 0.47 (the softmax's chain
+// of steps, 4,000 cycles a tile against HBM's 2,800); two of nine tokens,
+// window 65,536: 102 us for 538 MB, 0.78; ragged e4m3 chains, window 4,096:
+// 309 us for 533 MB, 0.25 (the same chain, and moved references). A run of
+// entries for each team, so that one team's ends hide behind the others' tiles,
+// was built and was slower (74 to 103, 309 to 414): the warps that load and
+// issue follow several runs, and teams in different places fetch different
+// code.
 #pragma once
 
 #include <cuda.h>
@@ -293,7 +305,7 @@ struct Shape {
     static constexpr uint32_t q_bytes = Q8 ? 3 * N * 128 : N * DP * 2;  // e4m3: three parts
     static constexpr uint32_t p_bytes = NP * kTileTok * 2;
     static constexpr uint32_t aux_bytes = Q8 ? 1024 + 16 : 16;  // scales of K and V, validity bits
-    static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 6 : tight && Win ? 7 : 8;  // tiles of them: more than the K ring and scores can hold
+    static constexpr int aux_ring = TM == 4 ? 16 : Q8 && TM == 1 ? 4 : tight && Win ? 7 : 8;  // tiles of them: more than the K ring and scores can hold
     static constexpr uint32_t red_bytes = 5 * MC * 8 * 4 + (Q8 ? 4 * MC * 8 : 0);  // a group's scratch
     // after the tiles, Q and P: aux ring, per team and row the reference, weight sum, factor and (e4m3) unit, row factors
     // of Q, scratch, ancestors, (window) depths and poison before the new tokens, segments, poison, barriers

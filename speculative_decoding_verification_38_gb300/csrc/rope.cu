@@ -205,6 +205,9 @@ __device__ __forceinline__ void store_entry(const float (&x)[2][8], const Chunks
 // once for a token by all threads; then the warps take keys, values and queries, 2^lanes_log threads to a head. What a
 // warp takes first is asked for before the look-ups, and the next before the last is done with. n.k null: rows without a
 // cache, at q.x.
+// Bounds (8 key-value and 32 query heads of 128): HBM for many tokens, 130,238 with their queries bf16 to bf16 490 us, 6.5
+// TB/s (0.96 of the copy bandwidth), 131,072 rows of queries 333 us, 6.5 TB/s; latency for a round, 576 tokens 5.1 us
+// (offsets, length, page, store), 576 rows of queries alone 3.5.
 template <int DT, bool Q8, int ODT, bool VEC>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_constant__ KvView c, const __grid_constant__ KvNew n,
                                                                    const __grid_constant__ Rope r,
