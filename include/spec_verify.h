@@ -582,7 +582,8 @@ typedef struct {
 /* Rotate rows: x [rows, heads, head_dim], row r head h at
  * x + r*x_token_stride + h*head_dim (elements of x_dtype), to out likewise;
  * SPEC_BF16 or SPEC_F32 each. positions: device int32 [axes, rows]. out may be
- * x with its type and stride (in place), but must not overlap it otherwise.
+ * x with its type and stride (in place), but must not overlap it otherwise; x's
+ * rows may be one (stride 0), out's may not overlap each other.
  * x, out, their row strides and head_dim are multiples of 16 bytes, head_dim
  * up to 256 (larger: SPEC_ERR_UNSUPPORTED). */
 SPEC_API spec_status_t spec_rope(const spec_rope_t* rope, const void* x, int32_t x_dtype, int64_t x_token_stride,
@@ -617,7 +618,7 @@ typedef struct {
     int64_t new_token_stride; /* elements */
     const void* q;            /* device, row r head h at q + r*q_token_stride + h*head_dim, or NULL (q_heads = 0) */
     void* q_out;              /* device bf16, row r head h at q_out + r*q_out_token_stride + h*head_dim; q itself only
-                                 where new_dtype is SPEC_BF16 and the strides are equal */
+                                 where new_dtype is SPEC_BF16 and the strides are equal; its rows may not overlap */
     int64_t q_token_stride, q_out_token_stride; /* elements, multiples of 16 bytes */
     int32_t q_heads;          /* 0: no queries */
     int32_t* seq_status;      /* device [B] or NULL */

@@ -163,7 +163,7 @@ Rope rope_of(const spec_rope_t* r, const int32_t* positions, int64_t rows, int32
 }
 
 spec_status_t rope_rows(RopeRows& q, const void* x, int32_t x_dtype, int64_t x_stride, void* out, int32_t out_dtype,
-                        int64_t out_stride, int32_t heads, int32_t head_dim) {
+                        int64_t out_stride, int64_t rows, int32_t heads, int32_t head_dim) {
     for (int32_t t : {x_dtype, out_dtype})
         if (t != SPEC_BF16 && t != SPEC_F32) return SPEC_ERR_INVALID_ARG;
     if (x_stride < 0 || out_stride < 0) return SPEC_ERR_INVALID_ARG;
@@ -173,6 +173,7 @@ spec_status_t rope_rows(RopeRows& q, const void* x, int32_t x_dtype, int64_t x_s
         head_dim * osz % 16)
         return SPEC_ERR_ALIGNMENT;
     if (head_dim % 8) return SPEC_ERR_ALIGNMENT;
+    if (rows > 1 && out_stride < (int64_t)heads * head_dim) return SPEC_ERR_INVALID_ARG;  // rows of out would overlap
     q.x = (const unsigned char*)x;
     q.out = (unsigned char*)out;
     q.x_row_bytes = x_stride * xsz;
@@ -326,7 +327,7 @@ SPEC_API spec_status_t spec_rope(const spec_rope_t* rope, const void* x, int32_t
     if (!aligned(positions, 4)) return SPEC_ERR_ALIGNMENT;
     if (rows > kMaxEntries / heads) return SPEC_ERR_UNSUPPORTED;
     RopeRows q;
-    st = rope_rows(q, x, x_dtype, x_token_stride, out, out_dtype, out_token_stride, heads, head_dim);
+    st = rope_rows(q, x, x_dtype, x_token_stride, out, out_dtype, out_token_stride, rows, heads, head_dim);
     if (st) return st;
     return launched(launch_rope(rope_of(rope, positions, rows, heads), q, rows, (cudaStream_t)stream));
 }
@@ -349,7 +350,8 @@ SPEC_API spec_status_t spec_kv_append_rope(const spec_kv_cache_t* c, const spec_
     if (a->q_heads > 0 && a->rows > kMaxEntries / a->q_heads) return SPEC_ERR_UNSUPPORTED;
     RopeRows q = {};
     if (a->q_heads > 0) {
-        st = rope_rows(q, a->q, a->new_dtype, a->q_token_stride, a->q_out, SPEC_BF16, a->q_out_token_stride, a->q_heads, c->head_dim);
+        st = rope_rows(q, a->q, a->new_dtype, a->q_token_stride, a->q_out, SPEC_BF16, a->q_out_token_stride, a->rows, a->q_heads,
+                       c->head_dim);
         if (st) return st;
     }
     if (a->rows == 0) n.k = (const unsigned char*)c->k;  // (not read: null would mean rows without a cache)

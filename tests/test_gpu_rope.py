@@ -129,6 +129,24 @@ def test_values_that_are_not_finite_stay_in_their_pair(sv):
     assert same[~touched.cuda()].all() and not out[1][touched.cuda()].isfinite().any()
 
 
+def test_a_row_read_many_times(sv):
+    """A broadcast input (row stride 0) turned by each row's own position; one row alone in place, whatever its stride."""
+    x = torch.randn((1, 3, 64), generator=torch.Generator().manual_seed(5)).to(BF).cuda()
+    pos = torch.arange(70, dtype=torch.int32, device="cuda") * 11
+    rope = sv.Rope(rotary(32).cuda())
+    got, want = (torch.empty((70, 3, 64), dtype=BF, device="cuda") for _ in range(2))
+    sv.check(sv.spec_rope(rope, x.expand(70, 3, 64), got, pos), "spec_rope")
+    sv.check(sv.spec_rope(rope, x.repeat(70, 1, 1), want, pos), "spec_rope")
+    assert torch.equal(got, want)
+    y = x.expand(70, 3, 64)
+    before = x.clone()
+    assert sv.spec_rope(rope, y, y, pos) == sv.SPEC_ERR_INVALID_ARG
+    assert torch.equal(x, before)
+    one = y[:1]
+    sv.check(sv.spec_rope(rope, one, one, pos[5:6]), "spec_rope")
+    assert torch.equal(x[0], want[5])
+
+
 def test_no_rows(sv):
     x = torch.zeros((0, 2, 64), dtype=BF, device="cuda")
     pos = torch.zeros(0, dtype=torch.int32, device="cuda")

@@ -176,6 +176,15 @@ def test_rope_in_place_needs_one_type_and_stride(sv, at, value):  # noqa: F811
     assert sv.lib().spec_rope(*a) == 1
 
 
+@pytest.mark.parametrize("x,stride", [(FAKE, 0), (FAKE, 120), (FAKE + 4096, 0), (FAKE + 4096, 120)])
+def test_rows_that_overlap_are_not_written(sv, x, stride):  # noqa: F811
+    """Rows of a broadcast tensor may be read, but not turned in place or written to: two would be one row of memory."""
+    a = [ctypes.byref(_rope(sv)), x, 1, stride, FAKE, 1, stride, 36, 2, 64, FAKE, None]
+    assert sv.lib().spec_rope(*a) == 1
+    a = _append(sv, q=x, q_out=FAKE, q_token_stride=stride, q_out_token_stride=stride)
+    assert sv.lib().spec_kv_append_rope(ctypes.byref(_cache(sv)), ctypes.byref(_rope(sv)), ctypes.byref(a), None) == 1
+
+
 @pytest.mark.parametrize("kw,status", CACHE_REFUSALS)
 def test_append_rope_refuses_a_cache(sv, kw, status):  # noqa: F811
     c = _cache(sv, **kw)
