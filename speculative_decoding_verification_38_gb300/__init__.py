@@ -39,6 +39,7 @@ SEQ_TIMEOUT, SEQ_UNSUPPORTED = 6, 7
 SPEC_TREE_MAX_CANDIDATES = 64
 SPEC_KV_MAX_QUERIES = 128
 SPEC_ROPE_MAX_AXES = 4
+_I32_MAX = 2**31 - 1
 
 
 class SpecError(RuntimeError):
@@ -595,6 +596,8 @@ class Rope:
         sections = [] if sections is None else [int(x) for x in sections]
         if sections and not 2 <= len(sections) <= SPEC_ROPE_MAX_AXES:
             raise ValueError(f"sections must name 2 to {SPEC_ROPE_MAX_AXES} axes, got {len(sections)}")
+        if sections and not 0 <= min(sections) <= max(sections) <= inv_freq.numel():
+            raise ValueError(f"an axis has 0 to {inv_freq.numel()} pairs, got {sections}")
         self.inv_freq = inv_freq
         r = SpecRope()
         r.struct_size = ctypes.sizeof(SpecRope)
@@ -787,7 +790,9 @@ def spec_kv_attend(args: AttendArgs, stream=None) -> int:
 
 def spec_kv_attend_window(args: AttendArgs, window: int, sinks: int = 0, stream=None) -> int:
     """spec_kv_attend in which a token sees the `window` positions up to its own
-    and the cache's first `sinks`."""
+    and the cache's first `sinks` (either may be any int: no cache is 2**31 - 1 long)."""
+    if window > _I32_MAX or sinks > _I32_MAX or window < 0 or sinks < 0:  # (ctypes would keep the low 32 bits)
+        window, sinks = (max(-1, min(int(n), _I32_MAX)) for n in (window, sinks))
     return (_lib or lib()).spec_kv_attend_window(args.cache.ref, args.ref, window, sinks, _stream(stream))
 
 

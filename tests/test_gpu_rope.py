@@ -147,6 +147,12 @@ def test_a_row_read_many_times(sv):
     assert torch.equal(x[0], want[5])
 
 
+@pytest.mark.parametrize("sections", [(2**32 + 16, 16), (-1, 33), (33, 0)])
+def test_sections_that_no_head_has(sv, sections):
+    with pytest.raises(ValueError):
+        sv.Rope(rotary(32).cuda(), sections=sections)
+
+
 def test_no_rows(sv):
     x = torch.zeros((0, 2, 64), dtype=BF, device="cuda")
     pos = torch.zeros(0, dtype=torch.int32, device="cuda")

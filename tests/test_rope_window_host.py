@@ -227,6 +227,24 @@ def test_window_refuses_what_the_attention_refuses(sv, kw, status):  # noqa: F81
     assert sv.lib().spec_kv_attend_window(ctypes.byref(_cache(sv)), ctypes.byref(a), 16, 4, None) == status
 
 
+@pytest.mark.parametrize("window,sinks,want", [
+    (16, 4, (16, 4)), (2**31 - 1, 2**31 - 1, (2**31 - 1, 2**31 - 1)), (2**31, 0, (2**31 - 1, 0)), (2**32 + 5, 3, (2**31 - 1, 3)),
+    (7, 2**32 + 1, (7, 2**31 - 1)), (5 - 2**32, 0, (-1, 0)), (5, 1 - 2**32, (5, -1)), (-2**31 - 1, 2**40, (-1, 2**31 - 1)),
+])
+def test_binding_passes_no_window_by_its_low_bits(monkeypatch, window, sinks, want):
+    """A window past 32 bits is the largest one, and one below them stays a refusal."""
+    import types
+
+    import speculative_decoding_verification_38_gb300 as sv
+
+    called = []
+    fake = types.SimpleNamespace(spec_kv_attend_window=lambda *a: called.append(a[2:4]) or 0)
+    monkeypatch.setattr(sv, "_lib", fake)
+    args = types.SimpleNamespace(cache=types.SimpleNamespace(ref=None), ref=None)
+    sv.spec_kv_attend_window(args, window, sinks, stream=0)
+    assert called == [want]
+
+
 def test_binding_refuses_before_the_library():
     import speculative_decoding_verification_38_gb300 as sv
 
