@@ -32,9 +32,9 @@
 // read from TMEM, weights, their stores, the vote on references, the product),
 // with issue slots to spare: trees of 29 (116 rows), 176 us, 0.53, issue
 // active in 47 % of cycles, one place for P as two parts of 128 rows take
-// 64 KB; ragged e4m3 chains of up to 72 rows, 967 us for 2.2 GB, 0.34, about
-// 4,200 cycles a tile, issue active in 55 %, a fifth of the tiles make their
-// weights twice. One e4m3 token of each of the 64: 99 us for 310 MB, 0.46,
+// 64 KB; ragged e4m3 chains of up to 72 rows, 914 us for 2.2 GB, 0.36, about
+// 4,000 cycles a tile, issue slots to spare (active in 55 % when it took 967),
+// a fifth of the tiles make their weights twice. One e4m3 token of each of the 64: 99 us for 310 MB, 0.46,
 // issue active in 40 %: the ends of entries. A single sequence of 4,111:
 // 15 us, of which launch, start (the list, TMEM) and the chain page number -
 // tile - score - weight - product - join are latency. Far from the floor:
@@ -48,9 +48,9 @@
 // run); trees of 29, window 2,000: 169 us for 547 MB, 0.47 (the softmax's chain
 // of steps, 4,000 cycles a tile against HBM's 2,800); two of nine tokens,
 // window 65,536: 102 us for 538 MB, 0.78; ragged e4m3 chains, window 4,096:
-// 309 us for 533 MB, 0.25 (the same chain, and moved references). A run of
+// 302 us for 533 MB, 0.26 (the same chain, and moved references). A run of
 // entries for each team, so that one team's ends hide behind the others' tiles,
-// was built and was slower (74 to 103, 309 to 414): the warps that load and
+// was built and was slower (75 to 103, 329 to 414): the warps that load and
 // issue follow several runs, and teams in different places fetch different
 // code.
 #pragma once
@@ -1262,6 +1262,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
         constexpr float grow = Q8 ? (Win ? 9.75f : 8.f) : 16.f;
+        constexpr float reach_of = Q8 ? (Win ? 861.0779f : 256.f) : 65536.f;  // 2^grow
+        constexpr bool undo = !Q8 || TM == 4;  // how weights are made anew
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t team = gr % TM, sub = gr / TM;
         const uint32_t o_at = tmem + X::O_at + lanes + team * X::NP;
@@ -1542,12 +1544,16 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                     };
                     if (turn) wait(pv_done + ps, (turn - 1) & 1);  // P is free, and O where P is one for each team
                     tc_after();
-                    // ---- weights. When a score passes the reference by too much, they leave the row sums again
-                    // (exactly enough: what rounding leaves behind is within an ulp of that score's weight), the
-                    // reference moves, and they are made anew.
-                    // (e4m3 through a window, whose entries have few tiles: in a team's first eight, where half of them move a
-                    // reference, every tile finds its maxima first; ragged chains 329 to 313 us, in every tile 351)
-                    const bool young = i < first + (Q8 && Win ? 8 : 1) * TM;
+                    // ---- weights. When a score passes the reference by too much, the reference moves and they are made
+                    // anew. bf16, where that is rare: first they leave the row sums again (exactly enough: what rounding
+                    // leaves behind is within an ulp of that score's weight). e4m3: the sums, which have each weight up to
+                    // 2^grow, shrink with the reference and take only what it has above that (ragged chains without a
+                    // window 967 to 920 us, with one 309 to 303; in bf16 the same code spilled more, 74 to 78; one row of 64 sequences 99 to
+                    // 100).
+                    // (e4m3 of more than 32 rows: in a team's first four tiles, where half of them move a reference, each
+                    // finds its maxima first; one, two, four, eight tiles: ragged chains 920, 916, 914, 914 us, through a
+                    // window 308, 306, 302, 303, and in every tile 351; one row 99 us, with four 102)
+                    const bool young = i < first + (Q8 && TM < 4 ? 4 : 1) * TM;
                     bool moved = false, due = young;
 #pragma unroll 1
                     for (float sign = 1.f;;) {
@@ -1586,7 +1592,14 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     z[k] = make_float2(ex2(z[k].x), ex2(z[k].y));
-                                    l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
+                                    if (undo || !moved) {
+                                        l[m][k] = fma2(make_float2(sign, sign), z[k], l[m][k]);
+                                    } else {
+                                        // the sums hold what was within the old reference's reach, times f
+                                        const float2 f = *(const float2*)(red + 4 * MC * 8 + (m < live ? m : m0) * 8 + 2 * k);
+                                        const float2 had = mul2(f, make_float2(reach_of, reach_of));
+                                        l[m][k] = add2(l[m][k], sub2(z[k], make_float2(min_nan(z[k].x, had.x), min_nan(z[k].y, had.y))));
+                                    }
                                 }
                                 if (Q8) {
                                     if (!masked) {
@@ -1621,7 +1634,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                                 }
                             }
                         }
-                        if (sign < 0.f) {
+                        if (undo && sign < 0.f) {
                             bar_sync(bar_gr, 128);
                             due = moved = true;
                             sign = 1.f;
@@ -1629,7 +1642,10 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                         }
                         // (after a move nothing passes the reference, so that a second one is never due)
                         if (young || moved || !bar_or(bar_gr, 128, top > grow || !(big <= (Win ? 61440.f : 16384.f)))) break;
-                        sign = -1.f;
+                        if (undo)
+                            sign = -1.f;
+                        else
+                            due = moved = true;
                     }
                     // (Win: a box's slots that no token sees are cleared too)
                     const bool clear = Win ? !in && pos != INT32_MAX : pos >= L;
