@@ -542,7 +542,9 @@ SPEC_API spec_status_t spec_kv_attend(const spec_kv_cache_t* cache, const spec_k
  * give them to other sequences; what a token does not see has no effect on it.
  * A window of kv_lens[b] or more hides nothing. Up to 16 rows (t_max times the
  * query heads of a key-value head; head_dim up to 128) take a kernel of their
- * own, with batch * kv_heads up to 2^31 - 65536 (more: SPEC_ERR_UNSUPPORTED):
+ * own, with batch * kv_heads up to 2^31 - 65536 (more: SPEC_ERR_UNSUPPORTED),
+ * where min(window, max_blocks * block_size) is at most about 8192 (SPEC_E4M3:
+ * 16384), or that for each piece that a few sequences are cut into:
  * weights are at most one there, SPEC_BF16's in two bf16 parts, SPEC_E4M3's
  * times V's scales in fp16: 11 bits of what is 2^-29 of the largest V scale the
  * token sees or more (the rest to 2^-40 of that), queries exact down to 2^-31

@@ -17,10 +17,10 @@ namespace {
 // not been measured.
 int tile_rows(int64_t rows, bool window) {
     const int64_t tiles = (rows + 127) / 128, each = (rows + tiles - 1) / tiles;
-    // (Through a window, where up to 16 rows take attend_few.cu, 17 to 32 are faster in tiles of 48: two teams with more
-    // tiles each of an entry that has few. 20 rows of 64 sequences, window 1,024: 79 to 71 us; e4m3 98 to 95.)
+    // (Through a window 17 to 32 rows are faster in tiles of 48: two teams with more tiles each of an entry that has few. 20
+    // rows of 64 sequences, window 1,024: 79 to 71 us; e4m3 98 to 95.)
     for (int n : {16, 32, 48, 80})
-        if (each <= n && (!window || n >= 48)) return n;
+        if (each <= n && !(window && n == 32)) return n;
     return 128;
 }
 

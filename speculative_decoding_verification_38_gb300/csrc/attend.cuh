@@ -86,7 +86,7 @@ cudaError_t attend_bf16(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_bf16_wide(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_e4m3(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_e4m3_wide(int n, const AttParams& p, cudaStream_t s);
-// The same with a sliding window (p.a.window > 0; 48, 80 or 128).
+// The same with a sliding window (p.a.window > 0; 16, 48, 80 or 128).
 cudaError_t attend_window_bf16(int n, const AttParams& p, cudaStream_t s);
 cudaError_t attend_window_e4m3(int n, const AttParams& p, cudaStream_t s);
 

@@ -50,6 +50,8 @@ constexpr int kMaxWarps = 8;
 constexpr int kBoxLog = 4;        // log2 of the most positions that the list keeps together
 constexpr int64_t kLeast = 32;    // positions of a warp, at least, where an entry is in pieces
 constexpr int64_t kParts = 2048;  // most pieces where entries are split
+constexpr int64_t kMostRows = 16; // query rows of an entry
+constexpr int64_t kLongest = 16384;  // positions of a piece, times bytes of an element
 constexpr float kNone = -INFINITY;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {  // not there: zeros
@@ -631,29 +633,49 @@ cudaError_t launch_dim(const FewParams& p, int warps, cudaStream_t s) {
     return p.a.c.D <= 64 ? launch<NR, 64, Q8>(p, warps, s) : launch<NR, 128, Q8>(p, warps, s);
 }
 
+struct Plan {
+    int64_t rows, entries, most;  // most: positions that an entry's tokens may see
+    int warps;                    // of a CTA
+    int64_t splits;
+    explicit Plan(const KvAttend& a) : rows((int64_t)a.t_max * a.G), entries((int64_t)a.c.B * a.c.H) {
+        // Warps to an entry: with fewer a CTA starts and ends for more positions, but the CTAs of a call should be on the 152
+        // SMs at once (rings of 1 x 8, 2 x 4 or 4 x 2 warps fit). One e4m3 token through 1,024 positions, us with 8, 4 and 2
+        // warps: of 16 sequences (128 entries) 11.8, 13.9, 16; of 32 22, 17, 22; of 64 46, 36, 31; of 96 66, 52, 57.
+        // Pieces only where an entry's warps leave SMs empty, and none shorter than kLeast positions for each warp where the
+        // window is full (one sequence through 4,096: 32 positions 8.8 us, 64 10.4).
+        most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + 16);
+        warps = entries <= 152 ? 8 : entries <= 304 ? 4 : entries <= 608 ? 2 : 4;
+        splits = std::min(152 * 8 / warps / entries, most / (warps * kLeast));
+        splits = std::max<int64_t>(1, std::min<int64_t>({splits, 32, kParts / entries}));
+    }
+};
+
 }  // namespace
 
-bool attend_few_takes(int32_t head_dim, int64_t rows) { return head_dim <= 128 && rows <= 16; }
+bool attend_few_takes(const KvAttend& a) {
+    if (a.c.D > 128 || (int64_t)a.t_max * a.G > kMostRows) return false;
+    // A piece is one CTA's, however much shorter the others are, and the host does not know the lengths; attend.cuh shares
+    // all tiles out evenly. One token of 20 sequences x 8 heads through 16,384 positions, us here and there, bf16: all that
+    // long 216 and 214, lengths up to it 186 and 120, one of them that long and the rest 256 183 and 30. Of 64 sequences
+    // through 8,192: 309 and 331, 229 and 197, 184 and 43. e4m3, where a piece of as many bytes is twice as long, 64 through
+    // 16,384: 344 and 559, 335 and 320, 245 and 49; through 8,192: 177 and 297, 180 and 196, 127 and 44. So the limit is where
+    // lengths that differ a little are even; a single long one costs at most four times what it would there.
+    const Plan plan(a);
+    return plan.most * a.c.esz <= kLongest * plan.splits;
+}
 
 size_t attend_few_workspace(int64_t rows) {
-    return kHeaderBytes + ((size_t)kParts * rows * (128 * 4 + 16) + 255) / 256 * 256;
+    return rows > kMostRows ? 0 : kHeaderBytes + ((size_t)kParts * rows * (128 * 4 + 16) + 255) / 256 * 256;
 }
 
 cudaError_t launch_attend_few(const KvAttend& a, void* workspace, cudaStream_t s) {
-    const int64_t rows = (int64_t)a.t_max * a.G, entries = (int64_t)a.c.B * a.c.H;
-    // Warps to an entry: with fewer a CTA starts and ends for more positions, but the CTAs of a call should be on the 152 SMs
-    // at once (rings of 1 x 8, 2 x 4 or 4 x 2 warps fit). One e4m3 token through 1,024 positions, us with 8, 4 and 2 warps:
-    // of 16 sequences (128 entries) 11.8, 13.9, 16; of 32 22, 17, 22; of 64 46, 36, 31; of 96 66, 52, 57.
-    // Pieces only where an entry's warps leave SMs empty, and none shorter than kLeast positions for each warp where the
-    // window is full (one sequence through 4,096: 32 positions 8.8 us, 64 10.4).
-    const int64_t most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + 16);
-    const int warps = entries <= 152 ? 8 : entries <= 304 ? 4 : entries <= 608 ? 2 : 4;
-    int64_t splits = std::min(152 * 8 / warps / entries, most / (warps * kLeast));
-    splits = std::max<int64_t>(1, std::min<int64_t>({splits, 32, kParts / entries}));
+    const Plan plan(a);
+    const int64_t rows = plan.rows;
+    const int warps = plan.warps;
     FewParams p;
     p.a = a;
-    p.splits = (int32_t)splits;
-    p.ctas = entries * splits;
+    p.splits = (int32_t)plan.splits;
+    p.ctas = plan.entries * plan.splits;
     p.rows_max = (int32_t)rows;
     p.box_log = 0;
     while (p.box_log < kBoxLog && a.c.bs % (2 << p.box_log) == 0) ++p.box_log;

@@ -141,9 +141,9 @@ cudaError_t launch_rope(const Rope& r, const RopeRows& q, int64_t rows, cudaStre
 bool attend_takes(int32_t head_dim);
 size_t attend_workspace(int64_t rows, bool window);
 cudaError_t launch_attend(const KvAttend& a, void* workspace, cudaStream_t s);
-// Through a window, for rows = t_max * query heads of a key-value head up to 16 (attend_few.cu).
-bool attend_few_takes(int32_t head_dim, int64_t rows);
-size_t attend_few_workspace(int64_t rows);
+// Through a window, for rows up to 16 where no piece of an entry can be long (attend_few.cu).
+bool attend_few_takes(const KvAttend& a);
+size_t attend_few_workspace(int64_t rows);  // 0: more rows than it takes
 cudaError_t launch_attend_few(const KvAttend& a, void* workspace, cudaStream_t s);
 // A CTA for each query row, for the rest.
 cudaError_t launch_kv_attend_plain(const KvAttend& p, cudaStream_t s);

@@ -185,11 +185,11 @@ spec_status_t rope_rows(RopeRows& q, const void* x, int32_t x_dtype, int64_t x_s
     return SPEC_OK;
 }
 
-// Bytes that a call works on, with a window or without.
+// Bytes that a call works on, with a window (of any length: either kernel) or without.
 size_t workspace_of(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, bool window) {
     const int64_t rows = (int64_t)a->t_max * (a->q_heads / c->kv_heads);
     if (!attend_takes(c->head_dim)) return kHeaderBytes;
-    return window && attend_few_takes(c->head_dim, rows) ? attend_few_workspace(rows) : attend_workspace(rows, window);
+    return std::max(attend_workspace(rows, window), window ? attend_few_workspace(rows) : 0);
 }
 
 // window 0: none.
@@ -227,7 +227,7 @@ spec_status_t attend(const spec_kv_cache_t* c, const spec_kv_attend_args_t* a, i
     p.seq_status = a->seq_status;
     p.window = (int32_t)std::min<int64_t>(window, kMaxPositions);  // (so that sums with positions stay in range)
     p.sinks = (int32_t)std::min<int64_t>(sinks, kMaxPositions);
-    if (window && attend_few_takes(c->head_dim, (int64_t)a->t_max * p.G)) {
+    if (window && attend_few_takes(p)) {
         if ((int64_t)c->batch * c->kv_heads > kMaxEntries) return SPEC_ERR_UNSUPPORTED;  // a CTA for each
         return launched(launch_attend_few(p, a->workspace, (cudaStream_t)stream));
     }
