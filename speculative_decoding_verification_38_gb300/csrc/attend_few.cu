@@ -49,7 +49,7 @@ struct FewParams {
 constexpr int kMaxWarps = 8;
 constexpr int kBoxLog = 4;        // log2 of the most positions that the list keeps together
 constexpr int64_t kLeast = 32;    // positions of a warp, at least, where an entry is in pieces
-constexpr int64_t kParts = 2048;  // most pieces where entries are split
+constexpr int64_t kParts = 152;   // most pieces where entries are split: an SM for each
 constexpr int64_t kMostRows = 16; // query rows of an entry
 constexpr int64_t kLongest = 16384;  // positions of a piece, times bytes of an element
 constexpr float kNone = -INFINITY;
@@ -645,8 +645,7 @@ struct Plan {
         // window is full (one sequence through 4,096: 32 positions 8.8 us, 64 10.4).
         most = std::min<int64_t>((int64_t)a.c.max_blocks * a.c.bs, (int64_t)a.window + a.t_max + a.sinks + 16);
         warps = entries <= 152 ? 8 : entries <= 304 ? 4 : entries <= 608 ? 2 : 4;
-        splits = std::min(152 * 8 / warps / entries, most / (warps * kLeast));
-        splits = std::max<int64_t>(1, std::min<int64_t>({splits, 32, kParts / entries}));
+        splits = std::max<int64_t>(1, std::min<int64_t>({kParts / entries, 32, most / (warps * kLeast)}));
     }
 };
 
