@@ -600,8 +600,10 @@ SPEC_API spec_status_t spec_rope(const spec_rope_t* rope, const void* x, int32_t
  * local node indices as spec_tree_verify's); or given (positions, int32
  * [axes, rows]; parent must then be NULL). Without positions every axis has
  * the same one. Statuses are spec_kv_append's, and LAYOUT for a bad parent
- * (nothing is written for the tokens whose way to the root leads over it; a
- * node's depth is found by walking that way). A
+ * (nothing is written for the tokens whose way to the root leads over it) and
+ * for a node more than SPEC_KV_MAX_QUERIES - 1 below the root, which no
+ * attention call takes (nothing is written for such nodes: a longer chain has
+ * no parent array, a deeper tree gives its positions). A
  * sequence with an error of its offsets or length has no rows of q_out
  * written; a token on a page outside the pool has its queries rotated all the
  * same. */

@@ -62,6 +62,8 @@ __device__ __forceinline__ int place_of(int pair, bool adjacent) {
 
 constexpr int kResident = 4;             // CTAs on an SM: 64 registers a thread (3, 4, 5 and 6 of them: prompts 542, 490, 486
                                          // and 606 us; a round 5.1, 5.1, 5.6 and 6.8)
+constexpr int kDeepest = kKvMaxQueries - 1;  // of a tree's nodes: a way to the root is one load after another (without a limit a
+                                             // chain of 65,536 given as a tree took 25 ms, each token its whole way)
 struct Token {
     int64_t at, scale;  // its entry in the cache: bytes, scales
     bool known, cached; // it has a position; its page is there
@@ -230,6 +232,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
                 bad |= v == 0 ? u != -1 : (u < 0 || u >= v);
             }
             if (__any_sync(0xFFFFFFFFu, bad)) st = kKvBadLayout;
+            // (a smaller tree has no node that deep; every parent is before its child here)
+            for (int32_t v0 = 0; s.T > kKvMaxQueries && st == kKvOk && v0 < s.T; v0 += 32) {
+                int32_t v = min(v0 + lane, s.T - 1);
+                for (int i = 0; v > 0 && i < kDeepest; ++i) v = parent[s.lo + v];
+                if (__any_sync(0xFFFFFFFFu, v > 0)) st = kKvBadLayout;
+            }
         }
         if (st == kKvOk) st = check_pages(c, (int32_t)b, s.L - s.T, s.L);
         if (lane == 0) n.seq_status[b] = st;
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
                         if (parent) {  // its depth
                             p = s.L - s.T;
                             int32_t v = t;
-                            while (v > 0) {
+                            for (int i = 0; v > 0 && i < kDeepest; ++i) {
                                 const int32_t u = parent[s.lo + v];
                                 if (u < 0 || u >= v) break;
                                 v = u;
