@@ -635,6 +635,8 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
     // Once a wait has given up, every wait but those for segments returns at once, so that all roles run out in
     // step: the same segments, the same named barriers, whatever the data. A role whose own wait gave up issues no more
     // loads or products and gives no place of a loads' ring back, so that none goes where an earlier one may still be due.
+    // (The ring of e4m3 scales needs it less: a softmax warp gives its places back all the same, and a loading thread's copies
+    // go to words of its own and are waited for before it ends. tests/test_kv_scale_waits.py has a model of it.)
     auto wait_seg = [&](uint64_t* bar, uint32_t parity) -> bool {
         const uint32_t t0 = nanoseconds();
 #pragma unroll 1
