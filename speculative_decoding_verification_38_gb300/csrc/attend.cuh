@@ -1256,15 +1256,19 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
         // reference that starts as the row's maximum in its first tile and moves
         // only when a later score passes it by 2^grow. bf16: 2^16, as what the weights have above one the sums lose of
         // float32's range to values (with 2^60 values of 2^67 overflowed; moves are as rare, and no case took longer).
-        // e4m3: 2^8; a weight goes to f16 times V's scale and the row's unit u = 2^(6 - v), 2^v the smallest power of
-        // two that no scale the row has seen passes: at most 2^14 (f16's largest is 2^16), and f16's least is 2^-30 of
-        // a weight of one with that scale. The unit is a row's own, so that the scale of a new token that the row does
-        // not see leaves no trace in it.
+        // e4m3: a weight goes to f16 times V's scale and the row's unit u = 2^(6 - v), 2^v the smallest power of two that no
+        // scale the row has seen passes; f16's least is 2^-30 of a weight of one with that scale, its largest 65,504. The
+        // reference moves past 2^8, weights in their unit then being at most 2^14; through a window, whose few tiles move it
+        // more often, past 2^9.75, at most 55,109, and units past 61,440 (fewer moves: 344 to 329 us for ragged chains,
+        // with the scales' copies ahead). The unit is a row's own, so that the scale of a new token that the row does not
+        // see leaves no trace in it.
         const int gr = warp >> 2, wq = warp & 3, wt = tid & 127;
         const int bar_gr = 1 + gr;
         constexpr int bar_all = 1 + kGroups;
         constexpr float grow = Q8 ? (Win ? 9.75f : 8.f) : 16.f;
         constexpr float reach_of = Q8 ? (Win ? 861.0779f : 256.f) : 65536.f;  // 2^grow
+        constexpr float widest = Win ? 61440.f : 16384.f;  // Q8: of a weight in its row's unit
+        static_assert(!Q8 || (reach_of * 64.f <= widest && widest < 65504.f), "f16's range");
         constexpr bool undo = !Q8 || TM == 4;  // how weights are made anew
         const uint32_t lanes = (uint32_t)wq << 21;  // this warp's 32 TMEM lanes
         const uint32_t team = gr % TM, sub = gr / TM;
@@ -1643,7 +1647,7 @@ __global__ void __launch_bounds__(Shape<NN, DP, Q8, Win>::threads, 1) attend_ker
                             continue;
                         }
                         // (after a move nothing passes the reference, so that a second one is never due)
-                        if (young || moved || !bar_or(bar_gr, 128, top > grow || !(big <= (Win ? 61440.f : 16384.f)))) break;
+                        if (young || moved || !bar_or(bar_gr, 128, top > grow || !(big <= widest))) break;
                         if (undo)
                             sign = -1.f;
                         else
