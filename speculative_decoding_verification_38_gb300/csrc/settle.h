@@ -10,10 +10,12 @@
 
 #include <stdint.h>
 
+#ifndef SPECV_HD
 #ifdef __CUDACC__
 #define SPECV_HD __host__ __device__ __forceinline__
 #else
 #define SPECV_HD inline
+#endif
 #endif
 
 namespace specv {
