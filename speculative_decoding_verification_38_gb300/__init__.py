@@ -328,6 +328,11 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _i32(n) -> int:
+    """n as the calls take it: the nearest 32-bit number, which they refuse where n is none (ctypes would keep n's low bits)."""
+    return n if -_I32_MAX <= n <= _I32_MAX else max(-_I32_MAX, min(int(n), _I32_MAX))
+
+
 def _dtype_code(t, name="logits") -> int:
     T = _types()
     if t.dtype is T.bfloat16:
@@ -560,7 +565,7 @@ class AttendArgs:
                             seq_status=seq_status)
         a = SpecKvAttendArgs()
         a.struct_size = ctypes.sizeof(SpecKvAttendArgs)
-        a.layer, a.q_heads, a.t_max, a.rows = int(layer), heads, int(t_max), rows
+        a.layer, a.q_heads, a.t_max, a.rows = _i32(int(layer)), heads, _i32(int(t_max)), rows
         a.row_off, a.kv_lens, a.parent = _ptr(row_off), kv_lens.data_ptr(), _ptr(parent)
         a.q = q.data_ptr()
         a.q_token_stride = q.stride(0) if rows > 1 else 0
@@ -579,7 +584,7 @@ class AttendArgs:
         self.struct.workspace_bytes = buf.numel() * buf.element_size()
 
     def set_layer(self, layer: int):
-        self.struct.layer = int(layer)
+        self.struct.layer = _i32(int(layer))
 
 
 class Rope:
@@ -741,8 +746,11 @@ def spec_kv_append(cache: KVCache, k_new, v_new, kv_lens, row_off=None, t_max=No
     _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
     _check_typed(row_off, "row_off", T.int64, c.batch + 1)
     _check_typed(seq_status, "seq_status", T.int32, c.batch)
+    t_max = t_max or 0
+    if not (0 <= layer <= _I32_MAX and 0 <= t_max <= _I32_MAX):
+        layer, t_max = _i32(layer), _i32(t_max)
     return (_lib or lib()).spec_kv_append(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new, "k_new"),
-                                          rows[1], rows[0], _ptr(row_off), t_max or 0, kv_lens.data_ptr(), _ptr(seq_status),
+                                          rows[1], rows[0], _ptr(row_off), t_max, kv_lens.data_ptr(), _ptr(seq_status),
                                           _stream(stream))
 
 
@@ -756,7 +764,7 @@ def spec_kv_gather(cache: KVCache, kv_lens, out_off, k_out, v_out, layer=0, seq_
     _check_typed(kv_lens, "kv_lens", T.int32, c.batch, optional=False)
     _check_typed(out_off, "out_off", T.int64, c.batch + 1, optional=False)
     _check_typed(seq_status, "seq_status", T.int32, c.batch)
-    return (_lib or lib()).spec_kv_gather(cache.ref, layer, kv_lens.data_ptr(), out_off.data_ptr(), rows, k_out.data_ptr(),
+    return (_lib or lib()).spec_kv_gather(cache.ref, _i32(layer), kv_lens.data_ptr(), out_off.data_ptr(), rows, k_out.data_ptr(),
                                           v_out.data_ptr(), _dtype_code(k_out, "k_out"), _ptr(seq_status), _stream(stream))
 
 
@@ -791,7 +799,7 @@ def spec_kv_attend(args: AttendArgs, stream=None) -> int:
 def spec_kv_attend_window(args: AttendArgs, window: int, sinks: int = 0, stream=None) -> int:
     """spec_kv_attend in which a token sees the `window` positions up to its own
     and the cache's first `sinks` (either may be any int: no cache is 2**31 - 1 long)."""
-    if window > _I32_MAX or sinks > _I32_MAX or window < 0 or sinks < 0:  # (ctypes would keep the low 32 bits)
+    if window > _I32_MAX or sinks > _I32_MAX or window < 0 or sinks < 0:  # (none of them by its low 32 bits)
         window, sinks = (max(-1, min(int(n), _I32_MAX)) for n in (window, sinks))
     return (_lib or lib()).spec_kv_attend_window(args.cache.ref, args.ref, window, sinks, _stream(stream))
 
@@ -849,7 +857,10 @@ def spec_kv_append_rope(cache: KVCache, rope: Rope, k_new, v_new, kv_lens, row_o
             raise ValueError("q must have k_new's rows and type, and q_out its shape in bfloat16")
         out_stride = _head_rows(q_out, "q_out")[2]
         qp, outp = q.data_ptr(), q_out.data_ptr()
-    a = SpecKvAppendRopeArgs(_APPEND_ROPE_SIZE, layer, _dtype_code(k_new, "k_new"), t_max or 0, rows, _ptr(row_off),
+    t_max = t_max or 0
+    if not (0 <= layer <= _I32_MAX and 0 <= t_max <= _I32_MAX):
+        layer, t_max = _i32(layer), _i32(t_max)
+    a = SpecKvAppendRopeArgs(_APPEND_ROPE_SIZE, layer, _dtype_code(k_new, "k_new"), t_max, rows, _ptr(row_off),
                              kv_lens.data_ptr(), _ptr(parent), _ptr(positions), k_new.data_ptr(), v_new.data_ptr(), stride, qp,
                              outp, q_stride, out_stride, q_heads, _ptr(seq_status))
     return (_lib or lib()).spec_kv_append_rope(cache.ref, rope.ref, ctypes.byref(a), _stream(stream))
