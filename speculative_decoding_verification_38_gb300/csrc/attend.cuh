@@ -43,7 +43,9 @@
 // an entry's opening and end outweigh its few tiles.
 //
 // Through a sliding window (Win) the tiles are those of a list of what the
-// tokens see (sight.cuh). Nine bf16 tokens of 64 sequences, window 1,024:
+// tokens see (sight.cuh); up to 16 rows come here where windows are long
+// (attend_few.cu; 20 ragged sequences, one bf16 token through 65,536: 604 us,
+// 0.98 of the copy bandwidth). Nine bf16 tokens of 64 sequences, window 1,024:
 // 74 us for 270 MB, 0.54 (entries of nine tiles: their ends are a third of a
 // run); trees of 29, window 2,000: 169 us for 547 MB, 0.47 (the softmax's chain
 // of steps, 4,000 cycles a tile against HBM's 2,800); two of nine tokens,

@@ -3,27 +3,32 @@
 // drafts.
 //
 // A CTA takes one (sequence, key-value head), or one of `splits` equal pieces
-// of what its tokens see; each of its warps goes through every fourth run of 16
-// positions by itself: its own ring in shared memory, filled by asynchronous
+// of what its tokens see; each of its eight, four or two warps goes through
+// every eighth, fourth or second run of 16 positions (32 of e4m3 or of heads up
+// to 64) by itself: its own ring in shared memory, filled by asynchronous
 // copies, its own running maxima, sums and outputs in registers. Nothing is
 // waited for but the warp's own copies, and several CTAs on an SM are at
 // different places, so that one's start and end (lengths, pages, the join)
 // hide behind the others' loads. The products are warp-wide m16n8k16 matrix
 // instructions: scores S = Q K^T with the query rows as the instruction's rows,
 // O^T += V^T P^T with the rows as its 8 columns, as S's accumulators are that
-// operand as they lie.
+// operand as they lie. Windows so long that one CTA's piece would outlast a
+// call that is shared out evenly take attend.cuh (attend_few_takes).
 //
-// Bounds (8 heads of 128, pages of 16). bf16 tokens of 16 sequences through a
-// window of 4,096: 44 us for 268 MB, 0.90 of the copy bandwidth; of 64, 1.0.
-// e4m3 tokens of 64 sequences through 1,024: 31 us for 138 MB, 0.66: issue,
-// some 850 instructions for a warp's run of 32 positions (a third turn codes to
-// f16), at 0.4 a cycle with two warps to a scheduler. One sequence through
-// 4,096: 9.6 us, latency: launch, length, page, run, the warps' join, the
-// pieces'. On the tensor cores' asynchronous path (attend.cuh, rows in tiles of
-// 16) these took 62, 197, 73 and 14.6 us: there an entry's end waits for the
-// last of its tiles, and a window's entry has few. From 17 rows on it is the
-// faster one: rows of 16 to a warp, three warps to a run, 9 tokens x 4 query
-// heads of 64 sequences took 115 us, there 74.
+// Bounds (8 heads of 128, pages of 16; us in a graph). bf16 tokens of 16
+// sequences through a window of 4,096: 44 us for 269 MB, 0.90 of the copy
+// bandwidth; of 64, 159 us, 1.0. e4m3 tokens of 64 sequences through 1,024:
+// 30.5 us for 138 MB, 0.67: latency with few warps to hide it, 1.65 to a
+// scheduler that issues in 40 % of cycles (209 registers a thread and 25.7 KB of
+// ring a warp leave room for no more; a warp turns codes to f16 between its
+// loads and its products). One sequence through 4,096: 8.5 us, latency: launch,
+// length, page, run, the warps' join, the pieces'. One or two entries, in 32
+// pieces at most, leave SMs empty: one key-value head through 65,536 21 us,
+// through 131,072 34 (floors 5 and 10). On the tensor cores' asynchronous path
+// (attend.cuh, rows in tiles of 16) these took 62, 197, 73 and 14.6 us: there an
+// entry's end waits for the last of its tiles, and a window's entry has few. From
+// 17 rows on it is the faster one: rows of 16 to a warp, three warps to a run,
+// 9 tokens x 4 query heads of 64 sequences took 115 us, there 74.
 #include <algorithm>
 #include <atomic>
 
