@@ -747,7 +747,7 @@ def spec_kv_append(cache: KVCache, k_new, v_new, kv_lens, row_off=None, t_max=No
     _check_typed(row_off, "row_off", T.int64, c.batch + 1)
     _check_typed(seq_status, "seq_status", T.int32, c.batch)
     t_max = t_max or 0
-    if not (0 <= layer <= _I32_MAX and 0 <= t_max <= _I32_MAX):
+    if (layer | t_max) >> 31:  # either is none of 0 .. 2**31 - 1
         layer, t_max = _i32(layer), _i32(t_max)
     return (_lib or lib()).spec_kv_append(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new, "k_new"),
                                           rows[1], rows[0], _ptr(row_off), t_max, kv_lens.data_ptr(), _ptr(seq_status),
@@ -858,7 +858,7 @@ def spec_kv_append_rope(cache: KVCache, rope: Rope, k_new, v_new, kv_lens, row_o
         out_stride = _head_rows(q_out, "q_out")[2]
         qp, outp = q.data_ptr(), q_out.data_ptr()
     t_max = t_max or 0
-    if not (0 <= layer <= _I32_MAX and 0 <= t_max <= _I32_MAX):
+    if (layer | t_max) >> 31:  # either is none of 0 .. 2**31 - 1
         layer, t_max = _i32(layer), _i32(t_max)
     a = SpecKvAppendRopeArgs(_APPEND_ROPE_SIZE, layer, _dtype_code(k_new, "k_new"), t_max, rows, _ptr(row_off),
                              kv_lens.data_ptr(), _ptr(parent), _ptr(positions), k_new.data_ptr(), v_new.data_ptr(), stride, qp,
