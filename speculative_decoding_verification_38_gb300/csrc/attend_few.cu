@@ -663,7 +663,7 @@ bool attend_few_takes(const KvAttend& a) {
     // long 216 and 214, lengths up to it 186 and 120, one of them that long and the rest 256 183 and 30. Of 64 sequences
     // through 8,192: 309 and 331, 229 and 197, 184 and 43. e4m3, where a piece of as many bytes is twice as long, 64 through
     // 16,384: 344 and 559, 335 and 320, 245 and 49; through 8,192: 177 and 297, 180 and 196, 127 and 44. So the limit is where
-    // lengths that differ a little are even; a single long one costs at most four times what it would there.
+    // lengths that differ a little are even; a single long one below it costs up to five times (e4m3 six) what it would there.
     const Plan plan(a);
     return plan.most * a.c.esz <= kLongest * plan.splits;
 }
